@@ -11,4 +11,7 @@ from ._binding import (  # noqa: F401
     decode_workspace_bytes, expert_ffn_decode, new_stack_workspace,
     expert_ffn_prefill, lib, lib_path, lookup_workspace_bytes, prefill_workspace_bytes,
     route_topk, router_logits, slot_bytes, stage_layer,
+    Mxfp4, RouteBalance, group_pairs, group_workspace_bytes, mxfp4_dequantize, mxfp4_ffn_decode,
+    mxfp4_ffn_decode_workspace_bytes, mxfp4_gate_up, mxfp4_linear, mxfp4_quantize, route_backward,
+    route_balance, route_balance_workspace_bytes,
 )

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -49,6 +49,14 @@ class MoeStackLayerC(ctypes.Structure):
     ]
 
 
+class Mxfp4C(ctypes.Structure):
+    _fields_ = [
+        ("n_mats", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+    ]
+
+
+_MXP = ctypes.POINTER(Mxfp4C)
 _LP = ctypes.POINTER(MoeLayerC)
 _SLP = ctypes.POINTER(MoeStackLayerC)
 SIGNATURES = {
@@ -86,6 +94,20 @@ SIGNATURES = {
     "moe_expert_ffn_prefill": (_c_int, [_LP, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _c_sz, _vp]),
     "moe_combine": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_group_workspace_bytes": (_c_sz, [_c_int, _c_int]),
+    "moe_group_pairs": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_sz, _vp]),
+    "moe_mxfp4_quantize": (_c_int, [_vp, _c_int, _c_i64, _c_int, _vp, _vp, _vp]),
+    "moe_mxfp4_dequantize": (_c_int, [_vp, _vp, _c_i64, _c_int, _vp, _c_int, _vp]),
+    "moe_mxfp4_linear": (_c_int, [_MXP, _MXP, _vp, _vp, _c_int, _c_i64, _vp, _c_int, _vp]),
+    "moe_mxfp4_gate_up": (_c_int, [_MXP, _MXP, _vp, _vp, _c_int, _c_i64, _vp, _c_int, _vp]),
+    "moe_mxfp4_ffn_decode_workspace_bytes": (_c_sz, [_c_int, _c_int, _c_int]),
+    "moe_mxfp4_ffn_decode": (_c_int, [_MXP, _MXP, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                                      _c_sz, _vp]),
+    "moe_route_balance_workspace_bytes": (_c_sz, [_c_int, _c_int, _c_int]),
+    "moe_route_balance": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, _vp, _c_sz, _vp]),
+    "moe_route_backward": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -673,3 +695,345 @@ def combine(x, rows, pair_pos, w, shared=None, y=None, stream=None):
     _check(lib().moe_combine(_ptr(x), x_dtype, T, d, k, _ptr(rows), _ptr(pair_pos), _ptr(w),
                              _ptr(shared), _ptr(y), _stream(stream)), "moe_combine")
     return y
+
+
+# --- microscaled 4-bit floats and the router's losses ---------------------------
+#
+# These calls run on the device of their tensors (which must be one device)
+# and, for outputs and workspaces that they allocate, on the memory of the
+# stream they are given, so that a buffer handed back there is not used
+# elsewhere before the call is done with it.
+
+
+class _On:
+    """The device of the tensors (all the same one) and the stream of a call,
+    made current for its allocations and launches.  A stream of another device
+    is refused."""
+
+    def __init__(self, what, stream, **tensors):
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{what}: {name} is on {t.device}, the other tensors on {dev}")
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+        if self.stream.device != dev:
+            raise ValueError(f"{what}: the stream belongs to {self.stream.device}, the tensors to {dev}")
+        self.device = dev
+        self._ctx = None if stream is None and dev.index == torch.cuda.current_device() \
+            else torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+def _float_dtype(dtype, name):
+    if dtype == torch.float32:
+        return DTYPE_F32
+    if dtype == torch.bfloat16:
+        return DTYPE_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+
+
+def _ws(need, ws, device):
+    if ws is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+    return _dev(ws, torch.uint8, "ws")
+
+
+@dataclasses.dataclass
+class Mxfp4:
+    """Microscaled 4-bit floats: codes uint8 [..., rows, cols / 2] and scales
+    uint8 [..., rows, cols / 32] of one matrix or, with a leading dimension, of
+    several (the layout of moe_mxfp4)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        """(matrices, rows, cols)"""
+        c = self.codes
+        return (1 if c.dim() == 2 else c.shape[0], c.shape[-2], 2 * c.shape[-1])
+
+    def check(self, name):
+        if self.codes.dim() not in (2, 3):
+            raise ValueError(f"{name}.codes: shape (rows, cols / 2) or (matrices, rows, cols / 2) "
+                             f"expected, got {tuple(self.codes.shape)}")
+        cols = 2 * self.codes.shape[-1]
+        if cols % 32:
+            raise ValueError(f"{name}.codes: cols a multiple of 32 expected, got {cols}")
+        _shape(self.scales, tuple(self.codes.shape[:-1]) + (cols // 32,), f"{name}.scales")
+        return self
+
+    def on_device(self, name):
+        _dev(self.codes, torch.uint8, f"{name}.codes")
+        _dev(self.scales, torch.uint8, f"{name}.scales")
+        return self
+
+    def c_struct(self) -> Mxfp4C:
+        n, rows, cols = self.shape
+        return Mxfp4C(n, rows, cols, 0, self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def group_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().moe_group_workspace_bytes(T, E))
+
+
+def group_pairs(idx, n_experts, offsets=None, pair_pos=None, row_pair=None, ws=None, stream=None):
+    """Group the pairs of idx [T, k] by expert (moe_group_pairs).
+    Returns (offsets [E + 1], pair_pos [T, k], row_pair [T * k])."""
+    _shape(idx, (None, None), "idx")
+    T, k = idx.shape
+    E = int(n_experts)
+    for t, shp, name in ((offsets, (E + 1,), "offsets"), (pair_pos, (T, k), "pair_pos"),
+                         (row_pair, (T * k,), "row_pair")):
+        if t is not None:
+            _dev(_shape(t, shp, name), torch.int32, name)
+    _dev(idx, torch.int32, "idx")
+    with _On("group_pairs", stream, idx=idx, offsets=offsets, pair_pos=pair_pos, row_pair=row_pair,
+             ws=ws) as on:
+        i32 = dict(dtype=torch.int32, device=on.device)
+        offsets = torch.empty((E + 1,), **i32) if offsets is None else offsets
+        pair_pos = torch.empty((T, k), **i32) if pair_pos is None else pair_pos
+        row_pair = torch.empty((T * k,), **i32) if row_pair is None else row_pair
+        ws = _ws(group_workspace_bytes(T, E), ws, on.device)
+        _check(lib().moe_group_pairs(_ptr(idx), T, k, E, _ptr(offsets), _ptr(pair_pos),
+                                     _ptr(row_pair), _ptr(ws), ws.numel(), on.handle),
+               "moe_group_pairs")
+    return offsets, pair_pos, row_pair
+
+
+def mxfp4_quantize(x, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
+    """x [rows, cols] or [matrices, rows, cols] (fp32 or bf16) as microscaled
+    4-bit floats (moe_mxfp4_quantize)."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: 2 or 3 dimensions expected, got {tuple(x.shape)}")
+    cols = x.shape[-1]
+    if cols % 32:
+        raise ValueError(f"x: a last dimension that is a multiple of 32 expected, got {cols}")
+    dtype = _float_dtype(x.dtype, "x")
+    lead = tuple(x.shape[:-1])
+    if out is not None:
+        _shape(out.codes, lead + (cols // 2,), "out.codes")
+        _shape(out.scales, lead + (cols // 32,), "out.scales")
+        out.on_device("out")
+    _dev(x, x.dtype, "x")
+    with _On("mxfp4_quantize", stream, x=x, codes=out and out.codes, scales=out and out.scales) as on:
+        if out is None:
+            out = Mxfp4(torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=on.device),
+                        torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=on.device))
+        rows = x.numel() // cols if cols else 0
+        _check(lib().moe_mxfp4_quantize(_ptr(x), dtype, rows, cols, _ptr(out.codes),
+                                        _ptr(out.scales), on.handle), "moe_mxfp4_quantize")
+    return out
+
+
+def mxfp4_dequantize(q: Mxfp4, dtype=torch.float32, y=None, stream=None):
+    """The values of q in fp32 or bf16, shape [..., rows, cols]
+    (moe_mxfp4_dequantize)."""
+    q.check("q")
+    y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
+    shape = tuple(q.codes.shape[:-1]) + (2 * q.codes.shape[-1],)
+    if y is not None:
+        _dev(_shape(y, shape, "y"), y.dtype, "y")
+    q.on_device("q")
+    with _On("mxfp4_dequantize", stream, codes=q.codes, scales=q.scales, y=y) as on:
+        if y is None:
+            y = torch.empty(shape, dtype=dtype, device=on.device)
+        rows = y.numel() // shape[-1] if shape[-1] else 0
+        _check(lib().moe_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), rows, shape[-1], _ptr(y),
+                                          y_dtype, on.handle), "moe_mxfp4_dequantize")
+    return y
+
+
+def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
+    a.check("a")
+    w.check("w")
+    na, ma, K = a.shape
+    G, N, Kw = w.shape
+    if na != 1:
+        raise ValueError(f"{what}: a holds one matrix, got {na}")
+    if K != Kw:
+        raise ValueError(f"{what}: a has {K} columns, w {Kw}")
+    if offsets is not None:
+        _shape(offsets, (G + 1,), "offsets")
+    elif G != 1:
+        raise ValueError(f"{what}: offsets are needed with {G} matrices")
+    if row_src is not None:
+        _shape(row_src, (None,), "row_src")
+    R = ma if row_src is None else row_src.shape[0]
+    if gated and N % 2:
+        raise ValueError(f"{what}: an even number of rows of w expected, got {N}")
+    n_out = N // 2 if gated else N
+    y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
+    if y is not None:
+        _dev(_shape(y, (R, n_out), "y"), y.dtype, "y")
+    for t, name in ((offsets, "offsets"), (row_src, "row_src")):
+        if t is not None:
+            _dev(t, torch.int32, name)
+    a.on_device("a")
+    w.on_device("w")
+    with _On(what, stream, a=a.codes, a_scales=a.scales, w=w.codes, w_scales=w.scales,
+             offsets=offsets, row_src=row_src, y=y) as on:
+        if y is None:
+            y = torch.empty((R, n_out), dtype=dtype, device=on.device)
+        A, W = a.c_struct(), w.c_struct()
+        fn = lib().moe_mxfp4_gate_up if gated else lib().moe_mxfp4_linear
+        _check(fn(ctypes.byref(A), ctypes.byref(W), _ptr(offsets), _ptr(row_src), int(src_div), R,
+                  _ptr(y), y_dtype, on.handle), f"moe_{what}")
+    return y
+
+
+def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=None,
+                 dtype=torch.float32, stream=None):
+    """y[r] = a[src(r)] . w[g]^T for the rows r of group g (moe_mxfp4_linear).
+
+    a [rows, K]; w [G, N, K] (or [N, K]); offsets int32 [G + 1] bounds of the
+    groups (None: one group); row_src int32 [R] with src(r) = row_src[r] //
+    src_div (None: r).  Returns y [R, N] in dtype; rows of no group are left as
+    they were (undefined in a y allocated here)."""
+    return _mx_product("mxfp4_linear", False, a, w, offsets, row_src, src_div, y, dtype, stream)
+
+
+def mxfp4_gate_up(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, h=None,
+                  dtype=torch.bfloat16, stream=None):
+    """h[r] = silu(gate) * up of the product with w [G, 2 F, K], gate rows even,
+    up rows odd (moe_mxfp4_gate_up).  Returns h [R, F]; arguments as
+    mxfp4_linear."""
+    return _mx_product("mxfp4_gate_up", True, a, w, offsets, row_src, src_div, h, dtype, stream)
+
+
+def mxfp4_ffn_decode_workspace_bytes(T: int, k: int, d_ff: int) -> int:
+    return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, d_ff))
+
+
+def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=None, ws=None,
+                     stream=None):
+    """Decode / verify FFN of T = 1..4 tokens over 4-bit experts
+    (moe_mxfp4_ffn_decode).  gate_up [n, 2 F, d], down [n, d, F]; x fp32 [T, d];
+    slot int32 and w fp32 [T, k].  Returns y fp32 [T, d]."""
+    gate_up.check("gate_up")
+    down.check("down")
+    n, f2, d = gate_up.shape
+    if down.shape != (n, d, f2 // 2) or f2 % 2:
+        raise ValueError(f"down: (matrices, rows, cols) = {(n, d, f2 // 2)} expected, got {down.shape}")
+    _shape(x, (None, d), "x")
+    T = x.shape[0]
+    _shape(slot, (T, None), "slot")
+    k = slot.shape[1]
+    _shape(w, (T, k), "w")
+    if y is not None:
+        _dev(_shape(y, (T, d), "y"), torch.float32, "y")
+    _dev(x, torch.float32, "x")
+    _dev(slot, torch.int32, "slot")
+    _dev(w, torch.float32, "w")
+    gate_up.on_device("gate_up")
+    down.on_device("down")
+    with _On("mxfp4_ffn_decode", stream, x=x, slot=slot, w=w, gate_up=gate_up.codes,
+             gate_up_scales=gate_up.scales, down=down.codes, down_scales=down.scales, y=y,
+             ws=ws) as on:
+        if y is None:
+            y = torch.empty((T, d), dtype=torch.float32, device=on.device)
+        ws = _ws(mxfp4_ffn_decode_workspace_bytes(T, k, f2 // 2), ws, on.device)
+        GU, D = gate_up.c_struct(), down.c_struct()
+        _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), int(shared_slot),
+                                          _ptr(x), T, k, _ptr(slot), _ptr(w), _ptr(y), _ptr(ws),
+                                          ws.numel(), on.handle), "moe_mxfp4_ffn_decode")
+    return y
+
+
+class RouteBalance(NamedTuple):
+    """What route_balance returns, per sequence."""
+    balance: torch.Tensor     # fp32 [S]
+    z: torch.Tensor           # fp32 [S]
+    counts: torch.Tensor      # int32 [S, E]
+    prob_sum: torch.Tensor    # fp32 [S, E]
+    n_tokens: torch.Tensor    # int32 [S]
+
+
+def _balance_args(logits, idx, seq_offsets, mask):
+    """Shapes first, then devices and types.  Returns (T, E, k, S)."""
+    _shape(logits, (None, None), "logits")
+    T, E = logits.shape
+    _shape(idx, (T, None), "idx")
+    if seq_offsets is not None:
+        _shape(seq_offsets, (None,), "seq_offsets")
+        if seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets: at least 2 elements expected")
+    if mask is not None:
+        _shape(mask, (T,), "mask")
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise ValueError(f"mask must be uint8 or bool, got {mask.dtype}")
+    _dev(logits, torch.float32, "logits")
+    _dev(idx, torch.int32, "idx")
+    if seq_offsets is not None:
+        _dev(seq_offsets, torch.int32, "seq_offsets")
+    if mask is not None:
+        _dev(mask, mask.dtype, "mask")
+    return T, E, idx.shape[1], 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+
+
+def route_balance_workspace_bytes(T: int, E: int, n_seq: int) -> int:
+    return int(lib().moe_route_balance_workspace_bytes(T, E, n_seq))
+
+
+def route_balance(logits, idx, seq_offsets=None, mask=None, out: Optional[RouteBalance] = None,
+                  ws=None, stream=None) -> RouteBalance:
+    """The router's balance and z losses, per-expert counts and probability
+    sums, per sequence (moe_route_balance).  logits fp32 [T, E], idx int32
+    [T, k], seq_offsets int32 [S + 1] (None: one sequence of all rows), mask
+    uint8 or bool [T] (0: the row takes no part)."""
+    T, E, k, S = _balance_args(logits, idx, seq_offsets, mask)
+    want = (((S,), torch.float32), ((S,), torch.float32), ((S, E), torch.int32),
+            ((S, E), torch.float32), ((S,), torch.int32))
+    if out is not None:
+        for t, (shp, dt), name in zip(out, want, RouteBalance._fields):
+            _dev(_shape(t, shp, name), dt, name)
+    with _On("route_balance", stream, logits=logits, idx=idx, seq_offsets=seq_offsets, mask=mask,
+             ws=ws, **(out._asdict() if out is not None else {})) as on:
+        if out is None:
+            out = RouteBalance(*(torch.empty(shp, dtype=dt, device=on.device) for shp, dt in want))
+        ws = _ws(route_balance_workspace_bytes(T, E, S), ws, on.device)
+        _check(lib().moe_route_balance(_ptr(logits), _ptr(idx), T, E, k, _ptr(seq_offsets), S,
+                                       _ptr(mask), *(_ptr(t) for t in out), _ptr(ws), ws.numel(),
+                                       on.handle), "moe_route_balance")
+    return out
+
+
+def route_backward(logits, idx, counts=None, n_tokens=None, g_balance=None, g_z=None, w=None,
+                   dw=None, seq_offsets=None, mask=None, dlogits=None, stream=None):
+    """Gradient of the router's logits from those of the two losses (g_balance,
+    g_z fp32 [S]) and of the routing weights (dw fp32 [T, k], with w as
+    route_topk gave it) (moe_route_backward).  counts and n_tokens as
+    route_balance returns them.  Returns dlogits fp32 [T, E]."""
+    T, E, k, S = _balance_args(logits, idx, seq_offsets, mask)
+    checks = ((counts, (S, E), torch.int32, "counts"), (n_tokens, (S,), torch.int32, "n_tokens"),
+              (g_balance, (S,), torch.float32, "g_balance"), (g_z, (S,), torch.float32, "g_z"),
+              (w, (T, k), torch.float32, "w"), (dw, (T, k), torch.float32, "dw"),
+              (dlogits, (T, E), torch.float32, "dlogits"))
+    for t, shp, dt, name in checks:
+        if t is not None:
+            _dev(_shape(t, shp, name), dt, name)
+    with _On("route_backward", stream, logits=logits, idx=idx, counts=counts, n_tokens=n_tokens,
+             g_balance=g_balance, g_z=g_z, w=w, dw=dw, seq_offsets=seq_offsets, mask=mask,
+             dlogits=dlogits) as on:
+        if dlogits is None:
+            dlogits = torch.empty((T, E), dtype=torch.float32, device=on.device)
+        _check(lib().moe_route_backward(_ptr(logits), _ptr(idx), T, E, k, _ptr(seq_offsets), S,
+                                        _ptr(mask), _ptr(counts), _ptr(n_tokens), _ptr(g_balance),
+                                        _ptr(g_z), _ptr(w), _ptr(dw), _ptr(dlogits), on.handle),
+               "moe_route_backward")
+    return dlogits

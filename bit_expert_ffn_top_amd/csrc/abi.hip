@@ -105,6 +105,56 @@ int check_decode_layer(const moe_layer* L, const float* x, int T, const float* l
     return MOE_EALIGN;
   return MOE_OK;
 }
+
+bool valid_dtype(int t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
+
+constexpr int64_t kMaxMxRows = (int64_t{1} << 24) - 1;
+
+bool valid_mx_cols(int cols) { return cols >= 32 && cols <= MOE_MAX_MX_COLS && cols % 32 == 0; }
+
+int check_mxfp4(const moe_mxfp4* M) {
+  if (!M) return MOE_EINVAL;
+  if (M->n_mats < 1 || M->n_mats > MOE_MAX_EXPERTS) return MOE_EINVAL;
+  if (M->rows < 1 || M->rows > kMaxMxRows || !valid_mx_cols(M->cols)) return MOE_EINVAL;
+  if (M->reserved != 0) return MOE_EINVAL;
+  if (!M->codes || !M->scales) return MOE_EINVAL;
+  if (!aligned16(M->codes) || !aligned16(M->scales)) return MOE_EALIGN;
+  return MOE_OK;
+}
+
+// moe_mxfp4_linear and moe_mxfp4_gate_up (gated).
+int mx_product(const moe_mxfp4* A, const moe_mxfp4* W, const int32_t* offsets,
+               const int32_t* row_src, int src_div, int64_t R, void* y, int y_dtype, bool gated,
+               hipStream_t stream) {
+  int st = check_mxfp4(A);
+  if (st != MOE_OK) return st;
+  st = check_mxfp4(W);
+  if (st != MOE_OK) return st;
+  if (A->n_mats != 1 || A->cols != W->cols || !valid_dtype(y_dtype)) return MOE_EINVAL;
+  if (W->rows > 65536 || W->rows % (gated ? 64 : 16) != 0) return MOE_EINVAL;
+  if (R < 0 || R > kMaxMxRows || src_div < 1) return MOE_EINVAL;
+  if (!offsets && W->n_mats != 1) return MOE_EINVAL;
+  if (!row_src && R > A->rows) return MOE_EINVAL;
+  if (R == 0) return MOE_OK;
+  if (!y || y == A->codes || y == A->scales || y == W->codes || y == W->scales) return MOE_EINVAL;
+  if ((offsets && !aligned16(offsets)) || (row_src && !aligned16(row_src)) || !aligned16(y))
+    return MOE_EALIGN;
+  return hip_status(
+      bitffn::launch_mx_linear(*A, *W, offsets, row_src, src_div, R, y, y_dtype, gated, stream));
+}
+
+// The arguments that moe_route_balance and moe_route_backward share.
+int check_balance(const float* logits, const int32_t* idx, int T, int E, int k,
+                  const int32_t* seq_offsets, int n_seq, const uint8_t* mask) {
+  if (E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK) return MOE_EINVAL;
+  if (T < 0 || T >= (1 << 24) || n_seq < 1 || n_seq > 65536) return MOE_EINVAL;
+  if (!seq_offsets && n_seq != 1) return MOE_EINVAL;
+  if (T > 0 && (!logits || !idx)) return MOE_EINVAL;
+  if ((logits && !aligned16(logits)) || (idx && !aligned16(idx)) ||
+      (seq_offsets && !aligned16(seq_offsets)) || (mask && !aligned16(mask)))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
 }  // namespace
 
 extern "C" {
@@ -470,6 +520,131 @@ int moe_combine(const void* x, int x_dtype, int T, int d, int k, const float* ro
     return MOE_EALIGN;
   return hip_status(
       bitffn::launch_combine(x, x_dtype, T, d, k, rows, pair_pos, w, shared, y, stream));
+}
+
+size_t moe_group_workspace_bytes(int T, int E) {
+  if (T < 1 || T > 65536 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+  return bitffn::group_workspace_bytes(T, E);
+}
+
+int moe_group_pairs(const int32_t* idx, int T, int k, int E, int32_t* offsets, int32_t* pair_pos,
+                    int32_t* row_pair, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (T < 1 || T > 65536 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK)
+    return MOE_EINVAL;
+  if (!idx || !offsets || !row_pair || !ws) return MOE_EINVAL;
+  if (!aligned16(idx) || !aligned16(offsets) || (pair_pos && !aligned16(pair_pos)) ||
+      !aligned16(row_pair) || !aligned256(ws))
+    return MOE_EALIGN;
+  if (ws_bytes < bitffn::group_workspace_bytes(T, E)) return MOE_ENOSPC;
+  // the ids themselves as slots: a pair is selected where 0 <= id < E
+  const bitffn::GroupWorkspace gws = bitffn::group_workspace(ws, T, E);
+  return hip_status(bitffn::launch_group_pairs(idx, idx, nullptr, T, k, E, true, E, gws, offsets,
+                                               row_pair, pair_pos, nullptr, nullptr, nullptr, 0,
+                                               nullptr, nullptr, stream));
+}
+
+int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols, uint8_t* codes,
+                       uint8_t* scales, hipStream_t stream) {
+  if (!valid_dtype(x_dtype) || rows < 0 || rows > kMaxMxRows || !valid_mx_cols(cols))
+    return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_EALIGN;
+  return hip_status(bitffn::launch_mx_quantize(x, x_dtype, rows, cols, codes, scales, stream));
+}
+
+int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                         void* y, int y_dtype, hipStream_t stream) {
+  if (!valid_dtype(y_dtype) || rows < 0 || rows > kMaxMxRows || !valid_mx_cols(cols))
+    return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !y) return MOE_EINVAL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MOE_EALIGN;
+  return hip_status(bitffn::launch_mx_dequantize(codes, scales, rows, cols, y, y_dtype, stream));
+}
+
+int moe_mxfp4_linear(const moe_mxfp4* A, const moe_mxfp4* W, const int32_t* offsets,
+                     const int32_t* row_src, int src_div, int64_t R, void* y, int y_dtype,
+                     hipStream_t stream) {
+  return mx_product(A, W, offsets, row_src, src_div, R, y, y_dtype, false, stream);
+}
+
+int moe_mxfp4_gate_up(const moe_mxfp4* A, const moe_mxfp4* W, const int32_t* offsets,
+                      const int32_t* row_src, int src_div, int64_t R, void* h, int h_dtype,
+                      hipStream_t stream) {
+  return mx_product(A, W, offsets, row_src, src_div, R, h, h_dtype, true, stream);
+}
+
+size_t moe_mxfp4_ffn_decode_workspace_bytes(int T, int k, int d_ff) {
+  if (T < 1 || T > MOE_MAX_DECODE_T || k < 0 || k > MOE_MAX_TOPK || T * k > MOE_MAX_DECODE_PAIRS)
+    return 0;
+  if (d_ff < 32 || d_ff > 4096 || d_ff % 32 != 0) return 0;
+  return bitffn::mx_decode_workspace_bytes(T, k, d_ff);
+}
+
+int moe_mxfp4_ffn_decode(const moe_mxfp4* GU, const moe_mxfp4* D, int shared_slot, const float* x,
+                         int T, int k, const int32_t* slot, const float* w, float* y, void* ws,
+                         size_t ws_bytes, hipStream_t stream) {
+  int st = check_mxfp4(GU);
+  if (st != MOE_OK) return st;
+  st = check_mxfp4(D);
+  if (st != MOE_OK) return st;
+  if (GU->n_mats != D->n_mats || GU->cols != D->rows || GU->rows != 2 * D->cols) return MOE_EINVAL;
+  if (GU->cols > 4096 || D->cols > 4096) return MOE_EINVAL;
+  if (shared_slot < -1 || shared_slot >= GU->n_mats) return MOE_EINVAL;
+  if (T < 1 || T > MOE_MAX_DECODE_T || k < 0 || k > MOE_MAX_TOPK || T * k > MOE_MAX_DECODE_PAIRS)
+    return MOE_EINVAL;
+  if (!x || !y || !ws || (k > 0 && (!slot || !w))) return MOE_EINVAL;
+  if (static_cast<const void*>(x) == static_cast<const void*>(y)) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(y) || (slot && !aligned16(slot)) || (w && !aligned16(w)))
+    return MOE_EALIGN;
+  if (!aligned256(ws)) return MOE_EALIGN;
+  if (ws_bytes < bitffn::mx_decode_workspace_bytes(T, k, D->cols)) return MOE_ENOSPC;
+  return hip_status(bitffn::launch_mx_decode(*GU, *D, shared_slot, x, T, k, slot, w, y, ws, stream));
+}
+
+size_t moe_route_balance_workspace_bytes(int T, int E, int n_seq) {
+  if (T < 0 || T >= (1 << 24) || E < 1 || E > MOE_MAX_EXPERTS || n_seq < 1 || n_seq > 65536)
+    return 0;
+  return bitffn::route_balance_workspace_bytes(T, E, n_seq);
+}
+
+int moe_route_balance(const float* logits, const int32_t* idx, int T, int E, int k,
+                      const int32_t* seq_offsets, int n_seq, const uint8_t* mask, float* balance,
+                      float* z, int32_t* counts, float* prob_sum, int32_t* n_tokens, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
+  const int st = check_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask);
+  if (st != MOE_OK) return st;
+  if (!balance || !z || !counts || !prob_sum || !n_tokens || !ws) return MOE_EINVAL;
+  if (!aligned16(balance) || !aligned16(z) || !aligned16(counts) || !aligned16(prob_sum) ||
+      !aligned16(n_tokens) || !aligned256(ws))
+    return MOE_EALIGN;
+  if (ws_bytes < bitffn::route_balance_workspace_bytes(T, E, n_seq)) return MOE_ENOSPC;
+  return hip_status(bitffn::launch_route_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask,
+                                                 balance, z, counts, prob_sum, n_tokens, ws,
+                                                 stream));
+}
+
+int moe_route_backward(const float* logits, const int32_t* idx, int T, int E, int k,
+                       const int32_t* seq_offsets, int n_seq, const uint8_t* mask,
+                       const int32_t* counts, const int32_t* n_tokens, const float* g_balance,
+                       const float* g_z, const float* w, const float* dw, float* dlogits,
+                       hipStream_t stream) {
+  const int st = check_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask);
+  if (st != MOE_OK) return st;
+  if ((w != nullptr) != (dw != nullptr)) return MOE_EINVAL;
+  if ((g_balance && !counts) || ((g_balance || g_z) && !n_tokens)) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!dlogits) return MOE_EINVAL;
+  const void* ins[] = {logits, idx, seq_offsets, mask, counts, n_tokens, g_balance, g_z, w, dw};
+  for (const void* q : ins) {
+    if (q == static_cast<const void*>(dlogits)) return MOE_EINVAL;
+    if (q && !aligned16(q)) return MOE_EALIGN;
+  }
+  if (!aligned16(dlogits)) return MOE_EALIGN;
+  return hip_status(bitffn::launch_route_backward(logits, idx, T, E, k, seq_offsets, n_seq, mask,
+                                                  counts, n_tokens, g_balance, g_z, w, dw, dlogits,
+                                                  stream));
 }
 
 }  // extern "C"

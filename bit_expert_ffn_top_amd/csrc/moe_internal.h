@@ -127,4 +127,31 @@ hipError_t launch_combine(const void* x, int x_dtype, int T, int d, int k, const
                           const int32_t* pair_pos, const float* w, const float* shared,
                           float* y, hipStream_t s);
 
+// Microscaled 4-bit floats (mxfp4_quantize.hip, mxfp4_linear.hip,
+// mxfp4_decode.hip).
+hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t rows, int cols, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                int cols, void* y, int y_dtype, hipStream_t s);
+// gated: the gate/up product with silu(gate) * up formed before it is stored.
+hipError_t launch_mx_linear(const moe_mxfp4& A, const moe_mxfp4& W, const int32_t* offsets,
+                            const int32_t* row_src, int src_div, int64_t R, void* y, int y_dtype,
+                            bool gated, hipStream_t s);
+size_t mx_decode_workspace_bytes(int T, int k, int f);
+hipError_t launch_mx_decode(const moe_mxfp4& GU, const moe_mxfp4& D, int shared_slot,
+                            const float* x, int T, int k, const int32_t* slot, const float* w,
+                            float* y, void* ws, hipStream_t s);
+
+// The router's losses, counts and gradients (route_balance.hip).
+size_t route_balance_workspace_bytes(int T, int E, int S);
+hipError_t launch_route_balance(const float* logits, const int32_t* idx, int T, int E, int k,
+                                const int32_t* seq, int S, const uint8_t* mask, float* balance,
+                                float* z, int32_t* counts, float* prob_sum, int32_t* n_tokens,
+                                void* ws, hipStream_t s);
+hipError_t launch_route_backward(const float* logits, const int32_t* idx, int T, int E, int k,
+                                 const int32_t* seq, int S, const uint8_t* mask,
+                                 const int32_t* counts, const int32_t* n_tokens,
+                                 const float* g_balance, const float* g_z, const float* w,
+                                 const float* dw, float* dlogits, hipStream_t s);
+
 }  // namespace bitffn

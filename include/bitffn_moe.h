@@ -512,6 +512,155 @@ int moe_combine(const void* x, int x_dtype, int T, int d, int k,
                 const float* rows, const int32_t* pair_pos, const float* w,
                 const float* shared, float* y, hipStream_t stream);
 
+/* Grouping of (token, k-slot) pairs by expert, the order in which grouped
+ * products take their rows: groups ascending by expert id, inside a group by
+ * t then i.  idx int32 [T][k]; a pair whose id lies outside [0, E) is in no
+ * group.  Ids are distinct within a token, as moe_route_topk returns them
+ * (not checked; of equal ids in one token the order is not defined).
+ *   offsets   int32 [E+1]   bounds of the groups (offsets[E] = pairs grouped)
+ *   pair_pos  int32 [T*k]   row of every pair, -1 for one in no group (may be
+ *                           NULL); moe_combine reads it
+ *   row_pair  int32 [T*k]   t*k+i of every row; entries past offsets[E] are
+ *                           left as they were
+ * Limits: 1 <= T <= 65536, 1 <= k <= MOE_MAX_TOPK, 1 <= E <= MOE_MAX_EXPERTS.
+ * ws: at least moe_group_workspace_bytes(T, E) bytes, 256-byte aligned. */
+size_t moe_group_workspace_bytes(int T, int E);
+int moe_group_pairs(const int32_t* idx, int T, int k, int E, int32_t* offsets,
+                    int32_t* pair_pos, int32_t* row_pair, void* ws,
+                    size_t ws_bytes, hipStream_t stream);
+
+/* Microscaled 4-bit floats (the Open Compute Project's "MX" format MXFP4):
+ * 32 consecutive values of a row share a scale 2^(s-127), s one byte; each
+ * value is a sign and one of the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes
+ * 0..7, plus 8 for the negative ones) times that scale.  s = 255 makes the
+ * block NaN.  n_mats matrices of rows x cols follow each other, row-major:
+ *   codes   uint8 [n_mats][rows][cols/2], value 2i of a row in the low four
+ *           bits of its byte i, value 2i+1 in the high four
+ *   scales  uint8 [n_mats][rows][cols/32]
+ * cols is a multiple of 32 in 32..MOE_MAX_MX_COLS, both pointers are 16-byte
+ * aligned device memory.  A host struct, read during the call only. */
+#define MOE_MAX_MX_COLS 16384
+typedef struct moe_mxfp4 {
+  int32_t n_mats;     /* 1..MOE_MAX_EXPERTS             */
+  int32_t rows;       /* 1..2^24 - 1                    */
+  int32_t cols;
+  int32_t reserved;   /* must be 0                      */
+  const void* codes;
+  const void* scales;
+} moe_mxfp4;
+
+/* Quantize x [rows][cols] (fp32 or bf16 bits, x_dtype) into codes and scales
+ * of the layout above (n_mats * rows of a weight set, or the tokens' rows).
+ * With a the largest magnitude of a block, E = max(floor(log2 a) - 2, -127)
+ * (a = 0: -127), s = E + 127; a value becomes the nearest magnitude to
+ * |x| 2^-E, a tie the one with the even code, anything past 6 becomes 6, and
+ * the sign is kept (also of a zero).  A block that holds a NaN or an infinity
+ * gets s = 255 and codes 0.  1 <= rows < 2^24 (0 is a no-op). */
+int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols,
+                       uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* The values back, y [rows][cols] in fp32 or bf16 (y_dtype).  Exact in both
+ * types, apart from scales above 2^125 whose largest values are infinite
+ * (moe_mxfp4_quantize makes none). */
+int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
+                         int64_t rows, int cols, void* y, int y_dtype,
+                         hipStream_t stream);
+
+/* Products of 4-bit rows and 4-bit expert matrices on the matrix cores' own
+ * 4-bit format, sums in fp32, the result rounded once to y_dtype:
+ *   y[r][n] = sum_j A[src(r)][j] * W_g[n][j],   offsets[g] <= r < offsets[g+1]
+ * A: n_mats = 1, its rows the tokens; W: one matrix per group (n_mats = G,
+ * rows a multiple of 16), same cols.  offsets int32 [G+1] ascending (values
+ * are clamped to [0, R]); NULL needs G = 1 and makes one group of all R rows.
+ * src(r) = row_src ? row_src[r] / src_div : r; row_src int32 [R] is for
+ * instance moe_group_pairs' row_pair with src_div = k, so that a token's row is
+ * stored once.  A row whose src lies outside A gives zeros.  Without row_src,
+ * R may not exceed A's rows.  y [R][W rows] fp32 or bf16; rows in no group are
+ * left as they were.  0 <= R < 2^24, src_div >= 1.  y may not alias A or W. */
+int moe_mxfp4_linear(const moe_mxfp4* A, const moe_mxfp4* W,
+                     const int32_t* offsets, const int32_t* row_src,
+                     int src_div, int64_t R, void* y, int y_dtype,
+                     hipStream_t stream);
+
+/* The gate/up product of an expert FFN: W rows = 2 * F, row 2j the gate and
+ * row 2j+1 the up row of index j (as in a packed slot), and
+ *   h[r][j] = silu(g) * u,  g, u the products of rows 2j and 2j+1,
+ * formed in fp32 before one rounding to h_dtype.  h [R][F]; F a multiple of 32.
+ * Everything else as moe_mxfp4_linear. */
+int moe_mxfp4_gate_up(const moe_mxfp4* A, const moe_mxfp4* W,
+                      const int32_t* offsets, const int32_t* row_src,
+                      int src_div, int64_t R, void* h, int h_dtype,
+                      hipStream_t stream);
+
+/* Decode / verify FFN over 4-bit experts, T = 1..4 tokens; the activations
+ * stay in fp32:
+ *   y[t] = x[t] + sum_{i: 0 <= slot[t*k+i] < G.n_mats} w[t*k+i] * FFN_{slot}(x[t])
+ *               + FFN_{shared_slot}(x[t])              (if shared_slot >= 0)
+ * FFN_m(x) = D_m (silu(gate_m x) * (up_m x)); GU holds per expert the
+ * interleaved gate and up rows [2F][d], D the down rows [d][F]; GU and D have the
+ * same n_mats.  x, y fp32 [T][d] (y may not alias x), slot int32 [T][k], w fp32
+ * [T][k].  Sums have a fixed order; a token has the same bits whatever the other
+ * tokens of the step are.
+ * Limits: T * k <= MOE_MAX_DECODE_PAIRS, 0 <= k <= MOE_MAX_TOPK, d and F
+ * multiples of 32 in 32..4096.
+ * ws: at least moe_mxfp4_ffn_decode_workspace_bytes(T, k, F) bytes, 256-byte
+ * aligned. */
+size_t moe_mxfp4_ffn_decode_workspace_bytes(int T, int k, int d_ff);
+int moe_mxfp4_ffn_decode(const moe_mxfp4* GU, const moe_mxfp4* D, int shared_slot,
+                         const float* x, int T, int k, const int32_t* slot,
+                         const float* w, float* y, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/* The router's auxiliary losses and per-expert counts, for whoever trains or
+ * tunes the router.  logits fp32 [T][E], idx int32 [T][k] (the chosen experts,
+ * moe_route_topk's idx; ids outside [0, E) are not counted).  The rows come as
+ * n_seq packed sequences: sequence s holds rows seq_offsets[s] ..
+ * seq_offsets[s+1]-1 (int32 [n_seq+1], ascending, values clamped to [0, T]);
+ * NULL needs n_seq = 1 and takes all rows.  mask uint8 [T] (may be NULL): a row
+ * with 0 takes no part, nor does a row of no sequence; what such a row holds
+ * is not used.  With p_t the softmax over all E logits of row t,
+ * lse_t = log sum exp, and n the rows of s that take part:
+ *   n_tokens int32 [n_seq]        n
+ *   counts   int32 [n_seq][E]     times expert e was chosen
+ *   prob_sum fp32 [n_seq][E]      sum_t p_t[e]
+ *   balance  fp32 [n_seq]         E / (k n^2) * sum_e counts[e] * prob_sum[e]
+ *   z        fp32 [n_seq]         1/n * sum_t lse_t^2
+ * (0 for n = 0; 1 = perfectly even use).  NaN counts as -inf and the difference
+ * of two equal logits, infinities included, as 0, as in moe_route_topk; a row
+ * with an infinite lse adds nothing to z.  Sums have a fixed order.
+ * Limits: 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= MOE_MAX_TOPK, 0 <= T < 2^24,
+ * 1 <= n_seq <= 65536.
+ * ws: at least moe_route_balance_workspace_bytes(T, E, n_seq) bytes, 256-byte
+ * aligned (0 for sizes out of range). */
+size_t moe_route_balance_workspace_bytes(int T, int E, int n_seq);
+int moe_route_balance(const float* logits, const int32_t* idx, int T, int E, int k,
+                      const int32_t* seq_offsets, int n_seq, const uint8_t* mask,
+                      float* balance, float* z, int32_t* counts, float* prob_sum,
+                      int32_t* n_tokens, void* ws, size_t ws_bytes,
+                      hipStream_t stream);
+
+/* Gradient of the router's logits:
+ *   dlogits[t][j] = g_balance[s] E / (k n^2) p_t[j] (counts[s][j] - sum_e counts[s][e] p_t[e])
+ *                 + g_z[s] (2/n) lse_t p_t[j]
+ *                 + sum_{i: idx[t*k+i] = j} w_i (dw_i - sum_i' w_i' dw_i')
+ * the first line the balance loss's (counts carry no gradient), the second the
+ * z loss's, the third that of the routing weights w = moe_route_topk's w under
+ * their incoming gradient dw fp32 [T][k] (the softmax over the chosen).
+ * g_balance, g_z fp32 [n_seq]: gradients of the two losses, each may be NULL
+ * (0); w and dw may both be NULL.  counts int32 [n_seq][E] and n_tokens int32
+ * [n_seq] as moe_route_balance wrote them, or summed over processes; both may
+ * be NULL where neither loss has a gradient.  A row that takes no part (mask,
+ * sequences: as above) gets zeros, whatever it holds; where n_tokens is not
+ * above 0 the two losses have no gradient.  A row with an infinite lse has no
+ * z gradient.  idx entries outside [0, E) get no gradient (their w and dw count
+ * in the inner sum); equal entries of a row add up in k-slot order.
+ * dlogits fp32 [T][E], every row written; may not alias an input. */
+int moe_route_backward(const float* logits, const int32_t* idx, int T, int E, int k,
+                       const int32_t* seq_offsets, int n_seq, const uint8_t* mask,
+                       const int32_t* counts, const int32_t* n_tokens,
+                       const float* g_balance, const float* g_z, const float* w,
+                       const float* dw, float* dlogits, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
