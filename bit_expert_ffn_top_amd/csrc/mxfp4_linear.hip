@@ -22,6 +22,7 @@ namespace {
 
 typedef int mi4 __attribute__((ext_vector_type(4)));
 typedef int mi8 __attribute__((ext_vector_type(8)));
+typedef uint32_t mu2 __attribute__((ext_vector_type(2)));
 typedef float mf4 __attribute__((ext_vector_type(4)));
 
 constexpr int ML_THREADS = 256;   // four wavefronts
@@ -117,24 +118,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Output columns n .. n + 3 of row r.  Plain: four values.  GATED: columns
-// (gate, up, gate, up), two values at n / 2.
+// Four consecutive output columns of a row, stored at p.  GATED: the columns
+// are (gate, up, gate, up) and two values are stored.
 template <bool GATED, bool BF16>
-__device__ __forceinline__ void store_out(const LinearArgs& a, int64_t r, int n, mf4 v) {
+__device__ __forceinline__ void store_out(uint8_t* p, mf4 v) {
   if constexpr (GATED) {
-    const int64_t at = r * (a.N / 2) + n / 2;
     const float h0 = silu(v[0]) * v[1], h1 = silu(v[2]) * v[3];
     if constexpr (BF16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = pack_bf16(h0, h1);
+      *reinterpret_cast<uint32_t*>(p) = pack_bf16(h0, h1);
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(a.y) + at) = make_float2(h0, h1);
+      *reinterpret_cast<float2*>(p) = make_float2(h0, h1);
+  } else if constexpr (BF16) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   } else {
-    const int64_t at = r * a.N + n;
-    if constexpr (BF16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-          make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -205,9 +202,284 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int local = 16 * m + r;
-    if (local < t.rows)
-      store_out<GATED, BF16>(a, t.r0 + local, n0 + 4 * q, ok[m] ? acc[m] : mf4{0, 0, 0, 0});
+    if (local < t.rows) {
+      const int col = n0 + 4 * q;
+      const int64_t at = (t.r0 + local) * (GATED ? a.N / 2 : a.N) + (GATED ? col / 2 : col);
+      store_out<GATED, BF16>(static_cast<uint8_t*>(a.y) + at * (BF16 ? 2 : 4),
+                             ok[m] ? acc[m] : mf4{0, 0, 0, 0});
+    }
   }
+}
+
+// Many rows per group.  A workgroup takes MG_ROWS weight rows and up to 16 CAP
+// tokens of one group; each of its four wavefronts owns 32 of the weight rows
+// (two MFMA tiles) for all the tokens, so every weight is read from memory
+// straight into the registers of the one wavefront that uses it, a step ahead.
+// The tokens' codes are shared: a step's 256 columns (128 bytes of each row)
+// go to LDS by the loads that write it directly, double-buffered, 16-byte piece
+// p of row r at position p ^ swz(r), which spreads the 16 rows that a read of
+// one piece touches over all banks.  Their scales, 8 bytes of a row per step,
+// pass through registers.  Token tiles past a short group's rows are skipped.
+constexpr int MG_ROWS = 128;
+constexpr int MG_STEP = 256;             // columns per step
+
+typedef __amdgpu_buffer_rsrc_t MgRsrc;
+typedef __attribute__((address_space(3))) uint8_t LdsByte;
+
+__host__ __device__ constexpr int mg_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+__device__ __forceinline__ MgRsrc mg_rsrc(const uint8_t* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                           static_cast<int>(static_cast<uint32_t>(bytes)), 0x00020000);
+}
+
+struct MgWeights {   // a wavefront's weights of one step: [tile][half of the lane's 64 columns]
+  mi4 c[2][2];
+  uint32_t s[2];     // both halves' scale bytes
+};
+
+// Buffers (a read past one gives zeros) and this lane's byte offsets in them.
+struct MgLane {
+  MgRsrc ac, as, wc, ws;
+  uint32_t av[8];        // A codes: the row pieces this lane moves to LDS
+  uint32_t asv;          // A scales: the row this thread carries
+  uint32_t wv, wsv;      // weights and scales: this lane's row of the first tile
+  int wtile, wstile;     // from the first tile to the second
+  int nb, q;
+};
+
+// EVEN: rows are a whole number of steps, so every block exists and the scale
+// bytes of a step are aligned.
+template <bool EVEN>
+__device__ __forceinline__ void mg_load_w(MgWeights& w, const MgLane& l, int c) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int so = c * 128 + t * l.wtile;
+    w.c[t][0] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, l.wv, so, 0));
+    w.c[t][1] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, l.wv + 16, so, 0));
+    const int ss = c * 8 + t * l.wstile;
+    if constexpr (EVEN) {
+      w.s[t] = __builtin_amdgcn_raw_buffer_load_b16(l.ws, l.wsv, ss, 0);
+    } else {   // a block past the row: zeros with scale 1
+      const int b = 8 * c + 2 * l.q;
+      const uint32_t s0 = __builtin_amdgcn_raw_buffer_load_b8(l.ws, l.wsv, ss, 0);
+      const uint32_t s1 = __builtin_amdgcn_raw_buffer_load_b8(l.ws, l.wsv + 1, ss, 0);
+      if (b >= l.nb) w.c[t][0] = mi4{0, 0, 0, 0};
+      if (b + 1 >= l.nb) w.c[t][1] = mi4{0, 0, 0, 0};
+      w.s[t] = (b < l.nb ? s0 : kOne) | ((b + 1 < l.nb ? s1 : kOne) << 8);
+    }
+  }
+}
+
+template <bool EVEN>
+__device__ __forceinline__ uint2 mg_load_s(const MgLane& l, int c) {
+  if constexpr (EVEN) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(l.as, l.asv, 8 * c, 0);
+    return make_uint2(v[0], v[1]);
+  }
+  uint32_t v[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t s = __builtin_amdgcn_raw_buffer_load_b8(l.as, l.asv + i, 8 * c, 0);
+    v[i >> 2] |= (8 * c + i < l.nb ? s : kOne) << (8 * (i & 3));
+  }
+  return make_uint2(v[0], v[1]);
+}
+
+// The codes of 16 nt rows of step c: 8 rows per instruction, the four
+// wavefronts in turn.
+template <int CAP>
+__device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wave, int nt, int c) {
+#pragma unroll
+  for (int j = 0; j < CAP / 2; ++j)
+    if (2 * j < nt)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + wave) * 1024), 16, l.av[j],
+          c * 128, 0, 0);
+}
+
+// at: this lane's byte offsets of its two pieces of a tile's row, and of its
+// scale bytes
+struct MgRead {
+  int k0, k1, s;
+};
+
+// The operands of two token tiles.
+struct MgTokens {
+  mi4 x[2][2];
+  int s[2];
+};
+
+__device__ __forceinline__ MgTokens mg_read(const LdsByte* buf, const LdsByte* sbuf, const MgRead& at, int g) {
+  MgTokens x;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = 2 * g + u;
+    x.x[u][0] = *(__attribute__((address_space(3))) const mi4*)(buf + at.k0 + 2048 * i);
+    x.x[u][1] = *(__attribute__((address_space(3))) const mi4*)(buf + at.k1 + 2048 * i);
+    x.s[u] = *(__attribute__((address_space(3))) const uint16_t*)(sbuf + at.s + 128 * i);
+  }
+  return x;
+}
+
+template <int HALF>
+__device__ __forceinline__ mf4 mg_mfma(mi4 w, mi4 x, mf4 c, uint32_t sw, int sx) {
+  const mi8 a = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
+  const mi8 b = {x.x, x.y, x.z, x.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, HALF, static_cast<int>(sw), HALF, sx);
+}
+
+// One step, two token tiles at a time, the next two on their way from LDS
+// (past the last pair a read of whatever LDS holds there, not used).
+template <int CAP>
+__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgWeights& w, const LdsByte* buf,
+                                            const LdsByte* sbuf, const MgRead& at, int nt) {
+  MgTokens x = mg_read(buf, sbuf, at, 0);
+#pragma unroll
+  for (int g = 0; g < CAP / 2; ++g) {
+    if (2 * g < nt) {
+      MgTokens next = x;
+      if (g + 1 < CAP / 2) next = mg_read(buf, sbuf, at, g + 1);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[2 * g + u][t] = mg_mfma<0>(w.c[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t], x.s[u]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[2 * g + u][t] = mg_mfma<1>(w.c[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t], x.s[u]);
+      x = next;
+    }
+  }
+}
+
+// Everything of this wavefront's loads and LDS writes is done, then all meet.
+__device__ __forceinline__ void mg_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int CAP, bool EVEN, bool GATED, bool BF16>
+__device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
+                                        LdsByte* buf0, LdsByte* buf1, LdsByte* sb0, LdsByte* sb1,
+                                        const uint8_t* s_ok) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int nt = (t.rows + 15) / 16;
+  // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
+#pragma unroll
+  for (int j = 0; j < CAP / 2; ++j) {
+    const int row = 8 * (4 * j + wave) + (lane >> 3);
+    bool ok;
+    const int64_t src = source_row(a, t.r0 + min(row, t.rows - 1), ok);
+    l.av[j] = static_cast<uint32_t>(src * (a.K / 2)) + 16 * ((lane & 7) ^ mg_swz(row & 15));
+  }
+  const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
+                     r * 8 + 2 * q};
+  const int steps = (a.K + MG_STEP - 1) / MG_STEP;
+  mf4 acc[CAP][2] = {};
+  MgWeights w0, w1;
+  uint2 sc;
+  const auto put = [&](LdsByte* sb) {
+    *(__attribute__((address_space(3))) mu2*)(sb + 8 * tid) = mu2{sc.x, sc.y};
+  };
+  mg_load_a<CAP>(l, buf0, wave, nt, 0);
+  mg_load_w<EVEN>(w0, l, 0);
+  sc = mg_load_s<EVEN>(l, 0);
+  put(sb0);
+  mg_barrier();
+  // step c is multiplied while step c + 1 (the last one again at the end) is
+  // on its way to the other buffers
+  int c = 0;
+  for (; c + 2 <= steps; c += 2) {
+    mg_load_a<CAP>(l, buf1, wave, nt, c + 1);
+    mg_load_w<EVEN>(w1, l, c + 1);
+    sc = mg_load_s<EVEN>(l, c + 1);
+    mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
+    put(sb1);
+    mg_barrier();
+    const int next = min(c + 2, steps - 1);
+    mg_load_a<CAP>(l, buf0, wave, nt, next);
+    mg_load_w<EVEN>(w0, l, next);
+    sc = mg_load_s<EVEN>(l, next);
+    mg_multiply<CAP>(acc, w1, buf1, sb1, at, nt);
+    put(sb0);
+    mg_barrier();
+  }
+  if (c < steps) mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
+  // 32-bit offsets from the tile's first row; a row without a source is zeros
+  const int n = n0 + 32 * wave + 4 * q;
+  const int width = GATED ? a.N / 2 : a.N;
+  constexpr int kSize = BF16 ? 2 : 4;
+  uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + t.r0 * width * kSize;
+#pragma unroll
+  for (int i = 0; i < CAP; ++i) {
+    const int local = 16 * i + r;
+    if (local < t.rows) {
+      const bool has = s_ok[local] != 0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int col = n + 16 * w;
+        if (col < a.N)
+          store_out<GATED, BF16>(y + static_cast<uint32_t>(local * width + (GATED ? col / 2 : col)) * kSize,
+                                 has ? acc[i][w] : mf4{0, 0, 0, 0});
+      }
+    }
+  }
+}
+
+template <int CAP, bool EVEN, bool GATED, bool BF16>
+__global__ __launch_bounds__(ML_THREADS, CAP == 4 ? 3 : 2) void mx_linear_groups_kernel(
+    LinearArgs a) {
+  __shared__ __align__(16) uint8_t buf0[CAP * 2048];
+  __shared__ __align__(16) uint8_t buf1[CAP * 2048];
+  __shared__ __align__(16) uint8_t sb0[ML_THREADS * 8];   // every thread carries a row's scales
+  __shared__ __align__(16) uint8_t sb1[ML_THREADS * 8];
+  __shared__ uint8_t s_ok[CAP * 16];   // whether each row has a source
+  // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
+  // with all their column slices, so a tile's token rows meet in one L2
+  const int n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
+  const int i = static_cast<int>(blockIdx.x) >> 3;
+  const RowTile t = find_row_tile(a, 8 * (i / n_wg) + (static_cast<int>(blockIdx.x) & 7), 16 * CAP);
+  if (t.rows <= 0) return;
+  const int n0 = i % n_wg * MG_ROWS;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nb = a.K / 32, crow = a.K / 2;
+  MgLane l;
+  l.nb = nb;
+  l.q = lane >> 4;
+  l.ac = mg_rsrc(a.ac, a.a_rows * crow);
+  l.as = mg_rsrc(a.as, a.a_rows * nb);
+  const int64_t wrow = static_cast<int64_t>(t.g) * a.N;
+  l.wc = mg_rsrc(a.wc + wrow * crow, static_cast<int64_t>(a.N) * crow);
+  l.ws = mg_rsrc(a.ws + wrow * nb, static_cast<int64_t>(a.N) * nb);
+  const int row = n0 + 32 * wave + (lane & 15);
+  l.wv = static_cast<uint32_t>(row * crow + 32 * l.q);
+  l.wsv = static_cast<uint32_t>(row * nb + 2 * l.q);
+  l.wtile = 16 * crow;
+  l.wstile = 16 * nb;
+  bool ok;
+  const int64_t src = source_row(a, t.r0 + min(tid, t.rows - 1), ok);
+  l.asv = static_cast<uint32_t>(src * nb);
+  if (tid < 16 * CAP) s_ok[tid] = ok;
+  mg_tile<CAP, EVEN, GATED, BF16>(a, t, l, n0, (LdsByte*)buf0, (LdsByte*)buf1, (LdsByte*)sb0,
+                                  (LdsByte*)sb1, s_ok);
+}
+
+template <int CAP, bool GATED, bool BF16>
+void launch_groups(const LinearArgs& a, hipStream_t s) {
+  const int64_t m = 16 * CAP;
+  const int64_t tiles = a.offsets ? a.R / m + min(static_cast<int64_t>(a.G), a.R) : (a.R + m - 1) / m;
+  const int64_t n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
+  const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8 * n_wg);
+  if (a.K % MG_STEP == 0)
+    mx_linear_groups_kernel<CAP, true, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+  else
+    mx_linear_groups_kernel<CAP, false, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
 }
 
 template <bool GATED, bool BF16>
@@ -217,6 +489,19 @@ void launch_rows(const LinearArgs& a, hipStream_t s) {
   const int64_t tiles = a.offsets ? (a.R / (16 * MT)) + min(static_cast<int64_t>(a.G), a.R) : full;
   const unsigned grid = static_cast<unsigned>(tiles * ((a.N + 15) / 16));
   mx_linear_rows_kernel<MT, SPLIT, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+}
+
+template <bool GATED, bool BF16>
+void launch_product(const LinearArgs& a, hipStream_t s) {
+  const int64_t avg = a.R / a.G;
+  if (avg < 16 || a.a_rows * (a.K / 2) >= (int64_t{1} << 32))   // the other kernel has 32-bit offsets into A
+    launch_rows<GATED, BF16>(a, s);
+  else if (avg > 64)
+    launch_groups<16, GATED, BF16>(a, s);
+  else if (avg > 32)
+    launch_groups<8, GATED, BF16>(a, s);
+  else
+    launch_groups<4, GATED, BF16>(a, s);
 }
 
 }  // namespace
@@ -240,9 +525,9 @@ hipError_t launch_mx_linear(const moe_mxfp4& A, const moe_mxfp4& W, const int32_
   a.src_div = src_div;
   const bool bf16 = y_dtype == MOE_DTYPE_BF16;
   if (gated)
-    bf16 ? launch_rows<true, true>(a, s) : launch_rows<true, false>(a, s);
+    bf16 ? launch_product<true, true>(a, s) : launch_product<true, false>(a, s);
   else
-    bf16 ? launch_rows<false, true>(a, s) : launch_rows<false, false>(a, s);
+    bf16 ? launch_product<false, true>(a, s) : launch_product<false, false>(a, s);
   return hipGetLastError();
 }
 
