@@ -214,14 +214,16 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 // Many rows per group.  A workgroup takes MG_ROWS weight rows and up to 16 CAP
 // tokens of one group; each of its four wavefronts owns 32 of the weight rows
 // (two MFMA tiles) for all the tokens, so every weight is read from memory
-// straight into the registers of the one wavefront that uses it, a step ahead.
-// The tokens' codes are shared: a step's 256 columns (128 bytes of each row)
-// go to LDS by the loads that write it directly, double-buffered, 16-byte piece
-// p of row r at position p ^ swz(r), which spreads the 16 rows that a read of
-// one piece touches over all banks.  Their scales, 8 bytes of a row per step,
-// pass through registers.  Token tiles past a short group's rows are skipped.
+// straight into the registers of the one wavefront that uses it, three steps
+// ahead.  The tokens' codes are shared: a step's 256 columns (128 bytes of each
+// row) go to LDS by the loads that write it directly, two steps ahead, 16-byte
+// piece p of row r at position p ^ swz(r), which spreads the 16 rows that a read
+// of one piece touches over all banks.  Their scales, 8 bytes of a row per
+// step, pass through registers.  Token tiles past a short group's rows are
+// skipped.
 constexpr int MG_ROWS = 128;
 constexpr int MG_STEP = 256;             // columns per step
+constexpr uint32_t MG_OUT = 0x80000000u; // an offset outside every buffer: reads zeros, no traffic
 
 typedef __amdgpu_buffer_rsrc_t MgRsrc;
 typedef __attribute__((address_space(3))) uint8_t LdsByte;
@@ -233,9 +235,16 @@ __device__ __forceinline__ MgRsrc mg_rsrc(const uint8_t* base, int64_t bytes) {
                                            static_cast<int>(static_cast<uint32_t>(bytes)), 0x00020000);
 }
 
-struct MgWeights {   // a wavefront's weights of one step: [tile][half of the lane's 64 columns]
+// A wavefront's weights of one step: [tile][half of the lane's 64 columns].
+// EVEN (rows are a whole number of steps): both halves' scale bytes in s[t][0].
+struct MgWeights {
   mi4 c[2][2];
-  uint32_t s[2];     // both halves' scale bytes
+  uint16_t s[2][2];
+};
+
+// Eight scale bytes of a token's row, EVEN: in v[0] and v[1].
+struct MgScales {
+  uint32_t v[8];
 };
 
 // Buffers (a read past one gives zeros) and this lane's byte offsets in them.
@@ -245,57 +254,86 @@ struct MgLane {
   uint32_t asv;          // A scales: the row this thread carries
   uint32_t wv, wsv;      // weights and scales: this lane's row of the first tile
   int wtile, wstile;     // from the first tile to the second
-  int nb, q;
+  int nb, q, steps;
 };
 
-// EVEN: rows are a whole number of steps, so every block exists and the scale
-// bytes of a step are aligned.
+// Memory instructions of a step's loads.
+template <bool EVEN>
+constexpr int mg_w_loads() { return EVEN ? 6 : 8; }
+template <bool EVEN>
+constexpr int mg_s_loads() { return EVEN ? 1 : 8; }
+
 template <bool EVEN>
 __device__ __forceinline__ void mg_load_w(MgWeights& w, const MgLane& l, int c) {
+  const uint32_t wv = c < l.steps ? l.wv : MG_OUT, wsv = c < l.steps ? l.wsv : MG_OUT;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int so = c * 128 + t * l.wtile;
-    w.c[t][0] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, l.wv, so, 0));
-    w.c[t][1] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, l.wv + 16, so, 0));
-    const int ss = c * 8 + t * l.wstile;
+    const int so = c * 128 + t * l.wtile, ss = c * 8 + t * l.wstile;
+    w.c[t][0] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, wv, so, 0));
+    w.c[t][1] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, wv + 16, so, 0));
     if constexpr (EVEN) {
-      w.s[t] = __builtin_amdgcn_raw_buffer_load_b16(l.ws, l.wsv, ss, 0);
-    } else {   // a block past the row: zeros with scale 1
-      const int b = 8 * c + 2 * l.q;
-      const uint32_t s0 = __builtin_amdgcn_raw_buffer_load_b8(l.ws, l.wsv, ss, 0);
-      const uint32_t s1 = __builtin_amdgcn_raw_buffer_load_b8(l.ws, l.wsv + 1, ss, 0);
-      if (b >= l.nb) w.c[t][0] = mi4{0, 0, 0, 0};
-      if (b + 1 >= l.nb) w.c[t][1] = mi4{0, 0, 0, 0};
-      w.s[t] = (b < l.nb ? s0 : kOne) | ((b + 1 < l.nb ? s1 : kOne) << 8);
+      w.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(l.ws, wsv, ss, 0);
+    } else {
+      w.s[t][0] = __builtin_amdgcn_raw_buffer_load_b8(l.ws, wsv, ss, 0);
+      w.s[t][1] = __builtin_amdgcn_raw_buffer_load_b8(l.ws, wsv + 1, ss, 0);
+    }
+  }
+}
+
+// The weights of step c as the MFMAs take them: a block past the row is zeros
+// with scale 1 (what was loaded there belongs to the next row).
+template <bool EVEN>
+__device__ __forceinline__ void mg_ready(MgWeights& w, const MgLane& l, int c) {
+  if constexpr (!EVEN) {
+    const bool in0 = 8 * c + 2 * l.q < l.nb, in1 = 8 * c + 2 * l.q + 1 < l.nb;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w.c[t][0][i] = in0 ? w.c[t][0][i] : 0;
+        w.c[t][1][i] = in1 ? w.c[t][1][i] : 0;
+      }
+      w.s[t][0] = static_cast<uint16_t>((in0 ? w.s[t][0] : kOne) | ((in1 ? w.s[t][1] : kOne) << 8));
     }
   }
 }
 
 template <bool EVEN>
-__device__ __forceinline__ uint2 mg_load_s(const MgLane& l, int c) {
+__device__ __forceinline__ void mg_load_s(MgScales& s, const MgLane& l, int c) {
+  const uint32_t v = c < l.steps ? l.asv : MG_OUT;
   if constexpr (EVEN) {
-    const auto v = __builtin_amdgcn_raw_buffer_load_b64(l.as, l.asv, 8 * c, 0);
-    return make_uint2(v[0], v[1]);
-  }
-  uint32_t v[2] = {0, 0};
+    const auto q = __builtin_amdgcn_raw_buffer_load_b64(l.as, v, 8 * c, 0);
+    s.v[0] = q[0];
+    s.v[1] = q[1];
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t s = __builtin_amdgcn_raw_buffer_load_b8(l.as, l.asv + i, 8 * c, 0);
-    v[i >> 2] |= (8 * c + i < l.nb ? s : kOne) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b8(l.as, v + i, 8 * c, 0);
   }
-  return make_uint2(v[0], v[1]);
 }
 
-// The codes of 16 nt rows of step c: 8 rows per instruction, the four
-// wavefronts in turn.
+template <bool EVEN>
+__device__ __forceinline__ void mg_put_s(const MgScales& s, const MgLane& l, LdsByte* sb, int c) {
+  mu2 v;
+  if constexpr (EVEN) {
+    v = mu2{s.v[0], s.v[1]};
+  } else {
+    v = mu2{0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2] |= (8 * c + i < l.nb ? s.v[i] : kOne) << (8 * (i & 3));
+  }
+  *(__attribute__((address_space(3))) mu2*)(sb + 8 * threadIdx.x) = v;
+}
+
+// The codes of step c: 8 rows per instruction, the four wavefronts in turn
+// (always CAP / 2 instructions, so that waits can count them; rows past the
+// tile have offsets outside the buffer).
 template <int CAP>
-__device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wave, int nt, int c) {
+__device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wave, int c) {
 #pragma unroll
   for (int j = 0; j < CAP / 2; ++j)
-    if (2 * j < nt)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + wave) * 1024), 16, l.av[j],
-          c * 128, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + wave) * 1024), 16,
+        c < l.steps ? l.av[j] : MG_OUT, c * 128, 0, 0);
 }
 
 // at: this lane's byte offsets of its two pieces of a tile's row, and of its
@@ -344,73 +382,103 @@ __device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgWeights&
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<0>(w.c[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t], x.s[u]);
+          acc[2 * g + u][t] = mg_mfma<0>(w.c[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t][0], x.s[u]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<1>(w.c[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t], x.s[u]);
+          acc[2 * g + u][t] = mg_mfma<1>(w.c[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t][0], x.s[u]);
       x = next;
     }
   }
 }
 
-// Everything of this wavefront's loads and LDS writes is done, then all meet.
+// At most N of this wavefront's loads are still on their way (they arrive in
+// order) and its LDS writes are done; then all wavefronts meet.
+template <int N>
 __device__ __forceinline__ void mg_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));   // vmcnt(N) lgkmcnt(0)
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Step c, whose tokens are in buf and sb and whose weights are in w.  Into the
+// buffers that step c - 1 has left go the tokens of step c + 2, into w the
+// weights of step c + 3; the scales of step c + 1 move on to LDS.
+template <int CAP, bool EVEN>
+__device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgLane& l, const MgRead& at, int nt,
+                                        int c, MgWeights& w, const LdsByte* buf, const LdsByte* sb,
+                                        LdsByte* buf2, MgScales& s2, const MgScales& s1, LdsByte* sb1) {
+  mg_load_a<CAP>(l, buf2, threadIdx.x >> 6, c + 2);
+  mg_load_s<EVEN>(s2, l, c + 2);
+  mg_ready<EVEN>(w, l, c);
+  mg_multiply<CAP>(acc, w, buf, sb, at, nt);
+  mg_load_w<EVEN>(w, l, c + 3);
+  mg_put_s<EVEN>(s1, l, sb1, c + 1);
+  // newer than the tokens of step c + 1: the weights of steps c + 2 and c + 3,
+  // the tokens and scales of step c + 2
+  mg_barrier<2 * mg_w_loads<EVEN>() + CAP / 2 + mg_s_loads<EVEN>()>();
 }
 
 template <int CAP, bool EVEN, bool GATED, bool BF16>
 __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
-                                        LdsByte* buf0, LdsByte* buf1, LdsByte* sb0, LdsByte* sb1,
-                                        const uint8_t* s_ok) {
+                                        LdsByte* buf0, LdsByte* buf1, LdsByte* buf2, LdsByte* sb0,
+                                        LdsByte* sb1, LdsByte* sb2, uint8_t* s_ok) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int nt = (t.rows + 15) / 16;
+  // opaque, so that no step's first products count as unconditional: the
+  // compiler would move them past the barriers, to where their sums are used
+  int nt = (t.rows + 15) / 16;
+  asm volatile("" : "+s"(nt));
+  MgWeights w0, w1, w2;
+  MgScales s0, s1, s2;
+  mg_load_w<EVEN>(w0, l, 0);
+  mg_load_w<EVEN>(w1, l, 1);
+  mg_load_w<EVEN>(w2, l, 2);
+  bool ok;
+  const int64_t src = source_row(a, t.r0 + min(tid, t.rows - 1), ok);
+  l.asv = tid < t.rows ? static_cast<uint32_t>(src * l.nb) : MG_OUT;
+  if (tid < 16 * CAP) s_ok[tid] = ok;
   // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
 #pragma unroll
   for (int j = 0; j < CAP / 2; ++j) {
     const int row = 8 * (4 * j + wave) + (lane >> 3);
-    bool ok;
-    const int64_t src = source_row(a, t.r0 + min(row, t.rows - 1), ok);
-    l.av[j] = static_cast<uint32_t>(src * (a.K / 2)) + 16 * ((lane & 7) ^ mg_swz(row & 15));
+    const int64_t from = source_row(a, t.r0 + min(row, t.rows - 1), ok);
+    l.av[j] = row < t.rows ? static_cast<uint32_t>(from * (a.K / 2)) + 16 * ((lane & 7) ^ mg_swz(row & 15))
+                           : MG_OUT;
   }
   const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
                      r * 8 + 2 * q};
-  const int steps = (a.K + MG_STEP - 1) / MG_STEP;
   mf4 acc[CAP][2] = {};
-  MgWeights w0, w1;
-  uint2 sc;
-  const auto put = [&](LdsByte* sb) {
-    *(__attribute__((address_space(3))) mu2*)(sb + 8 * tid) = mu2{sc.x, sc.y};
-  };
-  mg_load_a<CAP>(l, buf0, wave, nt, 0);
-  mg_load_w<EVEN>(w0, l, 0);
-  sc = mg_load_s<EVEN>(l, 0);
-  put(sb0);
-  mg_barrier();
-  // step c is multiplied while step c + 1 (the last one again at the end) is
-  // on its way to the other buffers
+  mg_load_a<CAP>(l, buf0, wave, 0);
+  mg_load_s<EVEN>(s0, l, 0);
+  mg_load_a<CAP>(l, buf1, wave, 1);
+  mg_load_s<EVEN>(s1, l, 1);
+  mg_put_s<EVEN>(s0, l, sb0, 0);
+  mg_barrier<CAP / 2 + mg_s_loads<EVEN>()>();
   int c = 0;
-  for (; c + 2 <= steps; c += 2) {
-    mg_load_a<CAP>(l, buf1, wave, nt, c + 1);
-    mg_load_w<EVEN>(w1, l, c + 1);
-    sc = mg_load_s<EVEN>(l, c + 1);
-    mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
-    put(sb1);
-    mg_barrier();
-    const int next = min(c + 2, steps - 1);
-    mg_load_a<CAP>(l, buf0, wave, nt, next);
-    mg_load_w<EVEN>(w0, l, next);
-    sc = mg_load_s<EVEN>(l, next);
-    mg_multiply<CAP>(acc, w1, buf1, sb1, at, nt);
-    put(sb0);
-    mg_barrier();
+  for (; c + 3 <= l.steps; c += 3) {
+    mg_step<CAP, EVEN>(acc, l, at, nt, c, w0, buf0, sb0, buf2, s2, s1, sb1);
+    mg_step<CAP, EVEN>(acc, l, at, nt, c + 1, w1, buf1, sb1, buf0, s0, s2, sb2);
+    mg_step<CAP, EVEN>(acc, l, at, nt, c + 2, w2, buf2, sb2, buf1, s1, s0, sb0);
   }
-  if (c < steps) mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
+  // one or two steps left: nothing more to request.  (Their waits may not
+  // count loads: the ones whose values nobody would use are not there.)
+  if (c < l.steps) {
+    mg_put_s<EVEN>(s1, l, sb1, c + 1);
+    mg_barrier<0>();
+    mg_ready<EVEN>(w0, l, c);
+    mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
+    if (c + 1 < l.steps) {
+      mg_ready<EVEN>(w1, l, c + 1);
+      mg_multiply<CAP>(acc, w1, buf1, sb1, at, nt);
+    }
+  } else {
+    mg_barrier<0>();   // a load still on its way to LDS may not outlive the workgroup
+  }
   // 32-bit offsets from the tile's first row; a row without a source is zeros
   const int n = n0 + 32 * wave + 4 * q;
   const int width = GATED ? a.N / 2 : a.N;
@@ -433,12 +501,10 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
 }
 
 template <int CAP, bool EVEN, bool GATED, bool BF16>
-__global__ __launch_bounds__(ML_THREADS, CAP == 4 ? 3 : 2) void mx_linear_groups_kernel(
-    LinearArgs a) {
-  __shared__ __align__(16) uint8_t buf0[CAP * 2048];
-  __shared__ __align__(16) uint8_t buf1[CAP * 2048];
-  __shared__ __align__(16) uint8_t sb0[ML_THREADS * 8];   // every thread carries a row's scales
-  __shared__ __align__(16) uint8_t sb1[ML_THREADS * 8];
+__global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearArgs a) {
+  __shared__ __align__(16) uint8_t buf0[CAP * 2048], buf1[CAP * 2048], buf2[CAP * 2048];
+  // every thread carries a row's scales
+  __shared__ __align__(16) uint8_t sb0[ML_THREADS * 8], sb1[ML_THREADS * 8], sb2[ML_THREADS * 8];
   __shared__ uint8_t s_ok[CAP * 16];   // whether each row has a source
   // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
   // with all their column slices, so a tile's token rows meet in one L2
@@ -447,11 +513,12 @@ __global__ __launch_bounds__(ML_THREADS, CAP == 4 ? 3 : 2) void mx_linear_groups
   const RowTile t = find_row_tile(a, 8 * (i / n_wg) + (static_cast<int>(blockIdx.x) & 7), 16 * CAP);
   if (t.rows <= 0) return;
   const int n0 = i % n_wg * MG_ROWS;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int nb = a.K / 32, crow = a.K / 2;
   MgLane l;
   l.nb = nb;
   l.q = lane >> 4;
+  l.steps = (a.K + MG_STEP - 1) / MG_STEP;
   l.ac = mg_rsrc(a.ac, a.a_rows * crow);
   l.as = mg_rsrc(a.as, a.a_rows * nb);
   const int64_t wrow = static_cast<int64_t>(t.g) * a.N;
@@ -462,12 +529,8 @@ __global__ __launch_bounds__(ML_THREADS, CAP == 4 ? 3 : 2) void mx_linear_groups
   l.wsv = static_cast<uint32_t>(row * nb + 2 * l.q);
   l.wtile = 16 * crow;
   l.wstile = 16 * nb;
-  bool ok;
-  const int64_t src = source_row(a, t.r0 + min(tid, t.rows - 1), ok);
-  l.asv = static_cast<uint32_t>(src * nb);
-  if (tid < 16 * CAP) s_ok[tid] = ok;
-  mg_tile<CAP, EVEN, GATED, BF16>(a, t, l, n0, (LdsByte*)buf0, (LdsByte*)buf1, (LdsByte*)sb0,
-                                  (LdsByte*)sb1, s_ok);
+  mg_tile<CAP, EVEN, GATED, BF16>(a, t, l, n0, (LdsByte*)buf0, (LdsByte*)buf1, (LdsByte*)buf2,
+                                  (LdsByte*)sb0, (LdsByte*)sb1, (LdsByte*)sb2, s_ok);
 }
 
 template <int CAP, bool GATED, bool BF16>
@@ -494,10 +557,8 @@ void launch_rows(const LinearArgs& a, hipStream_t s) {
 template <bool GATED, bool BF16>
 void launch_product(const LinearArgs& a, hipStream_t s) {
   const int64_t avg = a.R / a.G;
-  if (avg < 16 || a.a_rows * (a.K / 2) >= (int64_t{1} << 32))   // the other kernel has 32-bit offsets into A
+  if (avg < 16 || a.a_rows * (a.K / 2) >= int64_t{MG_OUT})   // the other kernel has 32-bit offsets into A
     launch_rows<GATED, BF16>(a, s);
-  else if (avg > 64)
-    launch_groups<16, GATED, BF16>(a, s);
   else if (avg > 32)
     launch_groups<8, GATED, BF16>(a, s);
   else
