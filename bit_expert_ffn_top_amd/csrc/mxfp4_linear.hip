@@ -37,7 +37,10 @@ struct LinearArgs {
   const int32_t* row_src;  // [R] or null
   void* y;
   int64_t R, a_rows;
-  int G, N, K, src_div;
+  int G, N, K;
+  // row_src[r] / src_div = row_src[r] * div_mul >> div_shift, exact below 2^31
+  uint32_t div_mul;
+  int div_shift;
 };
 
 // What a wavefront works on: rows r0 .. r0 + rows - 1 of group g.
@@ -95,14 +98,21 @@ __device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int tile, 
     at += nt[i];
   }
   __syncthreads();
-  return RowTile{s_g, s_rows, s_r0};
+  // the same in every thread: kept in scalar registers
+  return RowTile{__builtin_amdgcn_readfirstlane(s_g), __builtin_amdgcn_readfirstlane(s_rows),
+                 __builtin_amdgcn_readfirstlane(s_r0)};
 }
 
-// A's row for output row r, and whether it exists.
-__device__ __forceinline__ int64_t source_row(const LinearArgs& a, int64_t r, bool& ok) {
-  const int64_t s = a.row_src ? static_cast<int64_t>(a.row_src[r]) / a.src_div : r;
-  ok = s >= 0 && s < a.a_rows && (!a.row_src || a.row_src[r] >= 0);
-  return ok ? s : 0;
+// A's row for output row r; 0 and ok = false if there is none.
+__device__ __forceinline__ int source_row(const LinearArgs& a, int64_t r, bool& ok) {
+  if (!a.row_src) {
+    ok = true;   // R is at most A's rows
+    return static_cast<int>(r);
+  }
+  const int v = a.row_src[r];
+  const uint32_t s = static_cast<uint32_t>(static_cast<uint64_t>(static_cast<uint32_t>(v)) * a.div_mul >> a.div_shift);
+  ok = v >= 0 && s < static_cast<uint32_t>(a.a_rows);
+  return ok ? static_cast<int>(s) : 0;
 }
 
 __device__ __forceinline__ mf4 mfma_fp4(mi4 w, mi4 x, mf4 c, uint32_t sw, uint32_t sx) {
@@ -120,10 +130,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // Four consecutive output columns of a row, stored at p.  GATED: the columns
 // are (gate, up, gate, up) and two values are stored.
+// silu(z) = z / (1 + e^-z).  The product with log2(e) is carried in two parts,
+// so the exponential is good to about 2 units in the last place for every z;
+// the hardware's exponential and reciprocal are each good to 1.  Past +-126
+// the exponential is 0 or infinite either way.
+__device__ __forceinline__ float silu_hw(float z) {
+  const float c = __builtin_amdgcn_fmed3f(z, -126.0f, 126.0f);
+  const float t = -c * 1.44269502f;                                  // log2(e), rounded
+  const float lo = fmaf(-c, 1.44269502f, -t) - c * 1.92596303e-8f;   // what both roundings lost
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182f, 1.0f);
+  return z * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
 template <bool GATED, bool BF16>
 __device__ __forceinline__ void store_out(uint8_t* p, mf4 v) {
   if constexpr (GATED) {
-    const float h0 = silu(v[0]) * v[1], h1 = silu(v[2]) * v[3];
+    const float h0 = silu_hw(v[0]) * v[1], h1 = silu_hw(v[2]) * v[3];
     if constexpr (BF16)
       *reinterpret_cast<uint32_t*>(p) = pack_bf16(h0, h1);
     else
@@ -161,7 +183,7 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int local = 16 * m + r;
-    const int64_t s = source_row(a, t.r0 + min(local, t.rows - 1), ok[m]);
+    const int64_t s = source_row(a, t.r0 + min(local, t.rows - 1), ok[m]);   // widened: offsets may pass 2^32
     xc[m] = a.ac + s * crow;
     xs[m] = a.as + s * nb;
   }
@@ -426,7 +448,7 @@ __device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgLane& l, con
 template <int CAP, bool EVEN, bool GATED, bool BF16>
 __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
                                         LdsByte* buf0, LdsByte* buf1, LdsByte* buf2, LdsByte* sb0,
-                                        LdsByte* sb1, LdsByte* sb2, uint8_t* s_ok) {
+                                        LdsByte* sb1, LdsByte* sb2, int* s_src) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
   // opaque, so that no step's first products count as unconditional: the
@@ -438,16 +460,21 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
   mg_load_w<EVEN>(w0, l, 0);
   mg_load_w<EVEN>(w1, l, 1);
   mg_load_w<EVEN>(w2, l, 2);
-  bool ok;
-  const int64_t src = source_row(a, t.r0 + min(tid, t.rows - 1), ok);
-  l.asv = tid < t.rows ? static_cast<uint32_t>(src * l.nb) : MG_OUT;
-  if (tid < 16 * CAP) s_ok[tid] = ok;
+  // thread tid looks up tile row tid's source; the others take it from LDS
+  int src = -1;
+  if (tid < t.rows) {
+    bool ok;
+    src = source_row(a, t.r0 + tid, ok);
+    if (tid < 16 * CAP) s_src[tid] = ok ? src : ~src;
+  }
+  l.asv = tid < t.rows ? static_cast<uint32_t>(src) * l.nb : MG_OUT;
+  __syncthreads();
   // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
 #pragma unroll
   for (int j = 0; j < CAP / 2; ++j) {
     const int row = 8 * (4 * j + wave) + (lane >> 3);
-    const int64_t from = source_row(a, t.r0 + min(row, t.rows - 1), ok);
-    l.av[j] = row < t.rows ? static_cast<uint32_t>(from * (a.K / 2)) + 16 * ((lane & 7) ^ mg_swz(row & 15))
+    const int v = s_src[row];
+    l.av[j] = row < t.rows ? static_cast<uint32_t>(v < 0 ? ~v : v) * (a.K / 2) + 16 * ((lane & 7) ^ mg_swz(row & 15))
                            : MG_OUT;
   }
   const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
@@ -488,7 +515,7 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
   for (int i = 0; i < CAP; ++i) {
     const int local = 16 * i + r;
     if (local < t.rows) {
-      const bool has = s_ok[local] != 0;
+      const bool has = s_src[local] >= 0;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const int col = n + 16 * w;
@@ -505,7 +532,7 @@ __global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearA
   __shared__ __align__(16) uint8_t buf0[CAP * 2048], buf1[CAP * 2048], buf2[CAP * 2048];
   // every thread carries a row's scales
   __shared__ __align__(16) uint8_t sb0[ML_THREADS * 8], sb1[ML_THREADS * 8], sb2[ML_THREADS * 8];
-  __shared__ uint8_t s_ok[CAP * 16];   // whether each row has a source
+  __shared__ int s_src[CAP * 16];   // each row's source, complemented where it has none
   // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
   // with all their column slices, so a tile's token rows meet in one L2
   const int n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
@@ -530,7 +557,7 @@ __global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearA
   l.wtile = 16 * crow;
   l.wstile = 16 * nb;
   mg_tile<CAP, EVEN, GATED, BF16>(a, t, l, n0, (LdsByte*)buf0, (LdsByte*)buf1, (LdsByte*)buf2,
-                                  (LdsByte*)sb0, (LdsByte*)sb1, (LdsByte*)sb2, s_ok);
+                                  (LdsByte*)sb0, (LdsByte*)sb1, (LdsByte*)sb2, s_src);
 }
 
 template <int CAP, bool GATED, bool BF16>
@@ -583,7 +610,12 @@ hipError_t launch_mx_linear(const moe_mxfp4& A, const moe_mxfp4& W, const int32_
   a.G = W.n_mats;
   a.N = W.rows;
   a.K = W.cols;
-  a.src_div = src_div;
+  // with l = ceil(log2 d): ceil(2^(31+l) / d) < 2^32, and the error of the
+  // rounded-up factor stays below 1 / d for every dividend below 2^31
+  int l = 0;
+  while ((int64_t{1} << l) < src_div) ++l;
+  a.div_shift = 31 + l;
+  a.div_mul = static_cast<uint32_t>(((uint64_t{1} << a.div_shift) + src_div - 1) / src_div);
   const bool bf16 = y_dtype == MOE_DTYPE_BF16;
   if (gated)
     bf16 ? launch_product<true, true>(a, s) : launch_product<true, false>(a, s);
