@@ -143,6 +143,22 @@ __device__ __forceinline__ float silu_hw(float z) {
 }
 
 template <bool GATED, bool BF16>
+__device__ __forceinline__ void put_out(__attribute__((address_space(3))) uint8_t* p, mf4 v) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  if constexpr (GATED) {
+    const float h0 = silu_hw(v[0]) * v[1], h1 = silu_hw(v[2]) * v[3];
+    if constexpr (BF16)
+      *(__attribute__((address_space(3))) uint32_t*)p = pack_bf16(h0, h1);
+    else
+      *(__attribute__((address_space(3))) f2*)p = f2{h0, h1};
+  } else if constexpr (BF16) {
+    *(__attribute__((address_space(3))) mu2*)p = mu2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  } else {
+    *(__attribute__((address_space(3))) mf4*)p = v;
+  }
+}
+
+template <bool GATED, bool BF16>
 __device__ __forceinline__ void store_out(uint8_t* p, mf4 v) {
   if constexpr (GATED) {
     const float h0 = silu_hw(v[0]) * v[1], h1 = silu_hw(v[2]) * v[3];
@@ -235,20 +251,31 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 
 // Many rows per group.  A workgroup takes MG_ROWS weight rows and up to 16 CAP
 // tokens of one group; each of its four wavefronts owns 32 of the weight rows
-// (two MFMA tiles) for all the tokens, so every weight is read from memory
-// straight into the registers of the one wavefront that uses it, three steps
-// ahead.  The tokens' codes are shared: a step's 256 columns (128 bytes of each
-// row) go to LDS by the loads that write it directly, two steps ahead, 16-byte
-// piece p of row r at position p ^ swz(r), which spreads the 16 rows that a read
-// of one piece touches over all banks.  Their scales, 8 bytes of a row per
-// step, pass through registers.  Token tiles past a short group's rows are
-// skipped.
+// (two MFMA tiles) for all the tokens, 256 columns per step.
+//
+// The MFMA wants row l % 16 in lane l, so a load straight into its operands
+// would touch 64 places with 16 bytes each, and the path from the caches, which
+// takes 64 contiguous bytes of four neighbouring lanes at a time, would be the
+// bound (measured: its return path busy 92% of the time).  Everything is
+// therefore loaded as it lies, 8 rows of 128 bytes per instruction, and changes
+// lanes in LDS, 16-byte piece p of row r at position p ^ swz(r), which spreads
+// the 16 rows that a read of one piece touches over all banks:
+//   the tokens' codes, which all wavefronts share, by loads that write LDS
+//     directly, one step ahead (they come from L2);
+//   a wavefront's weights through its registers, two steps ahead (they come
+//     from memory), and a piece of LDS of its own, without a barrier;
+//   scales, four steps at a time, through registers.
+// Token tiles past a short group's rows are skipped.
 constexpr int MG_ROWS = 128;
 constexpr int MG_STEP = 256;             // columns per step
+constexpr int MG_CHUNK = 4;              // steps per load of scales, 32 bytes of a row
 constexpr uint32_t MG_OUT = 0x80000000u; // an offset outside every buffer: reads zeros, no traffic
 
 typedef __amdgpu_buffer_rsrc_t MgRsrc;
 typedef __attribute__((address_space(3))) uint8_t LdsByte;
+typedef __attribute__((address_space(3))) mi4 LdsInt4;
+typedef __attribute__((address_space(3))) mf4 LdsFloat4;
+typedef __attribute__((address_space(3))) uint16_t LdsU16;
 
 __host__ __device__ constexpr int mg_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
@@ -257,98 +284,80 @@ __device__ __forceinline__ MgRsrc mg_rsrc(const uint8_t* base, int64_t bytes) {
                                            static_cast<int>(static_cast<uint32_t>(bytes)), 0x00020000);
 }
 
-// A wavefront's weights of one step: [tile][half of the lane's 64 columns].
-// EVEN (rows are a whole number of steps): both halves' scale bytes in s[t][0].
-struct MgWeights {
-  mi4 c[2][2];
-  uint16_t s[2][2];
-};
-
-// Eight scale bytes of a token's row, EVEN: in v[0] and v[1].
-struct MgScales {
-  uint32_t v[8];
-};
+// Keeps the compiler to the program order of this wavefront's LDS accesses
+// (which is the order in which they take effect).
+__device__ __forceinline__ void mg_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Buffers (a read past one gives zeros) and this lane's byte offsets in them.
 struct MgLane {
   MgRsrc ac, as, wc, ws;
   uint32_t av[8];        // A codes: the row pieces this lane moves to LDS
-  uint32_t asv;          // A scales: the row this thread carries
-  uint32_t wv, wsv;      // weights and scales: this lane's row of the first tile
-  int wtile, wstile;     // from the first tile to the second
-  int nb, q, steps;
+  uint32_t asv;          // A scales: half a chunk of row tid / 2
+  uint32_t wv;           // weights: piece lane % 8 of the wavefront's row lane / 8
+  uint32_t wsv;          // weight scales: half a chunk of the wavefront's row lane / 2
+  int w8;                // 8 rows of weights
+  int nb, steps;
 };
 
-// Memory instructions of a step's loads.
-template <bool EVEN>
-constexpr int mg_w_loads() { return EVEN ? 6 : 8; }
-template <bool EVEN>
-constexpr int mg_s_loads() { return EVEN ? 1 : 8; }
+// 16 scale bytes as loaded.  G: the largest power of two up to 8 that divides
+// the blocks of a row, so that a load of G bytes is aligned and lies wholly
+// inside or outside the buffer.
+template <int G>
+struct MgScales {
+  uint32_t v[G == 1 ? 16 : 4];
+};
 
-template <bool EVEN>
-__device__ __forceinline__ void mg_load_w(MgWeights& w, const MgLane& l, int c) {
-  const uint32_t wv = c < l.steps ? l.wv : MG_OUT, wsv = c < l.steps ? l.wsv : MG_OUT;
+template <int G>
+__device__ __forceinline__ void mg_load_s(MgScales<G>& s, MgRsrc rs, uint32_t at, int chunk) {
+  const int so = chunk * (8 * MG_CHUNK);
+  if constexpr (G == 8) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int so = c * 128 + t * l.wtile, ss = c * 8 + t * l.wstile;
-    w.c[t][0] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, wv, so, 0));
-    w.c[t][1] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, wv + 16, so, 0));
-    if constexpr (EVEN) {
-      w.s[t][0] = __builtin_amdgcn_raw_buffer_load_b16(l.ws, wsv, ss, 0);
-    } else {
-      w.s[t][0] = __builtin_amdgcn_raw_buffer_load_b8(l.ws, wsv, ss, 0);
-      w.s[t][1] = __builtin_amdgcn_raw_buffer_load_b8(l.ws, wsv + 1, ss, 0);
+    for (int i = 0; i < 2; ++i) {
+      const auto q = __builtin_amdgcn_raw_buffer_load_b64(rs, at + 8 * i, so, 0);
+      s.v[2 * i] = q[0];
+      s.v[2 * i + 1] = q[1];
     }
-  }
-}
-
-// The weights of step c as the MFMAs take them: a block past the row is zeros
-// with scale 1 (what was loaded there belongs to the next row).
-template <bool EVEN>
-__device__ __forceinline__ void mg_ready(MgWeights& w, const MgLane& l, int c) {
-  if constexpr (!EVEN) {
-    const bool in0 = 8 * c + 2 * l.q < l.nb, in1 = 8 * c + 2 * l.q + 1 < l.nb;
+  } else if constexpr (G == 4) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w.c[t][0][i] = in0 ? w.c[t][0][i] : 0;
-        w.c[t][1][i] = in1 ? w.c[t][1][i] : 0;
-      }
-      w.s[t][0] = static_cast<uint16_t>((in0 ? w.s[t][0] : kOne) | ((in1 ? w.s[t][1] : kOne) << 8));
-    }
-  }
-}
-
-template <bool EVEN>
-__device__ __forceinline__ void mg_load_s(MgScales& s, const MgLane& l, int c) {
-  const uint32_t v = c < l.steps ? l.asv : MG_OUT;
-  if constexpr (EVEN) {
-    const auto q = __builtin_amdgcn_raw_buffer_load_b64(l.as, v, 8 * c, 0);
-    s.v[0] = q[0];
-    s.v[1] = q[1];
+    for (int i = 0; i < 4; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, at + 4 * i, so, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b8(l.as, v + i, 8 * c, 0);
+    for (int i = 0; i < 16; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, at + i, so, 0);
   }
 }
 
-template <bool EVEN>
-__device__ __forceinline__ void mg_put_s(const MgScales& s, const MgLane& l, LdsByte* sb, int c) {
-  mu2 v;
-  if constexpr (EVEN) {
-    v = mu2{s.v[0], s.v[1]};
-  } else {
-    v = mu2{0, 0};
+// To LDS; b0 is the first block's number, a block past the row gets scale 1
+// (its codes are zeros in the weights).
+template <int G>
+__device__ __forceinline__ void mg_put_s(const MgScales<G>& s, LdsByte* to, int b0, int nb) {
+  mi4 v;
+  if constexpr (G == 1) {
+    v = mi4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i >> 2] |= (8 * c + i < l.nb ? s.v[i] : kOne) << (8 * (i & 3));
+    for (int i = 0; i < 16; ++i)
+      v[i >> 2] |= static_cast<int>((b0 + i < nb ? s.v[i] : kOne) << (8 * (i & 3)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = static_cast<int>(G == 8 || b0 + 4 * i < nb ? s.v[i] : 0x01010101u * kOne);
   }
-  *(__attribute__((address_space(3))) mu2*)(sb + 8 * threadIdx.x) = v;
+  *(LdsInt4*)to = v;
 }
 
-// The codes of step c: 8 rows per instruction, the four wavefronts in turn
-// (always CAP / 2 instructions, so that waits can count them; rows past the
-// tile have offsets outside the buffer).
+// This wavefront's 32 weight rows of step c, 8 rows per instruction.
+__device__ __forceinline__ void mg_load_w(mi4 (&w)[4], const MgLane& l, int c) {
+  const uint32_t v = c < l.steps ? l.wv : MG_OUT;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v, c * 128 + j * l.w8, 0));
+}
+
+// The codes of step c's tokens: 8 rows per instruction, the four wavefronts in
+// turn (rows past the tile have offsets outside the buffer).
 template <int CAP>
 __device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wave, int c) {
 #pragma unroll
@@ -358,58 +367,58 @@ __device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wav
         c < l.steps ? l.av[j] : MG_OUT, c * 128, 0, 0);
 }
 
-// at: this lane's byte offsets of its two pieces of a tile's row, and of its
-// scale bytes
+// This lane's byte offsets of its two pieces of a tile's row, and of the row's
+// scale bytes.
 struct MgRead {
   int k0, k1, s;
 };
 
-// The operands of two token tiles.
-struct MgTokens {
+// The operands of two tiles of 16 rows (weights or tokens).
+struct MgPair {
   mi4 x[2][2];
   int s[2];
 };
 
-__device__ __forceinline__ MgTokens mg_read(const LdsByte* buf, const LdsByte* sbuf, const MgRead& at, int g) {
-  MgTokens x;
+__device__ __forceinline__ MgPair mg_read(const LdsByte* buf, const LdsByte* sbuf, const MgRead& at, int g) {
+  MgPair x;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = 2 * g + u;
-    x.x[u][0] = *(__attribute__((address_space(3))) const mi4*)(buf + at.k0 + 2048 * i);
-    x.x[u][1] = *(__attribute__((address_space(3))) const mi4*)(buf + at.k1 + 2048 * i);
-    x.s[u] = *(__attribute__((address_space(3))) const uint16_t*)(sbuf + at.s + 128 * i);
+    x.x[u][0] = *(const LdsInt4*)(buf + at.k0 + 2048 * i);
+    x.x[u][1] = *(const LdsInt4*)(buf + at.k1 + 2048 * i);
+    x.s[u] = *(const LdsU16*)(sbuf + at.s + 16 * 8 * MG_CHUNK * i);
   }
   return x;
 }
 
 template <int HALF>
-__device__ __forceinline__ mf4 mg_mfma(mi4 w, mi4 x, mf4 c, uint32_t sw, int sx) {
+__device__ __forceinline__ mf4 mg_mfma(mi4 w, mi4 x, mf4 c, int sw, int sx) {
   const mi8 a = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
   const mi8 b = {x.x, x.y, x.z, x.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, HALF, static_cast<int>(sw), HALF, sx);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, HALF, sw, HALF, sx);
 }
 
 // One step, two token tiles at a time, the next two on their way from LDS
 // (past the last pair a read of whatever LDS holds there, not used).
 template <int CAP>
-__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgWeights& w, const LdsByte* buf,
+__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgPair& w, const LdsByte* buf,
                                             const LdsByte* sbuf, const MgRead& at, int nt) {
-  MgTokens x = mg_read(buf, sbuf, at, 0);
+  MgPair x = mg_read(buf, sbuf, at, 0);
 #pragma unroll
   for (int g = 0; g < CAP / 2; ++g) {
     if (2 * g < nt) {
-      MgTokens next = x;
+      MgPair next = x;
       if (g + 1 < CAP / 2) next = mg_read(buf, sbuf, at, g + 1);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<0>(w.c[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t][0], x.s[u]);
+          acc[2 * g + u][t] = mg_mfma<0>(w.x[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t], x.s[u]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<1>(w.c[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t][0], x.s[u]);
+          acc[2 * g + u][t] = mg_mfma<1>(w.x[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t], x.s[u]);
       x = next;
     }
   }
@@ -427,47 +436,84 @@ __device__ __forceinline__ void mg_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Step c, whose tokens are in buf and sb and whose weights are in w.  Into the
-// buffers that step c - 1 has left go the tokens of step c + 2, into w the
-// weights of step c + 3; the scales of step c + 1 move on to LDS.
-template <int CAP, bool EVEN>
-__device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgLane& l, const MgRead& at, int nt,
-                                        int c, MgWeights& w, const LdsByte* buf, const LdsByte* sb,
-                                        LdsByte* buf2, MgScales& s2, const MgScales& s1, LdsByte* sb1) {
-  mg_load_a<CAP>(l, buf2, threadIdx.x >> 6, c + 2);
-  mg_load_s<EVEN>(s2, l, c + 2);
-  mg_ready<EVEN>(w, l, c);
-  mg_multiply<CAP>(acc, w, buf, sb, at, nt);
-  mg_load_w<EVEN>(w, l, c + 3);
-  mg_put_s<EVEN>(s1, l, sb1, c + 1);
-  // newer than the tokens of step c + 1: the weights of steps c + 2 and c + 3,
-  // the tokens and scales of step c + 2
-  mg_barrier<2 * mg_w_loads<EVEN>() + CAP / 2 + mg_s_loads<EVEN>()>();
+template <int CAP>
+struct MgShared {
+  LdsByte* a[2];    // tokens' codes, 2048 bytes per tile
+  LdsByte* w;       // this wavefront's weights, 4096 bytes
+  LdsByte* sa;      // tokens' scales: two chunks, 32 bytes per row
+  LdsByte* sw;      // this wavefront's weight scales: two chunks
+  static constexpr int kSa = CAP * 16 * 8 * MG_CHUNK;
+  static constexpr int kSw = 32 * 8 * MG_CHUNK;
+};
+
+// The weights of step c from the registers through LDS into MFMA operands.
+template <int G, int CAP>
+__device__ __forceinline__ MgPair mg_turn_w(mi4 (&w)[4], const MgShared<CAP>& m, const MgLane& l,
+                                            const MgRead& at, int c) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (G != 8) {   // a piece past the row belongs to the next one
+    if (8 * c + (lane & 7) >= l.nb) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = mi4{0, 0, 0, 0};
+    }
+  }
+  mg_wave_sync();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = 8 * j + (lane >> 3);
+    *(LdsInt4*)(m.w + 128 * row + 16 * ((lane & 7) ^ mg_swz(row & 15))) = w[j];
+  }
+  mg_wave_sync();
+  return mg_read(m.w, m.sw + (c / MG_CHUNK & 1) * MgShared<CAP>::kSw + 8 * (c % MG_CHUNK), at, 0);
 }
 
-template <int CAP, bool EVEN, bool GATED, bool BF16>
+// Step c: its weights in w, its tokens in m.a[B].  The tokens of step c + 1 go
+// into the other buffer, which step c - 1 has left, the weights of step c + 2
+// into w; at the first step of a chunk the next chunk's scales are requested,
+// at its last they move on to LDS.
+template <int CAP, int G, int B>
+__device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgShared<CAP>& m, const MgLane& l,
+                                        const MgRead& at, int nt, int c, mi4 (&w)[4], MgScales<G>& sa,
+                                        MgScales<G>& sw) {
+  const int next = c / MG_CHUNK + 1;
+  if (c % MG_CHUNK == 0 && next * MG_CHUNK < l.steps) {
+    mg_load_s<G>(sa, l.as, l.asv, next);
+    mg_load_s<G>(sw, l.ws, l.wsv, next);
+  }
+  mg_load_a<CAP>(l, m.a[1 - B], threadIdx.x >> 6, c + 1);
+  const MgPair wp = mg_turn_w<G, CAP>(w, m, l, at, c);
+  mg_load_w(w, l, c + 2);
+  mg_multiply<CAP>(acc, wp, m.a[B], m.sa + (c / MG_CHUNK & 1) * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK),
+                   at, nt);
+  if (c % MG_CHUNK == MG_CHUNK - 1) {
+    const int tid = threadIdx.x, b0 = next * (8 * MG_CHUNK) + 16 * (tid & 1);
+    if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + (next & 1) * MgShared<CAP>::kSa + 16 * tid, b0, l.nb);
+    mg_put_s<G>(sw, m.sw + (next & 1) * MgShared<CAP>::kSw + 16 * (tid & 63), b0, l.nb);
+  }
+  mg_barrier<4>();   // newer than the tokens of step c + 1: the weights of step c + 2
+}
+
+template <int CAP, int G, bool GATED, bool BF16>
 __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
-                                        LdsByte* buf0, LdsByte* buf1, LdsByte* buf2, LdsByte* sb0,
-                                        LdsByte* sb1, LdsByte* sb2, int* s_src) {
+                                        const MgShared<CAP>& m, int* s_src) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 15, q = lane >> 4;
   // opaque, so that no step's first products count as unconditional: the
   // compiler would move them past the barriers, to where their sums are used
   int nt = (t.rows + 15) / 16;
   asm volatile("" : "+s"(nt));
-  MgWeights w0, w1, w2;
-  MgScales s0, s1, s2;
-  mg_load_w<EVEN>(w0, l, 0);
-  mg_load_w<EVEN>(w1, l, 1);
-  mg_load_w<EVEN>(w2, l, 2);
+  mi4 w0[4], w1[4];
+  MgScales<G> sa, sw;
+  mg_load_s<G>(sw, l.ws, l.wsv, 0);
+  mg_load_w(w0, l, 0);
+  mg_load_w(w1, l, 1);
   // thread tid looks up tile row tid's source; the others take it from LDS
-  int src = -1;
-  if (tid < t.rows) {
-    bool ok;
-    src = source_row(a, t.r0 + tid, ok);
-    if (tid < 16 * CAP) s_src[tid] = ok ? src : ~src;
+  if (tid < 16 * CAP) {
+    bool ok = false;
+    int src = -1;
+    if (tid < t.rows) src = source_row(a, t.r0 + tid, ok);
+    s_src[tid] = ok ? src : ~src;   // ~src >= 0 only past the tile's rows
   }
-  l.asv = tid < t.rows ? static_cast<uint32_t>(src) * l.nb : MG_OUT;
   __syncthreads();
   // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
 #pragma unroll
@@ -477,61 +523,65 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
     l.av[j] = row < t.rows ? static_cast<uint32_t>(v < 0 ? ~v : v) * (a.K / 2) + 16 * ((lane & 7) ^ mg_swz(row & 15))
                            : MG_OUT;
   }
+  {
+    const int row = tid >> 1;
+    const int v = row < 16 * CAP ? s_src[row] : 0;
+    l.asv = row < t.rows && row < 16 * CAP ? static_cast<uint32_t>(v < 0 ? ~v : v) * l.nb + 16 * (tid & 1) : MG_OUT;
+  }
   const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
-                     r * 8 + 2 * q};
+                     r * (8 * MG_CHUNK) + 2 * q};
   mf4 acc[CAP][2] = {};
-  mg_load_a<CAP>(l, buf0, wave, 0);
-  mg_load_s<EVEN>(s0, l, 0);
-  mg_load_a<CAP>(l, buf1, wave, 1);
-  mg_load_s<EVEN>(s1, l, 1);
-  mg_put_s<EVEN>(s0, l, sb0, 0);
-  mg_barrier<CAP / 2 + mg_s_loads<EVEN>()>();
+  mg_load_s<G>(sa, l.as, l.asv, 0);
+  mg_load_a<CAP>(l, m.a[0], wave, 0);
+  if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + 16 * tid, 16 * (tid & 1), l.nb);
+  mg_put_s<G>(sw, m.sw + 16 * lane, 16 * (tid & 1), l.nb);
+  mg_barrier<0>();
   int c = 0;
-  for (; c + 3 <= l.steps; c += 3) {
-    mg_step<CAP, EVEN>(acc, l, at, nt, c, w0, buf0, sb0, buf2, s2, s1, sb1);
-    mg_step<CAP, EVEN>(acc, l, at, nt, c + 1, w1, buf1, sb1, buf0, s0, s2, sb2);
-    mg_step<CAP, EVEN>(acc, l, at, nt, c + 2, w2, buf2, sb2, buf1, s1, s0, sb0);
+  for (; c + 2 <= l.steps; c += 2) {
+    mg_step<CAP, G, 0>(acc, m, l, at, nt, c, w0, sa, sw);
+    mg_step<CAP, G, 1>(acc, m, l, at, nt, c + 1, w1, sa, sw);
   }
-  // one or two steps left: nothing more to request.  (Their waits may not
-  // count loads: the ones whose values nobody would use are not there.)
-  if (c < l.steps) {
-    mg_put_s<EVEN>(s1, l, sb1, c + 1);
-    mg_barrier<0>();
-    mg_ready<EVEN>(w0, l, c);
-    mg_multiply<CAP>(acc, w0, buf0, sb0, at, nt);
-    if (c + 1 < l.steps) {
-      mg_ready<EVEN>(w1, l, c + 1);
-      mg_multiply<CAP>(acc, w1, buf1, sb1, at, nt);
-    }
-  } else {
-    mg_barrier<0>();   // a load still on its way to LDS may not outlive the workgroup
+  if (c < l.steps) {   // one step left, with nothing more to request
+    const MgPair wp = mg_turn_w<G, CAP>(w0, m, l, at, c);
+    mg_multiply<CAP>(acc, wp, m.a[0], m.sa + (c / MG_CHUNK & 1) * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK),
+                     at, nt);
   }
-  // 32-bit offsets from the tile's first row; a row without a source is zeros
-  const int n = n0 + 32 * wave + 4 * q;
-  const int width = GATED ? a.N / 2 : a.N;
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // a load still on its way to LDS may not outlive the workgroup
+  // A tile of 16 tokens at a time through this wavefront's piece of LDS, so
+  // that neighbouring lanes store neighbouring bytes: kPer lanes to a token
   constexpr int kSize = BF16 ? 2 : 4;
-  uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + t.r0 * width * kSize;
+  constexpr int kRow = (GATED ? 16 : 32) * kSize;   // bytes of a token
+  constexpr int kPer = kRow / 16;
+  const int width = GATED ? a.N / 2 : a.N;
+  const int col = (n0 + 32 * wave) / (GATED ? 2 : 1);
+  uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + (t.r0 * width + col) * kSize;
 #pragma unroll
   for (int i = 0; i < CAP; ++i) {
-    const int local = 16 * i + r;
-    if (local < t.rows) {
-      const bool has = s_src[local] >= 0;
+    if (i < nt) {
+      mg_wave_sync();
+      const bool has = s_src[16 * i + r] >= 0;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int col = n + 16 * w;
-        if (col < a.N)
-          store_out<GATED, BF16>(y + static_cast<uint32_t>(local * width + (GATED ? col / 2 : col)) * kSize,
-                                 has ? acc[i][w] : mf4{0, 0, 0, 0});
+      for (int w = 0; w < 2; ++w)
+        put_out<GATED, BF16>(m.w + r * kRow + (16 * w + 4 * q) / (GATED ? 2 : 1) * kSize,
+                             has ? acc[i][w] : mf4{0, 0, 0, 0});
+      mg_wave_sync();
+#pragma unroll
+      for (int e = lane; e < 16 * kPer; e += 64) {
+        const int row = 16 * i + e / kPer, piece = e % kPer;
+        const mi4 v = *(const LdsInt4*)(m.w + 16 * e);
+        if (row < t.rows && col + piece * (16 / kSize) < width)
+          *reinterpret_cast<mi4*>(y + static_cast<uint32_t>(row * width) * kSize + 16 * piece) = v;
       }
     }
   }
 }
 
-template <int CAP, bool EVEN, bool GATED, bool BF16>
-__global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearArgs a) {
-  __shared__ __align__(16) uint8_t buf0[CAP * 2048], buf1[CAP * 2048], buf2[CAP * 2048];
-  // every thread carries a row's scales
-  __shared__ __align__(16) uint8_t sb0[ML_THREADS * 8], sb1[ML_THREADS * 8], sb2[ML_THREADS * 8];
+template <int CAP, int G, bool GATED, bool BF16>
+__global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups_kernel(LinearArgs a) {
+  typedef MgShared<CAP> M;
+  __shared__ __align__(16) uint8_t s_a0[CAP * 2048], s_a1[CAP * 2048];
+  __shared__ __align__(16) uint8_t s_w[4 * 4096];
+  __shared__ __align__(16) uint8_t s_sa[2 * M::kSa], s_sw[4 * 2 * M::kSw];
   __shared__ int s_src[CAP * 16];   // each row's source, complemented where it has none
   // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
   // with all their column slices, so a tile's token rows meet in one L2
@@ -540,24 +590,22 @@ __global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearA
   const RowTile t = find_row_tile(a, 8 * (i / n_wg) + (static_cast<int>(blockIdx.x) & 7), 16 * CAP);
   if (t.rows <= 0) return;
   const int n0 = i % n_wg * MG_ROWS;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = a.K / 32, crow = a.K / 2;
   MgLane l;
   l.nb = nb;
-  l.q = lane >> 4;
   l.steps = (a.K + MG_STEP - 1) / MG_STEP;
   l.ac = mg_rsrc(a.ac, a.a_rows * crow);
   l.as = mg_rsrc(a.as, a.a_rows * nb);
   const int64_t wrow = static_cast<int64_t>(t.g) * a.N;
   l.wc = mg_rsrc(a.wc + wrow * crow, static_cast<int64_t>(a.N) * crow);
   l.ws = mg_rsrc(a.ws + wrow * nb, static_cast<int64_t>(a.N) * nb);
-  const int row = n0 + 32 * wave + (lane & 15);
-  l.wv = static_cast<uint32_t>(row * crow + 32 * l.q);
-  l.wsv = static_cast<uint32_t>(row * nb + 2 * l.q);
-  l.wtile = 16 * crow;
-  l.wstile = 16 * nb;
-  mg_tile<CAP, EVEN, GATED, BF16>(a, t, l, n0, (LdsByte*)buf0, (LdsByte*)buf1, (LdsByte*)buf2,
-                                  (LdsByte*)sb0, (LdsByte*)sb1, (LdsByte*)sb2, s_src);
+  l.wv = static_cast<uint32_t>((n0 + 32 * wave + (lane >> 3)) * crow + 16 * (lane & 7));
+  l.wsv = static_cast<uint32_t>((n0 + 32 * wave + (lane >> 1)) * nb + 16 * (lane & 1));
+  l.w8 = 8 * crow;
+  const M m = {{(LdsByte*)s_a0, (LdsByte*)s_a1}, (LdsByte*)s_w + 4096 * wave, (LdsByte*)s_sa,
+               (LdsByte*)s_sw + 2 * M::kSw * wave};
+  mg_tile<CAP, G, GATED, BF16>(a, t, l, n0, m, s_src);
 }
 
 template <int CAP, bool GATED, bool BF16>
@@ -566,10 +614,13 @@ void launch_groups(const LinearArgs& a, hipStream_t s) {
   const int64_t tiles = a.offsets ? a.R / m + min(static_cast<int64_t>(a.G), a.R) : (a.R + m - 1) / m;
   const int64_t n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
   const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8 * n_wg);
-  if (a.K % MG_STEP == 0)
-    mx_linear_groups_kernel<CAP, true, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+  const int nb = a.K / 32;
+  if (nb % 8 == 0)
+    mx_linear_groups_kernel<CAP, 8, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+  else if (nb % 4 == 0)
+    mx_linear_groups_kernel<CAP, 4, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
   else
-    mx_linear_groups_kernel<CAP, false, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+    mx_linear_groups_kernel<CAP, 1, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
 }
 
 template <bool GATED, bool BF16>
