@@ -293,14 +293,17 @@ __device__ __forceinline__ void mg_wave_sync() {
 }
 
 // Buffers (a read past one gives zeros) and this lane's byte offsets in them.
+// Every offset is formed in full before the load: of a load's two offsets only
+// the vector one is checked against the buffer's end.
 struct MgLane {
   MgRsrc ac, as, wc, ws;
   uint32_t av[8];        // A codes: the row pieces this lane moves to LDS
   uint32_t asv;          // A scales: half a chunk of row tid / 2
   uint32_t wv;           // weights: piece lane % 8 of the wavefront's row lane / 8
   uint32_t wsv;          // weight scales: half a chunk of the wavefront's row lane / 2
-  int w8;                // 8 rows of weights
-  int nb, steps;
+  uint32_t w8;           // 8 rows of weights
+  uint32_t wslice, wsslice;   // one slice of weight rows: codes, scales
+  int nb, steps, slices, wave;
 };
 
 // 16 scale bytes as loaded.  G: the largest power of two up to 8 that divides
@@ -313,20 +316,20 @@ struct MgScales {
 
 template <int G>
 __device__ __forceinline__ void mg_load_s(MgScales<G>& s, MgRsrc rs, uint32_t at, int chunk) {
-  const int so = chunk * (8 * MG_CHUNK);
+  at += chunk * (8 * MG_CHUNK);
   if constexpr (G == 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const auto q = __builtin_amdgcn_raw_buffer_load_b64(rs, at + 8 * i, so, 0);
+      const auto q = __builtin_amdgcn_raw_buffer_load_b64(rs, at + 8 * i, 0, 0);
       s.v[2 * i] = q[0];
       s.v[2 * i + 1] = q[1];
     }
   } else if constexpr (G == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, at + 4 * i, so, 0);
+    for (int i = 0; i < 4; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, at + 4 * i, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, at + i, so, 0);
+    for (int i = 0; i < 16; ++i) s.v[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, at + i, 0, 0);
   }
 }
 
@@ -348,23 +351,23 @@ __device__ __forceinline__ void mg_put_s(const MgScales<G>& s, LdsByte* to, int 
   *(LdsInt4*)to = v;
 }
 
-// This wavefront's 32 weight rows of step c, 8 rows per instruction.
-__device__ __forceinline__ void mg_load_w(mi4 (&w)[4], const MgLane& l, int c) {
-  const uint32_t v = c < l.steps ? l.wv : MG_OUT;
+// This wavefront's 32 weight rows of step c of a slice, 8 rows per instruction.
+__device__ __forceinline__ void mg_load_w(mi4 (&w)[4], const MgLane& l, int slice, int c) {
+  const uint32_t v = slice < l.slices ? l.wv + slice * l.wslice + c * 128 : MG_OUT;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v, c * 128 + j * l.w8, 0));
+    w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v + j * l.w8, 0, 0));
 }
 
 // The codes of step c's tokens: 8 rows per instruction, the four wavefronts in
 // turn (rows past the tile have offsets outside the buffer).
 template <int CAP>
-__device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int wave, int c) {
+__device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int c) {
 #pragma unroll
   for (int j = 0; j < CAP / 2; ++j)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + wave) * 1024), 16,
-        c < l.steps ? l.av[j] : MG_OUT, c * 128, 0, 0);
+        l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + l.wave) * 1024), 16,
+        l.av[j] + c * 128, 0, 0, 0);
 }
 
 // This lane's byte offsets of its two pieces of a tile's row, and of the row's
@@ -398,29 +401,28 @@ __device__ __forceinline__ mf4 mg_mfma(mi4 w, mi4 x, mf4 c, int sw, int sx) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, HALF, sw, HALF, sx);
 }
 
-// One step, two token tiles at a time, the next two on their way from LDS
-// (past the last pair a read of whatever LDS holds there, not used).
-template <int CAP>
-__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgPair& w, const LdsByte* buf,
-                                            const LdsByte* sbuf, const MgRead& at, int nt) {
-  MgPair x = mg_read(buf, sbuf, at, 0);
+// One step, two token tiles (from pair P on, whose operands are x) at a time,
+// the next two on their way from LDS (past the last pair a read of whatever LDS
+// holds there, not used).  Each pair is nested in the one before, so that no
+// operand is merged from two paths, which costs copies.
+template <int CAP, int P = 0>
+__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgPair& w, const MgPair& x,
+                                            const LdsByte* buf, const LdsByte* sbuf, const MgRead& at,
+                                            int nt) {
+  if (2 * P < nt) {
+    MgPair next;
+    if constexpr (P + 1 < CAP / 2) next = mg_read(buf, sbuf, at, P + 1);
 #pragma unroll
-  for (int g = 0; g < CAP / 2; ++g) {
-    if (2 * g < nt) {
-      MgPair next = x;
-      if (g + 1 < CAP / 2) next = mg_read(buf, sbuf, at, g + 1);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < 2; ++t)
+        acc[2 * P + u][t] = mg_mfma<0>(w.x[t][0], x.x[u][0], acc[2 * P + u][t], w.s[t], x.s[u]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<0>(w.x[t][0], x.x[u][0], acc[2 * g + u][t], w.s[t], x.s[u]);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          acc[2 * g + u][t] = mg_mfma<1>(w.x[t][1], x.x[u][1], acc[2 * g + u][t], w.s[t], x.s[u]);
-      x = next;
-    }
+      for (int t = 0; t < 2; ++t)
+        acc[2 * P + u][t] = mg_mfma<1>(w.x[t][1], x.x[u][1], acc[2 * P + u][t], w.s[t], x.s[u]);
+    if constexpr (P + 1 < CAP / 2) mg_multiply<CAP, P + 1>(acc, w, next, buf, sbuf, at, nt);
   }
 }
 
@@ -446,10 +448,10 @@ struct MgShared {
   static constexpr int kSw = 32 * 8 * MG_CHUNK;
 };
 
-// The weights of step c from the registers through LDS into MFMA operands.
+// The weights of step c from the registers through LDS into MFMA operands:
+// written here,
 template <int G, int CAP>
-__device__ __forceinline__ MgPair mg_turn_w(mi4 (&w)[4], const MgShared<CAP>& m, const MgLane& l,
-                                            const MgRead& at, int c) {
+__device__ __forceinline__ void mg_write_w(mi4 (&w)[4], const MgShared<CAP>& m, const MgLane& l, int c) {
   const int lane = threadIdx.x & 63;
   if constexpr (G != 8) {   // a piece past the row belongs to the next one
     if (8 * c + (lane & 7) >= l.nb) {
@@ -464,96 +466,88 @@ __device__ __forceinline__ MgPair mg_turn_w(mi4 (&w)[4], const MgShared<CAP>& m,
     *(LdsInt4*)(m.w + 128 * row + 16 * ((lane & 7) ^ mg_swz(row & 15))) = w[j];
   }
   mg_wave_sync();
-  return mg_read(m.w, m.sw + (c / MG_CHUNK & 1) * MgShared<CAP>::kSw + 8 * (c % MG_CHUNK), at, 0);
 }
 
-// Step c: its weights in w, its tokens in m.a[B].  The tokens of step c + 1 go
-// into the other buffer, which step c - 1 has left, the weights of step c + 2
-// into w; at the first step of a chunk the next chunk's scales are requested,
-// at its last they move on to LDS.
-template <int CAP, int G, int B>
+// and read here; p: which half of the scales' LDS holds the step's chunk.
+template <int CAP>
+__device__ __forceinline__ MgPair mg_read_w(const MgShared<CAP>& m, const MgRead& at, int p, int c) {
+  return mg_read(m.w, m.sw + p * MgShared<CAP>::kSw + 8 * (c % MG_CHUNK), at, 0);
+}
+
+template <int CAP>
+__device__ __forceinline__ const LdsByte* mg_scales_at(const MgShared<CAP>& m, int p, int c) {
+  return m.sa + p * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK);
+}
+
+// Scales of a chunk into half p of their LDS.
+template <int CAP, int G>
+__device__ __forceinline__ void mg_put_chunk(const MgShared<CAP>& m, const MgLane& l, const MgScales<G>& sa,
+                                             const MgScales<G>& sw, int p, int chunk) {
+  const int tid = threadIdx.x, b0 = chunk * (8 * MG_CHUNK) + 16 * (tid & 1);
+  if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + p * MgShared<CAP>::kSa + 16 * tid, b0, l.nb);
+  mg_put_s<G>(sw, m.sw + p * MgShared<CAP>::kSw + 16 * (tid & 63), b0, l.nb);
+}
+
+// Where the products are: step c of a slice, its scales in half p.
+struct MgAt {
+  int slice, c, p;
+};
+
+// One step: its weights are operands already (wp), its tokens in m.a[B].  The
+// tokens of the next step (of the next slice's first one, after the last) go
+// into the other buffer, which the step before has left; the next step's
+// weights (in w) change lanes while the products run, and those two steps
+// further on are requested in their place.  At the first step of a chunk the
+// next chunk's scales are requested, at its last they move on to LDS.
+// LAST: nothing follows.
+template <int CAP, int G, int B, bool LAST>
 __device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgShared<CAP>& m, const MgLane& l,
-                                        const MgRead& at, int nt, int c, mi4 (&w)[4], MgScales<G>& sa,
-                                        MgScales<G>& sw) {
-  const int next = c / MG_CHUNK + 1;
-  if (c % MG_CHUNK == 0 && next * MG_CHUNK < l.steps) {
-    mg_load_s<G>(sa, l.as, l.asv, next);
-    mg_load_s<G>(sw, l.ws, l.wsv, next);
+                                        const MgRead& at, int nt, MgAt& pos, MgAt& ahead, mi4 (&w)[4],
+                                        MgPair& wp, MgScales<G>& sa, MgScales<G>& sw) {
+  const LdsByte* sbuf = mg_scales_at(m, pos.p, pos.c);
+  const MgPair x = mg_read(m.a[B], sbuf, at, 0);
+  if constexpr (LAST) {
+    mg_multiply<CAP>(acc, wp, x, m.a[B], sbuf, at, nt);
+    return;
   }
-  mg_load_a<CAP>(l, m.a[1 - B], threadIdx.x >> 6, c + 1);
-  const MgPair wp = mg_turn_w<G, CAP>(w, m, l, at, c);
-  mg_load_w(w, l, c + 2);
-  mg_multiply<CAP>(acc, wp, m.a[B], m.sa + (c / MG_CHUNK & 1) * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK),
-                   at, nt);
-  if (c % MG_CHUNK == MG_CHUNK - 1) {
-    const int tid = threadIdx.x, b0 = next * (8 * MG_CHUNK) + 16 * (tid & 1);
-    if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + (next & 1) * MgShared<CAP>::kSa + 16 * tid, b0, l.nb);
-    mg_put_s<G>(sw, m.sw + (next & 1) * MgShared<CAP>::kSw + 16 * (tid & 63), b0, l.nb);
+  const bool ends = pos.c + 1 == l.steps;   // of the slice
+  const int chunk = pos.c / MG_CHUNK;
+  const bool chunk_ends = ends || pos.c % MG_CHUNK == MG_CHUNK - 1;
+  const bool next_slice = ends || (chunk + 1) * MG_CHUNK >= l.steps;   // holds the next chunk
+  const int next_chunk = next_slice ? 0 : chunk + 1;
+  if (pos.c % MG_CHUNK == 0 && (!next_slice || pos.slice + 1 < l.slices)) {
+    mg_load_s<G>(sa, l.as, l.asv, next_chunk);
+    mg_load_s<G>(sw, l.ws, l.wsv + (pos.slice + (next_slice ? 1 : 0)) * l.wsslice, next_chunk);
   }
-  mg_barrier<4>();   // newer than the tokens of step c + 1: the weights of step c + 2
+  const int nc = ends ? 0 : pos.c + 1, np = chunk_ends ? 1 - pos.p : pos.p;
+  mg_load_a<CAP>(l, m.a[1 - B], nc);
+  if (chunk_ends) mg_put_chunk<CAP, G>(m, l, sa, sw, np, next_chunk);
+  mg_write_w<G, CAP>(w, m, l, nc);
+  mg_load_w(w, l, ahead.slice, ahead.c);
+  const MgPair wn = mg_read_w(m, at, np, nc);
+  mg_multiply<CAP>(acc, wp, x, m.a[B], sbuf, at, nt);
+  wp = wn;
+  pos.slice += ends ? 1 : 0;
+  pos.c = nc;
+  pos.p = np;
+  const bool over = ahead.c + 1 == l.steps;
+  ahead.slice += over ? 1 : 0;
+  ahead.c = over ? 0 : ahead.c + 1;
+  mg_barrier<4>();   // newer than the next step's tokens: the weights requested here
 }
 
-template <int CAP, int G, bool GATED, bool BF16>
-__device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
-                                        const MgShared<CAP>& m, int* s_src) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = lane & 15, q = lane >> 4;
-  // opaque, so that no step's first products count as unconditional: the
-  // compiler would move them past the barriers, to where their sums are used
-  int nt = (t.rows + 15) / 16;
-  asm volatile("" : "+s"(nt));
-  mi4 w0[4], w1[4];
-  MgScales<G> sa, sw;
-  mg_load_s<G>(sw, l.ws, l.wsv, 0);
-  mg_load_w(w0, l, 0);
-  mg_load_w(w1, l, 1);
-  // thread tid looks up tile row tid's source; the others take it from LDS
-  if (tid < 16 * CAP) {
-    bool ok = false;
-    int src = -1;
-    if (tid < t.rows) src = source_row(a, t.r0 + tid, ok);
-    s_src[tid] = ok ? src : ~src;   // ~src >= 0 only past the tile's rows
-  }
-  __syncthreads();
-  // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
-#pragma unroll
-  for (int j = 0; j < CAP / 2; ++j) {
-    const int row = 8 * (4 * j + wave) + (lane >> 3);
-    const int v = s_src[row];
-    l.av[j] = row < t.rows ? static_cast<uint32_t>(v < 0 ? ~v : v) * (a.K / 2) + 16 * ((lane & 7) ^ mg_swz(row & 15))
-                           : MG_OUT;
-  }
-  {
-    const int row = tid >> 1;
-    const int v = row < 16 * CAP ? s_src[row] : 0;
-    l.asv = row < t.rows && row < 16 * CAP ? static_cast<uint32_t>(v < 0 ? ~v : v) * l.nb + 16 * (tid & 1) : MG_OUT;
-  }
-  const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
-                     r * (8 * MG_CHUNK) + 2 * q};
-  mf4 acc[CAP][2] = {};
-  mg_load_s<G>(sa, l.as, l.asv, 0);
-  mg_load_a<CAP>(l, m.a[0], wave, 0);
-  if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + 16 * tid, 16 * (tid & 1), l.nb);
-  mg_put_s<G>(sw, m.sw + 16 * lane, 16 * (tid & 1), l.nb);
-  mg_barrier<0>();
-  int c = 0;
-  for (; c + 2 <= l.steps; c += 2) {
-    mg_step<CAP, G, 0>(acc, m, l, at, nt, c, w0, sa, sw);
-    mg_step<CAP, G, 1>(acc, m, l, at, nt, c + 1, w1, sa, sw);
-  }
-  if (c < l.steps) {   // one step left, with nothing more to request
-    const MgPair wp = mg_turn_w<G, CAP>(w0, m, l, at, c);
-    mg_multiply<CAP>(acc, wp, m.a[0], m.sa + (c / MG_CHUNK & 1) * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK),
-                     at, nt);
-  }
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // a load still on its way to LDS may not outlive the workgroup
-  // A tile of 16 tokens at a time through this wavefront's piece of LDS, so
-  // that neighbouring lanes store neighbouring bytes: kPer lanes to a token
+// The results of a slice: a tile of 16 tokens at a time through this
+// wavefront's piece of LDS, so that neighbouring lanes store neighbouring
+// bytes, kPer lanes to a token.  Leaves the sums zero.
+template <int CAP, bool GATED, bool BF16>
+__device__ __forceinline__ void mg_store(const LinearArgs& a, const RowTile& t, mf4 (&acc)[CAP][2],
+                                         const MgShared<CAP>& m, int n0, int nt, const int* s_src) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   constexpr int kSize = BF16 ? 2 : 4;
   constexpr int kRow = (GATED ? 16 : 32) * kSize;   // bytes of a token
   constexpr int kPer = kRow / 16;
   const int width = GATED ? a.N / 2 : a.N;
-  const int col = (n0 + 32 * wave) / (GATED ? 2 : 1);
+  const int col = n0 / (GATED ? 2 : 1);
   uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + (t.r0 * width + col) * kSize;
 #pragma unroll
   for (int i = 0; i < CAP; ++i) {
@@ -561,9 +555,11 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
       mg_wave_sync();
       const bool has = s_src[16 * i + r] >= 0;
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < 2; ++w) {
         put_out<GATED, BF16>(m.w + r * kRow + (16 * w + 4 * q) / (GATED ? 2 : 1) * kSize,
                              has ? acc[i][w] : mf4{0, 0, 0, 0});
+        acc[i][w] = mf4{0, 0, 0, 0};
+      }
       mg_wave_sync();
 #pragma unroll
       for (int e = lane; e < 16 * kPer; e += 64) {
@@ -577,7 +573,76 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
 }
 
 template <int CAP, int G, bool GATED, bool BF16>
-__global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups_kernel(LinearArgs a) {
+__device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
+                                        const MgShared<CAP>& m, int* s_src) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int r = lane & 15, q = lane >> 4;
+  // opaque, so that no step's first products count as unconditional: the
+  // compiler would move them past the barriers, to where their sums are used
+  int nt = (t.rows + 15) / 16;
+  asm volatile("" : "+s"(nt));
+  mi4 w0[4], w1[4];
+  MgScales<G> sa, sw;
+  MgAt pos = {0, 0, 0}, ahead = {0, 0, 0};
+  const auto load_ahead = [&](mi4 (&w)[4]) {
+    mg_load_w(w, l, ahead.slice, ahead.c);
+    const bool over = ahead.c + 1 == l.steps;
+    ahead.slice += over ? 1 : 0;
+    ahead.c = over ? 0 : ahead.c + 1;
+  };
+  mg_load_s<G>(sw, l.ws, l.wsv, 0);
+  load_ahead(w0);
+  load_ahead(w1);
+  // thread tid looks up tile row tid's source; the others take it from LDS
+  if (tid < 16 * CAP) {
+    bool ok = false;
+    int src = -1;
+    if (tid < t.rows) src = source_row(a, t.r0 + tid, ok);
+    s_src[tid] = ok ? src : ~src;   // ~src >= 0 only past the tile's rows
+  }
+  __syncthreads();
+  // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
+#pragma unroll
+  for (int j = 0; j < CAP / 2; ++j) {
+    const int row = 8 * (4 * j + l.wave) + (lane >> 3);
+    const int v = s_src[row];
+    l.av[j] = row < t.rows ? static_cast<uint32_t>(v < 0 ? ~v : v) * (a.K / 2) + 16 * ((lane & 7) ^ mg_swz(row & 15))
+                           : MG_OUT;
+  }
+  {
+    const int row = tid >> 1;
+    const int v = row < 16 * CAP ? s_src[row] : 0;
+    l.asv = row < t.rows && row < 16 * CAP ? static_cast<uint32_t>(v < 0 ? ~v : v) * l.nb + 16 * (tid & 1) : MG_OUT;
+  }
+  const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
+                     r * (8 * MG_CHUNK) + 2 * q};
+  mf4 acc[CAP][2] = {};
+  mg_load_s<G>(sa, l.as, l.asv, 0);
+  mg_load_a<CAP>(l, m.a[0], 0);
+  mg_put_chunk<CAP, G>(m, l, sa, sw, 0, 0);
+  mg_barrier<0>();
+  // the weights of the first step become operands; those of the next two are
+  // in w1 and on their way into w0
+  mg_write_w<G, CAP>(w0, m, l, 0);
+  load_ahead(w0);
+  MgPair wp = mg_read_w(m, at, 0, 0);
+  const int total = l.slices * l.steps;
+  int done = 0;   // slices stored
+  for (int v = 0; v + 2 <= total; v += 2) {
+    mg_step<CAP, G, 0, false>(acc, m, l, at, nt, pos, ahead, w1, wp, sa, sw);
+    if (pos.slice > done) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, nt, s_src);
+    mg_step<CAP, G, 1, false>(acc, m, l, at, nt, pos, ahead, w0, wp, sa, sw);
+    if (pos.slice > done) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, nt, s_src);
+  }
+  if (total & 1) mg_step<CAP, G, 0, true>(acc, m, l, at, nt, pos, ahead, w1, wp, sa, sw);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // a load still on its way to LDS may not outlive the workgroup
+  if (done < l.slices) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done, nt, s_src);
+}
+
+// slices: of MG_ROWS weight rows, one after the other, per workgroup.
+template <int CAP, int G, bool GATED, bool BF16>
+__global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups_kernel(LinearArgs a,
+                                                                                       int slices) {
   typedef MgShared<CAP> M;
   __shared__ __align__(16) uint8_t s_a0[CAP * 2048], s_a1[CAP * 2048];
   __shared__ __align__(16) uint8_t s_w[4 * 4096];
@@ -585,42 +650,51 @@ __global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups
   __shared__ int s_src[CAP * 16];   // each row's source, complemented where it has none
   // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
   // with all their column slices, so a tile's token rows meet in one L2
-  const int n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
+  const int n_slices = (a.N + MG_ROWS - 1) / MG_ROWS, n_wg = (n_slices + slices - 1) / slices;
   const int i = static_cast<int>(blockIdx.x) >> 3;
   const RowTile t = find_row_tile(a, 8 * (i / n_wg) + (static_cast<int>(blockIdx.x) & 7), 16 * CAP);
   if (t.rows <= 0) return;
-  const int n0 = i % n_wg * MG_ROWS;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int s0 = i % n_wg * slices, n0 = s0 * MG_ROWS;
+  const int lane = threadIdx.x & 63;
   const int nb = a.K / 32, crow = a.K / 2;
   MgLane l;
+  l.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   l.nb = nb;
   l.steps = (a.K + MG_STEP - 1) / MG_STEP;
+  l.slices = min(slices, n_slices - s0);
   l.ac = mg_rsrc(a.ac, a.a_rows * crow);
   l.as = mg_rsrc(a.as, a.a_rows * nb);
   const int64_t wrow = static_cast<int64_t>(t.g) * a.N;
   l.wc = mg_rsrc(a.wc + wrow * crow, static_cast<int64_t>(a.N) * crow);
   l.ws = mg_rsrc(a.ws + wrow * nb, static_cast<int64_t>(a.N) * nb);
-  l.wv = static_cast<uint32_t>((n0 + 32 * wave + (lane >> 3)) * crow + 16 * (lane & 7));
-  l.wsv = static_cast<uint32_t>((n0 + 32 * wave + (lane >> 1)) * nb + 16 * (lane & 1));
+  l.wv = static_cast<uint32_t>((n0 + 32 * l.wave + (lane >> 3)) * crow + 16 * (lane & 7));
+  l.wsv = static_cast<uint32_t>((n0 + 32 * l.wave + (lane >> 1)) * nb + 16 * (lane & 1));
   l.w8 = 8 * crow;
-  const M m = {{(LdsByte*)s_a0, (LdsByte*)s_a1}, (LdsByte*)s_w + 4096 * wave, (LdsByte*)s_sa,
-               (LdsByte*)s_sw + 2 * M::kSw * wave};
-  mg_tile<CAP, G, GATED, BF16>(a, t, l, n0, m, s_src);
+  l.wslice = MG_ROWS * crow;
+  l.wsslice = MG_ROWS * nb;
+  const M m = {{(LdsByte*)s_a0, (LdsByte*)s_a1}, (LdsByte*)s_w + 4096 * l.wave, (LdsByte*)s_sa,
+               (LdsByte*)s_sw + 2 * M::kSw * l.wave};
+  mg_tile<CAP, G, GATED, BF16>(a, t, l, n0 + 32 * l.wave, m, s_src);
 }
 
 template <int CAP, bool GATED, bool BF16>
 void launch_groups(const LinearArgs& a, hipStream_t s) {
   const int64_t m = 16 * CAP;
   const int64_t tiles = a.offsets ? a.R / m + min(static_cast<int64_t>(a.G), a.R) : (a.R + m - 1) / m;
-  const int64_t n_wg = (a.N + MG_ROWS - 1) / MG_ROWS;
-  const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8 * n_wg);
+  const int64_t n_slices = (a.N + MG_ROWS - 1) / MG_ROWS;
+  // A workgroup's start (its tile, its rows' sources, the first loads) costs as
+  // much as a third of a slice of 2,048 columns; up to four slices share it
+  // where enough workgroups are left to even out the end.
+  const int64_t want = int64_t{8} * device_cus();
+  const int slices = static_cast<int>(min(max(tiles * n_slices / want, int64_t{1}), min(int64_t{4}, n_slices)));
+  const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8 * ((n_slices + slices - 1) / slices));
   const int nb = a.K / 32;
   if (nb % 8 == 0)
-    mx_linear_groups_kernel<CAP, 8, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+    mx_linear_groups_kernel<CAP, 8, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a, slices);
   else if (nb % 4 == 0)
-    mx_linear_groups_kernel<CAP, 4, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+    mx_linear_groups_kernel<CAP, 4, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a, slices);
   else
-    mx_linear_groups_kernel<CAP, 1, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+    mx_linear_groups_kernel<CAP, 1, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a, slices);
 }
 
 template <bool GATED, bool BF16>
