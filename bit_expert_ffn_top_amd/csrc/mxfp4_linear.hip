@@ -48,20 +48,31 @@ struct RowTile {
   int g;
   int rows;
   int64_t r0;
+  bool whole;   // all rows of the group
 };
 
-// Tile number `tile` of the row tiles of all groups in order (tile_m rows
-// each, the last of a group shorter).  All threads of the workgroup take part;
-// rows = 0 past the last tile.  Each thread counts the tiles of its own run of
-// groups; the runs are scanned over the workgroup, and the thread whose run
-// holds the tile says where it lies.
-__device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int tile, int tile_m) {
+// Number `at` of the row tiles that XCD `xcd` takes (xcd < 0: of all), which is
+// an eighth of the row tiles of all groups, in order: neighbouring tiles mostly
+// belong to one group, and what they share meets in one L2.  tile_m rows each,
+// the last of a group shorter.  All threads of the workgroup take part; rows = 0
+// past the last tile.  Each thread counts the tiles of its own run of groups;
+// the runs are scanned over the workgroup, and the thread whose run holds the
+// tile says where it lies.
+__device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int xcd, int at_tile, int tile_m) {
+  const auto number = [&](int total) {   // of the tile among all, -1 if there is none
+    if (xcd < 0) return at_tile;
+    const int share = (total + 7) / 8;
+    return at_tile < share ? xcd * share + at_tile : -1;
+  };
   if (a.offsets == nullptr) {
+    const int tile = number(static_cast<int>((a.R + tile_m - 1) / tile_m));
+    if (tile < 0) return RowTile{0, 0, 0, true};
     const int64_t r0 = static_cast<int64_t>(tile) * tile_m;
-    return RowTile{0, static_cast<int>(min(static_cast<int64_t>(tile_m), max(a.R - r0, int64_t{0}))), r0};
+    return RowTile{0, static_cast<int>(min(static_cast<int64_t>(tile_m), max(a.R - r0, int64_t{0}))), r0,
+                   a.R <= tile_m};
   }
   __shared__ int s_wave[ML_THREADS / 64];
-  __shared__ int s_g, s_rows, s_r0;
+  __shared__ int s_g, s_rows, s_r0, s_whole;
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kPer = (MOE_MAX_EXPERTS + ML_THREADS - 1) / ML_THREADS;
   const int R = static_cast<int>(a.R);
@@ -85,8 +96,13 @@ __device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int tile, 
   if (lane == 63) s_wave[tid >> 6] = scan;
   if (tid == 0) s_rows = 0;
   __syncthreads();
-  int at = scan - mine;
-  for (int w = 0; w < (tid >> 6); ++w) at += s_wave[w];
+  int at = scan - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < ML_THREADS / 64; ++w) {
+    at += w < (tid >> 6) ? s_wave[w] : 0;
+    total += s_wave[w];
+  }
+  const int tile = number(total);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (tile >= at && tile < at + nt[i]) {   // one thread, one i
@@ -94,13 +110,14 @@ __device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int tile, 
       s_g = tid * kPer + i;
       s_r0 = r0;
       s_rows = min(tile_m, bound[i + 1] - r0);
+      s_whole = nt[i] == 1;
     }
     at += nt[i];
   }
   __syncthreads();
   // the same in every thread: kept in scalar registers
   return RowTile{__builtin_amdgcn_readfirstlane(s_g), __builtin_amdgcn_readfirstlane(s_rows),
-                 __builtin_amdgcn_readfirstlane(s_r0)};
+                 __builtin_amdgcn_readfirstlane(s_r0), __builtin_amdgcn_readfirstlane(s_whole) != 0};
 }
 
 // A's row for output row r; 0 and ok = false if there is none.
@@ -182,7 +199,7 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
   constexpr int WAVES = ML_THREADS / 64;
   constexpr int TILES = WAVES / SPLIT;       // 16-row weight tiles per workgroup
   const int n_wg = (a.N + 16 * TILES - 1) / (16 * TILES);
-  const RowTile t = find_row_tile(a, static_cast<int>(blockIdx.x) / n_wg, 16 * MT);
+  const RowTile t = find_row_tile(a, -1, static_cast<int>(blockIdx.x) / n_wg, 16 * MT);
   if (t.rows <= 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
@@ -250,8 +267,10 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 }
 
 // Many rows per group.  A workgroup takes MG_ROWS weight rows and up to 16 CAP
-// tokens of one group; each of its four wavefronts owns 32 of the weight rows
-// (two MFMA tiles) for all the tokens, 256 columns per step.
+// tokens of one group; each of its four wavefronts owns 64 of the weight rows
+// (four MFMA tiles) for all the tokens, 256 columns per step: the more weight
+// rows a wavefront has, the fewer times the tokens are read from LDS, which is
+// the busiest part where groups are full.
 //
 // The MFMA wants row l % 16 in lane l, so a load straight into its operands
 // would touch 64 places with 16 bytes each, and the path from the caches, which
@@ -261,12 +280,14 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 // lanes in LDS, 16-byte piece p of row r at position p ^ swz(r), which spreads
 // the 16 rows that a read of one piece touches over all banks:
 //   the tokens' codes, which all wavefronts share, by loads that write LDS
-//     directly, one step ahead (they come from L2);
-//   a wavefront's weights through its registers, two steps ahead (they come
-//     from memory), and a piece of LDS of its own, without a barrier;
-//   scales, four steps at a time, through registers.
-// Token tiles past a short group's rows are skipped.
-constexpr int MG_ROWS = 128;
+//     directly;
+//   a wavefront's weights through its registers and a piece of LDS of its own,
+//     without a barrier;
+//   scales, four steps at a time, through registers;
+// each requested one step ahead.
+// The products of 2, 4, 6 or 8 token tiles are code of their own.
+constexpr int MG_TILES = 4;              // of 16 weight rows per wavefront
+constexpr int MG_ROWS = 4 * 16 * MG_TILES;
 constexpr int MG_STEP = 256;             // columns per step
 constexpr int MG_CHUNK = 4;              // steps per load of scales, 32 bytes of a row
 constexpr uint32_t MG_OUT = 0x80000000u; // an offset outside every buffer: reads zeros, no traffic
@@ -300,10 +321,11 @@ struct MgLane {
   uint32_t av[8];        // A codes: the row pieces this lane moves to LDS
   uint32_t asv;          // A scales: half a chunk of row tid / 2
   uint32_t wv;           // weights: piece lane % 8 of the wavefront's row lane / 8
-  uint32_t wsv;          // weight scales: half a chunk of the wavefront's row lane / 2
+  uint32_t wsv, ws32;    // weight scales: half a chunk of the wavefront's row lane / 2; 32 rows
   uint32_t w8;           // 8 rows of weights
   uint32_t wslice, wsslice;   // one slice of weight rows: codes, scales
   int nb, steps, slices, wave;
+  bool stream;           // nobody else reads these weights: they need not stay in the caches
 };
 
 // 16 scale bytes as loaded.  G: the largest power of two up to 8 that divides
@@ -351,20 +373,26 @@ __device__ __forceinline__ void mg_put_s(const MgScales<G>& s, LdsByte* to, int 
   *(LdsInt4*)to = v;
 }
 
-// This wavefront's 32 weight rows of step c of a slice, 8 rows per instruction.
-__device__ __forceinline__ void mg_load_w(mi4 (&w)[4], const MgLane& l, int slice, int c) {
+// This wavefront's weight rows of step c of a slice, 8 rows per instruction.
+__device__ __forceinline__ void mg_load_w(mi4 (&w)[2 * MG_TILES], const MgLane& l, int slice, int c) {
   const uint32_t v = slice < l.slices ? l.wv + slice * l.wslice + c * 128 : MG_OUT;
+  if (l.stream) {   // cache policy 2: nontemporal
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v + j * l.w8, 0, 0));
+    for (int j = 0; j < 2 * MG_TILES; ++j)
+      w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v + j * l.w8, 0, 2));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2 * MG_TILES; ++j)
+      w[j] = __builtin_bit_cast(mi4, __builtin_amdgcn_raw_buffer_load_b128(l.wc, v + j * l.w8, 0, 0));
+  }
 }
 
 // The codes of step c's tokens: 8 rows per instruction, the four wavefronts in
 // turn (rows past the tile have offsets outside the buffer).
-template <int CAP>
+template <int NT>
 __device__ __forceinline__ void mg_load_a(const MgLane& l, LdsByte* buf, int c) {
 #pragma unroll
-  for (int j = 0; j < CAP / 2; ++j)
+  for (int j = 0; j < (NT + 1) / 2; ++j)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         l.ac, (__attribute__((address_space(3))) void*)(buf + (4 * j + l.wave) * 1024), 16,
         l.av[j] + c * 128, 0, 0, 0);
@@ -376,21 +404,18 @@ struct MgRead {
   int k0, k1, s;
 };
 
-// The operands of two tiles of 16 rows (weights or tokens).
-struct MgPair {
-  mi4 x[2][2];
-  int s[2];
+// The operands of N tiles of 16 rows (weights or tokens).
+template <int N>
+struct MgTiles {
+  mi4 x[N][2];
+  int s[N];
 };
 
-__device__ __forceinline__ MgPair mg_read(const LdsByte* buf, const LdsByte* sbuf, const MgRead& at, int g) {
-  MgPair x;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = 2 * g + u;
-    x.x[u][0] = *(const LdsInt4*)(buf + at.k0 + 2048 * i);
-    x.x[u][1] = *(const LdsInt4*)(buf + at.k1 + 2048 * i);
-    x.s[u] = *(const LdsU16*)(sbuf + at.s + 16 * 8 * MG_CHUNK * i);
-  }
+__device__ __forceinline__ MgTiles<1> mg_read(const LdsByte* buf, const LdsByte* sbuf, const MgRead& at, int i) {
+  MgTiles<1> x;
+  x.x[0][0] = *(const LdsInt4*)(buf + at.k0 + 2048 * i);
+  x.x[0][1] = *(const LdsInt4*)(buf + at.k1 + 2048 * i);
+  x.s[0] = *(const LdsU16*)(sbuf + at.s + 16 * 8 * MG_CHUNK * i);
   return x;
 }
 
@@ -401,29 +426,29 @@ __device__ __forceinline__ mf4 mg_mfma(mi4 w, mi4 x, mf4 c, int sw, int sx) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, HALF, sw, HALF, sx);
 }
 
-// One step, two token tiles (from pair P on, whose operands are x) at a time,
-// the next two on their way from LDS (past the last pair a read of whatever LDS
-// holds there, not used).  Each pair is nested in the one before, so that no
-// operand is merged from two paths, which costs copies.
-template <int CAP, int P = 0>
-__device__ __forceinline__ void mg_multiply(mf4 (&acc)[CAP][2], const MgPair& w, const MgPair& x,
-                                            const LdsByte* buf, const LdsByte* sbuf, const MgRead& at,
-                                            int nt) {
-  if (2 * P < nt) {
-    MgPair next;
-    if constexpr (P + 1 < CAP / 2) next = mg_read(buf, sbuf, at, P + 1);
+// One step, a token tile at a time, the next on its way from LDS.  The sums
+// are opaque afterwards: the compiler would move products past the barrier, to
+// where their sums are used next.
+template <int NT>
+__device__ __forceinline__ void mg_multiply(mf4 (&acc)[NT][MG_TILES], const MgTiles<MG_TILES>& w,
+                                            MgTiles<1> x, const LdsByte* buf, const LdsByte* sbuf,
+                                            const MgRead& at) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+  for (int i = 0; i < NT; ++i) {
+    MgTiles<1> next = x;
+    if (i + 1 < NT) next = mg_read(buf, sbuf, at, i + 1);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        acc[2 * P + u][t] = mg_mfma<0>(w.x[t][0], x.x[u][0], acc[2 * P + u][t], w.s[t], x.s[u]);
+    for (int t = 0; t < MG_TILES; ++t)
+      acc[i][t] = mg_mfma<0>(w.x[t][0], x.x[0][0], acc[i][t], w.s[t], x.s[0]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        acc[2 * P + u][t] = mg_mfma<1>(w.x[t][1], x.x[u][1], acc[2 * P + u][t], w.s[t], x.s[u]);
-    if constexpr (P + 1 < CAP / 2) mg_multiply<CAP, P + 1>(acc, w, next, buf, sbuf, at, nt);
+    for (int t = 0; t < MG_TILES; ++t)
+      acc[i][t] = mg_mfma<1>(w.x[t][1], x.x[0][1], acc[i][t], w.s[t], x.s[0]);
+    x = next;
   }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < MG_TILES; ++t) opaque(acc[i][t]);
 }
 
 // At most N of this wavefront's loads are still on their way (they arrive in
@@ -441,37 +466,43 @@ __device__ __forceinline__ void mg_barrier() {
 template <int CAP>
 struct MgShared {
   LdsByte* a[2];    // tokens' codes, 2048 bytes per tile
-  LdsByte* w;       // this wavefront's weights, 4096 bytes
+  LdsByte* w;       // this wavefront's: a weight tile, or results
   LdsByte* sa;      // tokens' scales: two chunks, 32 bytes per row
   LdsByte* sw;      // this wavefront's weight scales: two chunks
   static constexpr int kSa = CAP * 16 * 8 * MG_CHUNK;
-  static constexpr int kSw = 32 * 8 * MG_CHUNK;
+  static constexpr int kSw = 16 * MG_TILES * 8 * MG_CHUNK;
+  static constexpr int kW = 4096;
 };
 
-// The weights of step c from the registers through LDS into MFMA operands:
-// written here,
+// The weights of step c from the registers through LDS into MFMA operands, a
+// tile of 16 rows at a time; p: which half of the scales' LDS holds the step's
+// chunk.
 template <int G, int CAP>
-__device__ __forceinline__ void mg_write_w(mi4 (&w)[4], const MgShared<CAP>& m, const MgLane& l, int c) {
+__device__ __forceinline__ MgTiles<MG_TILES> mg_turn_w(mi4 (&w)[2 * MG_TILES], const MgShared<CAP>& m,
+                                                       const MgLane& l, const MgRead& at, int p, int c) {
   const int lane = threadIdx.x & 63;
   if constexpr (G != 8) {   // a piece past the row belongs to the next one
     if (8 * c + (lane & 7) >= l.nb) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = mi4{0, 0, 0, 0};
+      for (int j = 0; j < 2 * MG_TILES; ++j) w[j] = mi4{0, 0, 0, 0};
     }
   }
-  mg_wave_sync();
+  const LdsByte* sbuf = m.sw + p * MgShared<CAP>::kSw + 8 * (c % MG_CHUNK);
+  MgTiles<MG_TILES> x;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = 8 * j + (lane >> 3);
-    *(LdsInt4*)(m.w + 128 * row + 16 * ((lane & 7) ^ mg_swz(row & 15))) = w[j];
+  for (int u = 0; u < MG_TILES; ++u) {
+    mg_wave_sync();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * j + (lane >> 3);
+      *(LdsInt4*)(m.w + 128 * row + 16 * ((lane & 7) ^ mg_swz(row))) = w[2 * u + j];
+    }
+    mg_wave_sync();
+    x.x[u][0] = *(const LdsInt4*)(m.w + at.k0);
+    x.x[u][1] = *(const LdsInt4*)(m.w + at.k1);
+    x.s[u] = *(const LdsU16*)(sbuf + at.s + 16 * 8 * MG_CHUNK * u);
   }
-  mg_wave_sync();
-}
-
-// and read here; p: which half of the scales' LDS holds the step's chunk.
-template <int CAP>
-__device__ __forceinline__ MgPair mg_read_w(const MgShared<CAP>& m, const MgRead& at, int p, int c) {
-  return mg_read(m.w, m.sw + p * MgShared<CAP>::kSw + 8 * (c % MG_CHUNK), at, 0);
+  return x;
 }
 
 template <int CAP>
@@ -479,13 +510,28 @@ __device__ __forceinline__ const LdsByte* mg_scales_at(const MgShared<CAP>& m, i
   return m.sa + p * MgShared<CAP>::kSa + 8 * (c % MG_CHUNK);
 }
 
-// Scales of a chunk into half p of their LDS.
+// A chunk's scales on their way: of half a token row, and of half of two
+// weight rows, 32 apart.
+template <int G>
+struct MgChunk {
+  MgScales<G> a, w[2];
+};
+
+template <int G>
+__device__ __forceinline__ void mg_load_chunk(MgChunk<G>& s, const MgLane& l, int slice, int chunk) {
+  mg_load_s<G>(s.a, l.as, l.asv, chunk);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) mg_load_s<G>(s.w[i], l.ws, l.wsv + slice * l.wsslice + i * l.ws32, chunk);
+}
+
+// Into half p of their LDS.
 template <int CAP, int G>
-__device__ __forceinline__ void mg_put_chunk(const MgShared<CAP>& m, const MgLane& l, const MgScales<G>& sa,
-                                             const MgScales<G>& sw, int p, int chunk) {
-  const int tid = threadIdx.x, b0 = chunk * (8 * MG_CHUNK) + 16 * (tid & 1);
-  if (tid < 32 * CAP) mg_put_s<G>(sa, m.sa + p * MgShared<CAP>::kSa + 16 * tid, b0, l.nb);
-  mg_put_s<G>(sw, m.sw + p * MgShared<CAP>::kSw + 16 * (tid & 63), b0, l.nb);
+__device__ __forceinline__ void mg_put_chunk(const MgShared<CAP>& m, const MgLane& l, const MgChunk<G>& s,
+                                             int p, int chunk) {
+  const int tid = threadIdx.x, lane = tid & 63, b0 = chunk * (8 * MG_CHUNK) + 16 * (tid & 1);
+  if (tid < 32 * CAP) mg_put_s<G>(s.a, m.sa + p * MgShared<CAP>::kSa + 16 * tid, b0, l.nb);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) mg_put_s<G>(s.w[i], m.sw + p * MgShared<CAP>::kSw + 16 * (lane + 64 * i), b0, l.nb);
 }
 
 // Where the products are: step c of a slice, its scales in half p.
@@ -493,21 +539,18 @@ struct MgAt {
   int slice, c, p;
 };
 
-// One step: its weights are operands already (wp), its tokens in m.a[B].  The
-// tokens of the next step (of the next slice's first one, after the last) go
-// into the other buffer, which the step before has left; the next step's
-// weights (in w) change lanes while the products run, and those two steps
-// further on are requested in their place.  At the first step of a chunk the
-// next chunk's scales are requested, at its last they move on to LDS.
-// LAST: nothing follows.
-template <int CAP, int G, int B, bool LAST>
-__device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgShared<CAP>& m, const MgLane& l,
-                                        const MgRead& at, int nt, MgAt& pos, MgAt& ahead, mi4 (&w)[4],
-                                        MgPair& wp, MgScales<G>& sa, MgScales<G>& sw) {
+// One step: its weights are in w, its tokens in m.a[B].  The tokens of the next
+// step (of the next slice's first one, after the last) go into the other
+// buffer, which the step before has left, its weights into w once this step's
+// have left it.  At the first step of a chunk the next chunk's scales are
+// requested, at its last they move on to LDS.  LAST: nothing follows.
+template <int CAP, int NT, int G, int B, bool LAST>
+__device__ __forceinline__ void mg_step(mf4 (&acc)[NT][MG_TILES], const MgShared<CAP>& m, const MgLane& l,
+                                        const MgRead& at, MgAt& pos, mi4 (&w)[2 * MG_TILES], MgChunk<G>& sc) {
   const LdsByte* sbuf = mg_scales_at(m, pos.p, pos.c);
-  const MgPair x = mg_read(m.a[B], sbuf, at, 0);
   if constexpr (LAST) {
-    mg_multiply<CAP>(acc, wp, x, m.a[B], sbuf, at, nt);
+    const MgTiles<MG_TILES> wp = mg_turn_w<G, CAP>(w, m, l, at, pos.p, pos.c);
+    mg_multiply<NT>(acc, wp, mg_read(m.a[B], sbuf, at, 0), m.a[B], sbuf, at);
     return;
   }
   const bool ends = pos.c + 1 == l.steps;   // of the slice
@@ -516,83 +559,74 @@ __device__ __forceinline__ void mg_step(mf4 (&acc)[CAP][2], const MgShared<CAP>&
   const bool next_slice = ends || (chunk + 1) * MG_CHUNK >= l.steps;   // holds the next chunk
   const int next_chunk = next_slice ? 0 : chunk + 1;
   if (pos.c % MG_CHUNK == 0 && (!next_slice || pos.slice + 1 < l.slices)) {
-    mg_load_s<G>(sa, l.as, l.asv, next_chunk);
-    mg_load_s<G>(sw, l.ws, l.wsv + (pos.slice + (next_slice ? 1 : 0)) * l.wsslice, next_chunk);
+    mg_load_chunk<G>(sc, l, pos.slice + (next_slice ? 1 : 0), next_chunk);
   }
-  const int nc = ends ? 0 : pos.c + 1, np = chunk_ends ? 1 - pos.p : pos.p;
-  mg_load_a<CAP>(l, m.a[1 - B], nc);
-  if (chunk_ends) mg_put_chunk<CAP, G>(m, l, sa, sw, np, next_chunk);
-  mg_write_w<G, CAP>(w, m, l, nc);
-  mg_load_w(w, l, ahead.slice, ahead.c);
-  const MgPair wn = mg_read_w(m, at, np, nc);
-  mg_multiply<CAP>(acc, wp, x, m.a[B], sbuf, at, nt);
-  wp = wn;
+  const int nc = ends ? 0 : pos.c + 1;
+  mg_load_a<NT>(l, m.a[1 - B], nc);
+  const MgTiles<MG_TILES> wp = mg_turn_w<G, CAP>(w, m, l, at, pos.p, pos.c);
+  const MgTiles<1> x = mg_read(m.a[B], sbuf, at, 0);
+  mg_load_w(w, l, pos.slice + (ends ? 1 : 0), nc);
+  mg_multiply<NT>(acc, wp, x, m.a[B], sbuf, at);
+  if (chunk_ends) mg_put_chunk<CAP, G>(m, l, sc, 1 - pos.p, next_chunk);
   pos.slice += ends ? 1 : 0;
   pos.c = nc;
-  pos.p = np;
-  const bool over = ahead.c + 1 == l.steps;
-  ahead.slice += over ? 1 : 0;
-  ahead.c = over ? 0 : ahead.c + 1;
-  mg_barrier<4>();   // newer than the next step's tokens: the weights requested here
+  pos.p = chunk_ends ? 1 - pos.p : pos.p;
+  mg_barrier<2 * MG_TILES>();   // newer than the next step's tokens: its weights
 }
 
-// The results of a slice: a tile of 16 tokens at a time through this
+// The results of a slice: two tiles of 16 tokens at a time through this
 // wavefront's piece of LDS, so that neighbouring lanes store neighbouring
-// bytes, kPer lanes to a token.  Leaves the sums zero.
-template <int CAP, bool GATED, bool BF16>
-__device__ __forceinline__ void mg_store(const LinearArgs& a, const RowTile& t, mf4 (&acc)[CAP][2],
-                                         const MgShared<CAP>& m, int n0, int nt, const int* s_src) {
+// bytes, kPer lanes to a token; kPass weight tiles of it at a time, as fit.
+// Leaves the sums zero.
+template <int CAP, int NT, bool GATED, bool BF16>
+__device__ __forceinline__ void mg_store(const LinearArgs& a, const RowTile& t, mf4 (&acc)[NT][MG_TILES],
+                                         const MgShared<CAP>& m, int n0, const int* s_src) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  constexpr int kSize = BF16 ? 2 : 4;
-  constexpr int kRow = (GATED ? 16 : 32) * kSize;   // bytes of a token
+  constexpr int kSize = BF16 ? 2 : 4, kHalf = GATED ? 2 : 1;
+  constexpr int kPass = GATED || BF16 ? MG_TILES : MG_TILES / 2;
+  constexpr int kRow = 16 * kPass / kHalf * kSize;   // bytes of a token
+  static_assert(2 * 16 * kRow <= MgShared<CAP>::kW && NT % 2 == 0, "a wavefront's piece of LDS");
   constexpr int kPer = kRow / 16;
-  const int width = GATED ? a.N / 2 : a.N;
-  const int col = n0 / (GATED ? 2 : 1);
-  uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + (t.r0 * width + col) * kSize;
+  const int width = a.N / kHalf;
 #pragma unroll
-  for (int i = 0; i < CAP; ++i) {
-    if (i < nt) {
+  for (int i = 0; i < NT; i += 2) {
+#pragma unroll
+    for (int p = 0; p < MG_TILES / kPass; ++p) {
+      const int col = (n0 + 16 * kPass * p) / kHalf;
+      uint8_t* __restrict__ y = static_cast<uint8_t*>(a.y) + (t.r0 * width + col) * kSize;
       mg_wave_sync();
-      const bool has = s_src[16 * i + r] >= 0;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        put_out<GATED, BF16>(m.w + r * kRow + (16 * w + 4 * q) / (GATED ? 2 : 1) * kSize,
-                             has ? acc[i][w] : mf4{0, 0, 0, 0});
-        acc[i][w] = mf4{0, 0, 0, 0};
+      for (int u = 0; u < 2; ++u) {
+        const bool has = s_src[16 * (i + u) + r] >= 0;
+#pragma unroll
+        for (int w = 0; w < kPass; ++w) {
+          put_out<GATED, BF16>(m.w + (16 * u + r) * kRow + (16 * w + 4 * q) / kHalf * kSize,
+                               has ? acc[i + u][kPass * p + w] : mf4{0, 0, 0, 0});
+          acc[i + u][kPass * p + w] = mf4{0, 0, 0, 0};
+        }
       }
       mg_wave_sync();
 #pragma unroll
-      for (int e = lane; e < 16 * kPer; e += 64) {
+      for (int e = lane; e < 32 * kPer; e += 64) {
         const int row = 16 * i + e / kPer, piece = e % kPer;
         const mi4 v = *(const LdsInt4*)(m.w + 16 * e);
         if (row < t.rows && col + piece * (16 / kSize) < width)
-          *reinterpret_cast<mi4*>(y + static_cast<uint32_t>(row * width) * kSize + 16 * piece) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<mi4*>(y + static_cast<uint32_t>(row * width) * kSize + 16 * piece));
       }
     }
   }
 }
 
-template <int CAP, int G, bool GATED, bool BF16>
+// NT: token tiles, at least the tile's rows.
+template <int CAP, int NT, int G, bool GATED, bool BF16>
 __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, MgLane& l, int n0,
                                         const MgShared<CAP>& m, int* s_src) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int r = lane & 15, q = lane >> 4;
-  // opaque, so that no step's first products count as unconditional: the
-  // compiler would move them past the barriers, to where their sums are used
-  int nt = (t.rows + 15) / 16;
-  asm volatile("" : "+s"(nt));
-  mi4 w0[4], w1[4];
-  MgScales<G> sa, sw;
-  MgAt pos = {0, 0, 0}, ahead = {0, 0, 0};
-  const auto load_ahead = [&](mi4 (&w)[4]) {
-    mg_load_w(w, l, ahead.slice, ahead.c);
-    const bool over = ahead.c + 1 == l.steps;
-    ahead.slice += over ? 1 : 0;
-    ahead.c = over ? 0 : ahead.c + 1;
-  };
-  mg_load_s<G>(sw, l.ws, l.wsv, 0);
-  load_ahead(w0);
-  load_ahead(w1);
+  mi4 w[2 * MG_TILES];
+  MgChunk<G> sc;
+  MgAt pos = {0, 0, 0};
+  mg_load_w(w, l, 0, 0);
   // thread tid looks up tile row tid's source; the others take it from LDS
   if (tid < 16 * CAP) {
     bool ok = false;
@@ -603,7 +637,7 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
   __syncthreads();
   // the row pieces this lane moves: tile row 8 (4 j + wave) + lane / 8
 #pragma unroll
-  for (int j = 0; j < CAP / 2; ++j) {
+  for (int j = 0; j < (NT + 1) / 2; ++j) {
     const int row = 8 * (4 * j + l.wave) + (lane >> 3);
     const int v = s_src[row];
     l.av[j] = row < t.rows ? static_cast<uint32_t>(v < 0 ? ~v : v) * (a.K / 2) + 16 * ((lane & 7) ^ mg_swz(row & 15))
@@ -616,43 +650,38 @@ __device__ __forceinline__ void mg_tile(const LinearArgs& a, const RowTile& t, M
   }
   const MgRead at = {r * 128 + 16 * ((2 * q) ^ mg_swz(r)), r * 128 + 16 * ((2 * q + 1) ^ mg_swz(r)),
                      r * (8 * MG_CHUNK) + 2 * q};
-  mf4 acc[CAP][2] = {};
-  mg_load_s<G>(sa, l.as, l.asv, 0);
-  mg_load_a<CAP>(l, m.a[0], 0);
-  mg_put_chunk<CAP, G>(m, l, sa, sw, 0, 0);
+  mf4 acc[NT][MG_TILES] = {};
+  mg_load_chunk<G>(sc, l, 0, 0);
+  mg_load_a<NT>(l, m.a[0], 0);
+  mg_put_chunk<CAP, G>(m, l, sc, 0, 0);
   mg_barrier<0>();
-  // the weights of the first step become operands; those of the next two are
-  // in w1 and on their way into w0
-  mg_write_w<G, CAP>(w0, m, l, 0);
-  load_ahead(w0);
-  MgPair wp = mg_read_w(m, at, 0, 0);
   const int total = l.slices * l.steps;
   int done = 0;   // slices stored
   for (int v = 0; v + 2 <= total; v += 2) {
-    mg_step<CAP, G, 0, false>(acc, m, l, at, nt, pos, ahead, w1, wp, sa, sw);
-    if (pos.slice > done) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, nt, s_src);
-    mg_step<CAP, G, 1, false>(acc, m, l, at, nt, pos, ahead, w0, wp, sa, sw);
-    if (pos.slice > done) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, nt, s_src);
+    mg_step<CAP, NT, G, 0, false>(acc, m, l, at, pos, w, sc);
+    if (pos.slice > done) mg_store<CAP, NT, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, s_src);
+    mg_step<CAP, NT, G, 1, false>(acc, m, l, at, pos, w, sc);
+    if (pos.slice > done) mg_store<CAP, NT, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done++, s_src);
   }
-  if (total & 1) mg_step<CAP, G, 0, true>(acc, m, l, at, nt, pos, ahead, w1, wp, sa, sw);
+  if (total & 1) mg_step<CAP, NT, G, 0, true>(acc, m, l, at, pos, w, sc);
   __builtin_amdgcn_s_waitcnt(0x0F70);   // a load still on its way to LDS may not outlive the workgroup
-  if (done < l.slices) mg_store<CAP, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done, nt, s_src);
+  if (done < l.slices) mg_store<CAP, NT, GATED, BF16>(a, t, acc, m, n0 + MG_ROWS * done, s_src);
 }
 
 // slices: of MG_ROWS weight rows, one after the other, per workgroup.
 template <int CAP, int G, bool GATED, bool BF16>
-__global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups_kernel(LinearArgs a,
+__global__ __launch_bounds__(ML_THREADS, 2) void mx_linear_groups_kernel(LinearArgs a,
                                                                                        int slices) {
   typedef MgShared<CAP> M;
   __shared__ __align__(16) uint8_t s_a0[CAP * 2048], s_a1[CAP * 2048];
-  __shared__ __align__(16) uint8_t s_w[4 * 4096];
+  __shared__ __align__(16) uint8_t s_w[4 * M::kW];
   __shared__ __align__(16) uint8_t s_sa[2 * M::kSa], s_sw[4 * 2 * M::kSw];
   __shared__ int s_src[CAP * 16];   // each row's source, complemented where it has none
-  // XCD x (workgroups go to the 8 XCDs in turn) takes row tiles x, x + 8, ...
-  // with all their column slices, so a tile's token rows meet in one L2
+  // workgroups go to the 8 XCDs in turn; an XCD takes all slices of a tile, so
+  // that the tile's token rows meet in its L2, then the next tile's
   const int n_slices = (a.N + MG_ROWS - 1) / MG_ROWS, n_wg = (n_slices + slices - 1) / slices;
   const int i = static_cast<int>(blockIdx.x) >> 3;
-  const RowTile t = find_row_tile(a, 8 * (i / n_wg) + (static_cast<int>(blockIdx.x) & 7), 16 * CAP);
+  const RowTile t = find_row_tile(a, static_cast<int>(blockIdx.x) & 7, i / n_wg, 16 * CAP);
   if (t.rows <= 0) return;
   const int s0 = i % n_wg * slices, n0 = s0 * MG_ROWS;
   const int lane = threadIdx.x & 63;
@@ -662,19 +691,28 @@ __global__ __launch_bounds__(ML_THREADS, CAP == 8 ? 2 : 3) void mx_linear_groups
   l.nb = nb;
   l.steps = (a.K + MG_STEP - 1) / MG_STEP;
   l.slices = min(slices, n_slices - s0);
+  l.stream = t.whole;
   l.ac = mg_rsrc(a.ac, a.a_rows * crow);
   l.as = mg_rsrc(a.as, a.a_rows * nb);
   const int64_t wrow = static_cast<int64_t>(t.g) * a.N;
   l.wc = mg_rsrc(a.wc + wrow * crow, static_cast<int64_t>(a.N) * crow);
   l.ws = mg_rsrc(a.ws + wrow * nb, static_cast<int64_t>(a.N) * nb);
-  l.wv = static_cast<uint32_t>((n0 + 32 * l.wave + (lane >> 3)) * crow + 16 * (lane & 7));
-  l.wsv = static_cast<uint32_t>((n0 + 32 * l.wave + (lane >> 1)) * nb + 16 * (lane & 1));
+  const int wave0 = n0 + 16 * MG_TILES * l.wave;   // the wavefront's first weight row
+  l.wv = static_cast<uint32_t>((wave0 + (lane >> 3)) * crow + 16 * (lane & 7));
+  l.wsv = static_cast<uint32_t>((wave0 + (lane >> 1)) * nb + 16 * (lane & 1));
+  l.ws32 = 32 * nb;
   l.w8 = 8 * crow;
   l.wslice = MG_ROWS * crow;
   l.wsslice = MG_ROWS * nb;
-  const M m = {{(LdsByte*)s_a0, (LdsByte*)s_a1}, (LdsByte*)s_w + 4096 * l.wave, (LdsByte*)s_sa,
+  const M m = {{(LdsByte*)s_a0, (LdsByte*)s_a1}, (LdsByte*)s_w + M::kW * l.wave, (LdsByte*)s_sa,
                (LdsByte*)s_sw + 2 * M::kSw * l.wave};
-  mg_tile<CAP, G, GATED, BF16>(a, t, l, n0 + 32 * l.wave, m, s_src);
+  const int nt = (t.rows + 15) / 16;
+  if constexpr (CAP >= 8) {
+    if (nt > 6) return mg_tile<CAP, 8, G, GATED, BF16>(a, t, l, wave0, m, s_src);
+    if (nt > 4) return mg_tile<CAP, 6, G, GATED, BF16>(a, t, l, wave0, m, s_src);
+  }
+  if (nt > 2) return mg_tile<CAP, 4, G, GATED, BF16>(a, t, l, wave0, m, s_src);
+  mg_tile<CAP, 2, G, GATED, BF16>(a, t, l, wave0, m, s_src);
 }
 
 template <int CAP, bool GATED, bool BF16>
@@ -683,10 +721,11 @@ void launch_groups(const LinearArgs& a, hipStream_t s) {
   const int64_t tiles = a.offsets ? a.R / m + min(static_cast<int64_t>(a.G), a.R) : (a.R + m - 1) / m;
   const int64_t n_slices = (a.N + MG_ROWS - 1) / MG_ROWS;
   // A workgroup's start (its tile, its rows' sources, the first loads) costs as
-  // much as a third of a slice of 2,048 columns; up to four slices share it
-  // where enough workgroups are left to even out the end.
+  // much as a third of a slice of 2,048 columns; two slices share it
+  // where enough workgroups are left to even out the end (four: slower, the
+  // token rows of the workgroups under way no longer fit the L2s).
   const int64_t want = int64_t{8} * device_cus();
-  const int slices = static_cast<int>(min(max(tiles * n_slices / want, int64_t{1}), min(int64_t{4}, n_slices)));
+  const int slices = static_cast<int>(min(max(tiles * n_slices / want, int64_t{1}), min(int64_t{2}, n_slices)));
   const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8 * ((n_slices + slices - 1) / slices));
   const int nb = a.K / 32;
   if (nb % 8 == 0)
@@ -711,10 +750,8 @@ void launch_product(const LinearArgs& a, hipStream_t s) {
   const int64_t avg = a.R / a.G;
   if (avg < 16 || a.a_rows * (a.K / 2) >= int64_t{MG_OUT})   // the other kernel has 32-bit offsets into A
     launch_rows<GATED, BF16>(a, s);
-  else if (avg > 32)
-    launch_groups<8, GATED, BF16>(a, s);
   else
-    launch_groups<4, GATED, BF16>(a, s);
+    launch_groups<8, GATED, BF16>(a, s);
 }
 
 }  // namespace
