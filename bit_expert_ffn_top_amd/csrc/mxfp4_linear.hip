@@ -747,11 +747,15 @@ void launch_rows(const LinearArgs& a, hipStream_t s) {
 
 template <bool GATED, bool BF16>
 void launch_product(const LinearArgs& a, hipStream_t s) {
-  const int64_t avg = a.R / a.G;
-  if (avg < 16 || a.a_rows * (a.K / 2) >= int64_t{MG_OUT})   // the other kernel has 32-bit offsets into A
-    launch_rows<GATED, BF16>(a, s);
-  else
+  // The kernel for full tiles wherever it has two workgroups for every CU, also
+  // where its tiles are mostly empty: reading the weights is what counts then,
+  // and it reads them better.  Its offsets into A have 32 bits.
+  const int64_t wgs = (a.offsets ? a.R / 128 + min(static_cast<int64_t>(a.G), a.R) : (a.R + 127) / 128) *
+                      ((a.N + MG_ROWS - 1) / MG_ROWS);
+  if (wgs >= 2 * device_cus() && a.a_rows * (a.K / 2) < int64_t{MG_OUT})
     launch_groups<8, GATED, BF16>(a, s);
+  else
+    launch_rows<GATED, BF16>(a, s);
 }
 
 }  // namespace

@@ -72,12 +72,12 @@ def product(a, w, offsets=None, src=None):
     y, mag, covered = np.zeros((R, N)), np.zeros((R, N)), np.zeros(R, bool)
     bounds = [0, R] if offsets is None else list(offsets)
     for g in range(w.shape[0]):
-        for r in range(bounds[g], bounds[g + 1]):
-            covered[r] = True
-            s = r if src is None else src[r]
-            if 0 <= s < a.shape[0]:
-                y[r] = w[g] @ a[s]
-                mag[r] = np.abs(w[g]) @ np.abs(a[s])
+        rows = np.arange(bounds[g], bounds[g + 1])
+        covered[rows] = True
+        from_a = rows if src is None else np.asarray(src)[rows]
+        here = (from_a >= 0) & (from_a < a.shape[0])
+        y[rows[here]] = a[from_a[here]] @ w[g].T
+        mag[rows[here]] = np.abs(a[from_a[here]]) @ np.abs(w[g].T)
     return y, mag, covered
 
 

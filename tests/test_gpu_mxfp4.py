@@ -200,6 +200,44 @@ def test_linear_grouped(M, R, G, N, K, dtype):
     _close(y, ref, mag, K, dtype)
 
 
+WIDE = [  # enough row tiles and columns for the kernel of full tiles: M, R, G, N, K
+    (40, 1300, 600, 272, 160), (50, 900, 512, 528, 288), (31, 700, 530, 512, 640), (64, 640, 640, 400, 704),
+    (9, 1200, 520, 256, 1280), (77, 5000, 300, 512, 256), (200, 3000, 3, 8448, 64), (1300, 1300, 1, 12032, 96),
+    (1000, 1000, 2, 16640, 512), (20, 530, 530, 256, 2304),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,R,G,N,K", WIDE, ids=[f"M{c[0]}_R{c[1]}_G{c[2]}_N{c[3]}_K{c[4]}" for c in WIDE])
+def test_wide_products(M, R, G, N, K, dtype):
+    """Groups of one row and of thousands, several tiles to a group, a last
+    step and a last chunk of scales that a row ends inside; both products."""
+    bf = _bf()
+    dev = need_gpu()
+    rng = np.random.default_rng(M + R + G + N + K)
+    ac, as_, av = _rand_mx(rng, M, K, lo=122, hi=127)
+    wc, ws, wv = _rand_mx(rng, G, N, K, lo=118, hi=123)
+    used = R - 3
+    off = _bounds(rng, used, G)
+    src = rng.integers(0, 2 * M, R)
+    src[1], src[used - 1] = -1, 2 * M
+    gather = (_i32(off), _i32(src), 2)
+    ref, mag, cov = mx.product(av, wv, off, np.where(src < 0, -1, src // 2))
+    y = torch.full((R, N), 7.0, dtype=dtype, device=dev)
+    bf.mxfp4_linear(_dev(ac, as_), _dev(wc, ws), *gather, y=y)
+    assert (y[used:] == 7).all() and not cov[used:].any()
+    _close(y[:used], ref[:used], mag[:used], K, dtype)
+    h = torch.full((R, N // 2), 7.0, dtype=dtype, device=dev)
+    if N % 64 == 0:
+        bf.mxfp4_gate_up(_dev(ac, as_), _dev(wc, ws), *gather, h=h)
+        g, u, d = ref[:used, 0::2], ref[:used, 1::2], 2 * K * U * mag[:used]
+        want = mx.silu(g) * u
+        bound = _silu_bound(g, u, d[:, 0::2], d[:, 1::2])
+        bound += HALF_STEP[dtype] * (np.abs(want) + bound) + 1e-40
+        assert (np.abs(_np(h[:used]) - want) <= bound).all()
+        assert (h[used:] == 7).all()
+
+
 def _silu_bound(g, u, dg, du):
     """|silu(g') u' - silu(g) u| for g', u' off by dg, du: |silu'| <= 1.1 and
     |silu(z)| <= |z|; the function itself and the product in fp32 add 8 u."""
