@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 from typing import NamedTuple, Optional
 
@@ -699,45 +700,44 @@ def combine(x, rows, pair_pos, w, shared=None, y=None, stream=None):
 
 # --- microscaled 4-bit floats and the router's losses ---------------------------
 #
-# These calls run on the device of their tensors (which must be one device)
-# and, for outputs and workspaces that they allocate, on the memory of the
-# stream they are given, so that a buffer handed back there is not used
-# elsewhere before the call is done with it.
+# These calls run on the device of their tensors (which must be one device);
+# outputs and workspaces that they allocate come from the memory of the stream
+# they are given, so that a buffer given back there is not used elsewhere before
+# the call is done with it.
 
 
-class _On:
-    """The device of the tensors (all the same one) and the stream of a call,
-    made current for its allocations and launches.  A stream of another device
-    is refused."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, what, stream, **tensors):
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
+
+def _same_device(what, tensors):
+    """The device of the tensors (None entries passed over), which must be one."""
+    dev = None
+    for t in tensors:
+        if t is not None:
             if dev is None:
                 dev = t.device
             elif t.device != dev:
-                raise ValueError(f"{what}: {name} is on {t.device}, the other tensors on {dev}")
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-        if self.stream.device != dev:
-            raise ValueError(f"{what}: the stream belongs to {self.stream.device}, the tensors to {dev}")
-        self.device = dev
-        self._ctx = None if stream is None and dev.index == torch.cuda.current_device() \
-            else torch.cuda.stream(self.stream)
+                raise ValueError(f"{what}: tensors on {dev} and {t.device}, one device expected")
+    return dev
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+def _on_stream(fn):
+    """For fn(dev, handle, ...) -> run(what, stream, tensors, ...): the tensors'
+    one device and the handle of the stream (the device's current one if None),
+    with both current while fn allocates and launches.  A stream of another
+    device is refused."""
+    def run(what, stream, tensors, *args):
+        dev = _same_device(what, tensors)
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(dev, _raw_stream(dev.index), *args)
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream() if stream is None else stream
+            if s.device != dev:
+                raise ValueError(f"{what}: the stream belongs to {s.device}, the tensors to {dev}")
+            with torch.cuda.stream(s):
+                return fn(dev, s.cuda_stream, *args)
+    return run
 
 
 def _float_dtype(dtype, name):
@@ -748,10 +748,17 @@ def _float_dtype(dtype, name):
     raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
 
 
-def _ws(need, ws, device):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(need, ws, dev):
+    """(address, bytes, tensor to keep until the launch) of a workspace."""
     if ws is None:
-        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
-    return _dev(ws, torch.uint8, "ws")
+        if need == 0:
+            return None, 0, None
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 @dataclasses.dataclass
@@ -792,6 +799,20 @@ def group_workspace_bytes(T: int, E: int) -> int:
     return int(lib().moe_group_workspace_bytes(T, E))
 
 
+@_on_stream
+def _group_pairs(dev, stream, idx, T, k, E, offsets, pair_pos, row_pair, ws):
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    if pair_pos is None:
+        pair_pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if row_pair is None:
+        row_pair = torch.empty((T * k,), dtype=torch.int32, device=dev)
+    wp, wn, keep = _scratch(group_workspace_bytes(T, E), ws, dev)
+    _check(lib().moe_group_pairs(idx.data_ptr(), T, k, E, offsets.data_ptr(), pair_pos.data_ptr(),
+                                 row_pair.data_ptr(), wp, wn, stream), "moe_group_pairs")
+    return offsets, pair_pos, row_pair
+
+
 def group_pairs(idx, n_experts, offsets=None, pair_pos=None, row_pair=None, ws=None, stream=None):
     """Group the pairs of idx [T, k] by expert (moe_group_pairs).
     Returns (offsets [E + 1], pair_pos [T, k], row_pair [T * k])."""
@@ -803,17 +824,20 @@ def group_pairs(idx, n_experts, offsets=None, pair_pos=None, row_pair=None, ws=N
         if t is not None:
             _dev(_shape(t, shp, name), torch.int32, name)
     _dev(idx, torch.int32, "idx")
-    with _On("group_pairs", stream, idx=idx, offsets=offsets, pair_pos=pair_pos, row_pair=row_pair,
-             ws=ws) as on:
-        i32 = dict(dtype=torch.int32, device=on.device)
-        offsets = torch.empty((E + 1,), **i32) if offsets is None else offsets
-        pair_pos = torch.empty((T, k), **i32) if pair_pos is None else pair_pos
-        row_pair = torch.empty((T * k,), **i32) if row_pair is None else row_pair
-        ws = _ws(group_workspace_bytes(T, E), ws, on.device)
-        _check(lib().moe_group_pairs(_ptr(idx), T, k, E, _ptr(offsets), _ptr(pair_pos),
-                                     _ptr(row_pair), _ptr(ws), ws.numel(), on.handle),
-               "moe_group_pairs")
-    return offsets, pair_pos, row_pair
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
+    return _group_pairs("group_pairs", stream, (idx, offsets, pair_pos, row_pair, ws),
+                        idx, T, k, E, offsets, pair_pos, row_pair, ws)
+
+
+@_on_stream
+def _quantize(dev, stream, x, dtype, lead, cols, out):
+    if out is None:
+        out = Mxfp4(torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=dev),
+                    torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=dev))
+    _check(lib().moe_mxfp4_quantize(x.data_ptr(), dtype, math.prod(lead), cols, out.codes.data_ptr(),
+                                    out.scales.data_ptr(), stream), "moe_mxfp4_quantize")
+    return out
 
 
 def mxfp4_quantize(x, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
@@ -831,14 +855,18 @@ def mxfp4_quantize(x, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
         _shape(out.scales, lead + (cols // 32,), "out.scales")
         out.on_device("out")
     _dev(x, x.dtype, "x")
-    with _On("mxfp4_quantize", stream, x=x, codes=out and out.codes, scales=out and out.scales) as on:
-        if out is None:
-            out = Mxfp4(torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=on.device),
-                        torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=on.device))
-        rows = x.numel() // cols if cols else 0
-        _check(lib().moe_mxfp4_quantize(_ptr(x), dtype, rows, cols, _ptr(out.codes),
-                                        _ptr(out.scales), on.handle), "moe_mxfp4_quantize")
-    return out
+    return _quantize("mxfp4_quantize", stream,
+                     (x,) if out is None else (x, out.codes, out.scales), x, dtype, lead, cols, out)
+
+
+@_on_stream
+def _dequantize(dev, stream, q, shape, y, dtype, y_dtype):
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=dev)
+    _check(lib().moe_mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), math.prod(shape[:-1]),
+                                      shape[-1], y.data_ptr(), y_dtype, stream),
+           "moe_mxfp4_dequantize")
+    return y
 
 
 def mxfp4_dequantize(q: Mxfp4, dtype=torch.float32, y=None, stream=None):
@@ -850,12 +878,16 @@ def mxfp4_dequantize(q: Mxfp4, dtype=torch.float32, y=None, stream=None):
     if y is not None:
         _dev(_shape(y, shape, "y"), y.dtype, "y")
     q.on_device("q")
-    with _On("mxfp4_dequantize", stream, codes=q.codes, scales=q.scales, y=y) as on:
-        if y is None:
-            y = torch.empty(shape, dtype=dtype, device=on.device)
-        rows = y.numel() // shape[-1] if shape[-1] else 0
-        _check(lib().moe_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), rows, shape[-1], _ptr(y),
-                                          y_dtype, on.handle), "moe_mxfp4_dequantize")
+    return _dequantize("mxfp4_dequantize", stream, (q.codes, q.scales, y), q, shape, y, dtype, y_dtype)
+
+
+@_on_stream
+def _product(dev, stream, name, a, w, offsets, row_src, src_div, R, n_out, y, dtype, y_dtype):
+    if y is None:
+        y = torch.empty((R, n_out), dtype=dtype, device=dev)
+    A, W = a.c_struct(), w.c_struct()
+    _check(getattr(lib(), name)(ctypes.byref(A), ctypes.byref(W), _addr(offsets), _addr(row_src),
+                                int(src_div), R, y.data_ptr(), y_dtype, stream), name)
     return y
 
 
@@ -881,20 +913,14 @@ def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
     y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
     if y is not None:
         _dev(_shape(y, (R, n_out), "y"), y.dtype, "y")
-    for t, name in ((offsets, "offsets"), (row_src, "row_src")):
-        if t is not None:
-            _dev(t, torch.int32, name)
+    if offsets is not None:
+        _dev(offsets, torch.int32, "offsets")
+    if row_src is not None:
+        _dev(row_src, torch.int32, "row_src")
     a.on_device("a")
     w.on_device("w")
-    with _On(what, stream, a=a.codes, a_scales=a.scales, w=w.codes, w_scales=w.scales,
-             offsets=offsets, row_src=row_src, y=y) as on:
-        if y is None:
-            y = torch.empty((R, n_out), dtype=dtype, device=on.device)
-        A, W = a.c_struct(), w.c_struct()
-        fn = lib().moe_mxfp4_gate_up if gated else lib().moe_mxfp4_linear
-        _check(fn(ctypes.byref(A), ctypes.byref(W), _ptr(offsets), _ptr(row_src), int(src_div), R,
-                  _ptr(y), y_dtype, on.handle), f"moe_{what}")
-    return y
+    return _product(what, stream, (a.codes, a.scales, w.codes, w.scales, offsets, row_src, y),
+                    f"moe_{what}", a, w, offsets, row_src, src_div, R, n_out, y, dtype, y_dtype)
 
 
 def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=None,
@@ -920,6 +946,18 @@ def mxfp4_ffn_decode_workspace_bytes(T: int, k: int, d_ff: int) -> int:
     return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, d_ff))
 
 
+@_on_stream
+def _mx_decode(dev, stream, gate_up, down, shared_slot, x, T, d, k, f, slot, w, y, ws):
+    if y is None:
+        y = torch.empty((T, d), dtype=torch.float32, device=dev)
+    wp, wn, keep = _scratch(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, f), ws, dev)
+    GU, D = gate_up.c_struct(), down.c_struct()
+    _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), int(shared_slot),
+                                      x.data_ptr(), T, k, slot.data_ptr(), w.data_ptr(),
+                                      y.data_ptr(), wp, wn, stream), "moe_mxfp4_ffn_decode")
+    return y
+
+
 def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=None, ws=None,
                      stream=None):
     """Decode / verify FFN of T = 1..4 tokens over 4-bit experts
@@ -937,22 +975,16 @@ def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=
     _shape(w, (T, k), "w")
     if y is not None:
         _dev(_shape(y, (T, d), "y"), torch.float32, "y")
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
     _dev(x, torch.float32, "x")
     _dev(slot, torch.int32, "slot")
     _dev(w, torch.float32, "w")
     gate_up.on_device("gate_up")
     down.on_device("down")
-    with _On("mxfp4_ffn_decode", stream, x=x, slot=slot, w=w, gate_up=gate_up.codes,
-             gate_up_scales=gate_up.scales, down=down.codes, down_scales=down.scales, y=y,
-             ws=ws) as on:
-        if y is None:
-            y = torch.empty((T, d), dtype=torch.float32, device=on.device)
-        ws = _ws(mxfp4_ffn_decode_workspace_bytes(T, k, f2 // 2), ws, on.device)
-        GU, D = gate_up.c_struct(), down.c_struct()
-        _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), int(shared_slot),
-                                          _ptr(x), T, k, _ptr(slot), _ptr(w), _ptr(y), _ptr(ws),
-                                          ws.numel(), on.handle), "moe_mxfp4_ffn_decode")
-    return y
+    return _mx_decode("mxfp4_ffn_decode", stream,
+                      (x, slot, w, gate_up.codes, gate_up.scales, down.codes, down.scales, y, ws),
+                      gate_up, down, shared_slot, x, T, d, k, f2 // 2, slot, w, y, ws)
 
 
 class RouteBalance(NamedTuple):
@@ -990,6 +1022,22 @@ def route_balance_workspace_bytes(T: int, E: int, n_seq: int) -> int:
     return int(lib().moe_route_balance_workspace_bytes(T, E, n_seq))
 
 
+@_on_stream
+def _route_balance(dev, stream, logits, idx, T, E, k, seq_offsets, S, mask, out, ws):
+    if out is None:
+        f32, i32 = torch.float32, torch.int32
+        out = RouteBalance(torch.empty((S,), dtype=f32, device=dev), torch.empty((S,), dtype=f32, device=dev),
+                           torch.empty((S, E), dtype=i32, device=dev),
+                           torch.empty((S, E), dtype=f32, device=dev), torch.empty((S,), dtype=i32, device=dev))
+    wp, wn, keep = _scratch(lib().moe_route_balance_workspace_bytes(T, E, S), ws, dev)
+    balance, z, counts, prob_sum, n_tokens = out
+    _check(lib().moe_route_balance(logits.data_ptr(), idx.data_ptr(), T, E, k, _addr(seq_offsets), S,
+                                   _addr(mask), balance.data_ptr(), z.data_ptr(), counts.data_ptr(),
+                                   prob_sum.data_ptr(), n_tokens.data_ptr(), wp, wn, stream),
+           "moe_route_balance")
+    return out
+
+
 def route_balance(logits, idx, seq_offsets=None, mask=None, out: Optional[RouteBalance] = None,
                   ws=None, stream=None) -> RouteBalance:
     """The router's balance and z losses, per-expert counts and probability
@@ -997,20 +1045,27 @@ def route_balance(logits, idx, seq_offsets=None, mask=None, out: Optional[RouteB
     [T, k], seq_offsets int32 [S + 1] (None: one sequence of all rows), mask
     uint8 or bool [T] (0: the row takes no part)."""
     T, E, k, S = _balance_args(logits, idx, seq_offsets, mask)
-    want = (((S,), torch.float32), ((S,), torch.float32), ((S, E), torch.int32),
-            ((S, E), torch.float32), ((S,), torch.int32))
     if out is not None:
+        want = (((S,), torch.float32), ((S,), torch.float32), ((S, E), torch.int32),
+                ((S, E), torch.float32), ((S,), torch.int32))
         for t, (shp, dt), name in zip(out, want, RouteBalance._fields):
             _dev(_shape(t, shp, name), dt, name)
-    with _On("route_balance", stream, logits=logits, idx=idx, seq_offsets=seq_offsets, mask=mask,
-             ws=ws, **(out._asdict() if out is not None else {})) as on:
-        if out is None:
-            out = RouteBalance(*(torch.empty(shp, dtype=dt, device=on.device) for shp, dt in want))
-        ws = _ws(route_balance_workspace_bytes(T, E, S), ws, on.device)
-        _check(lib().moe_route_balance(_ptr(logits), _ptr(idx), T, E, k, _ptr(seq_offsets), S,
-                                       _ptr(mask), *(_ptr(t) for t in out), _ptr(ws), ws.numel(),
-                                       on.handle), "moe_route_balance")
-    return out
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
+    return _route_balance("route_balance", stream, (logits, idx, seq_offsets, mask, ws) + (out or ()),
+                          logits, idx, T, E, k, seq_offsets, S, mask, out, ws)
+
+
+@_on_stream
+def _route_backward(dev, stream, logits, idx, T, E, k, seq_offsets, S, mask, counts, n_tokens,
+                    g_balance, g_z, w, dw, dlogits):
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _check(lib().moe_route_backward(logits.data_ptr(), idx.data_ptr(), T, E, k, _addr(seq_offsets), S,
+                                    _addr(mask), _addr(counts), _addr(n_tokens), _addr(g_balance),
+                                    _addr(g_z), _addr(w), _addr(dw), dlogits.data_ptr(), stream),
+           "moe_route_backward")
+    return dlogits
 
 
 def route_backward(logits, idx, counts=None, n_tokens=None, g_balance=None, g_z=None, w=None,
@@ -1027,13 +1082,7 @@ def route_backward(logits, idx, counts=None, n_tokens=None, g_balance=None, g_z=
     for t, shp, dt, name in checks:
         if t is not None:
             _dev(_shape(t, shp, name), dt, name)
-    with _On("route_backward", stream, logits=logits, idx=idx, counts=counts, n_tokens=n_tokens,
-             g_balance=g_balance, g_z=g_z, w=w, dw=dw, seq_offsets=seq_offsets, mask=mask,
-             dlogits=dlogits) as on:
-        if dlogits is None:
-            dlogits = torch.empty((T, E), dtype=torch.float32, device=on.device)
-        _check(lib().moe_route_backward(_ptr(logits), _ptr(idx), T, E, k, _ptr(seq_offsets), S,
-                                        _ptr(mask), _ptr(counts), _ptr(n_tokens), _ptr(g_balance),
-                                        _ptr(g_z), _ptr(w), _ptr(dw), _ptr(dlogits), on.handle),
-               "moe_route_backward")
-    return dlogits
+    return _route_backward("route_backward", stream,
+                           (logits, idx, seq_offsets, mask, counts, n_tokens, g_balance, g_z, w, dw, dlogits),
+                           logits, idx, T, E, k, seq_offsets, S, mask, counts, n_tokens, g_balance, g_z,
+                           w, dw, dlogits)

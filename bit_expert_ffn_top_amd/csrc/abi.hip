@@ -615,11 +615,12 @@ int moe_route_balance(const float* logits, const int32_t* idx, int T, int E, int
                       size_t ws_bytes, hipStream_t stream) {
   const int st = check_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask);
   if (st != MOE_OK) return st;
-  if (!balance || !z || !counts || !prob_sum || !n_tokens || !ws) return MOE_EINVAL;
+  const size_t need = bitffn::route_balance_workspace_bytes(T, E, n_seq);
+  if (!balance || !z || !counts || !prob_sum || !n_tokens || (need > 0 && !ws)) return MOE_EINVAL;
   if (!aligned16(balance) || !aligned16(z) || !aligned16(counts) || !aligned16(prob_sum) ||
-      !aligned16(n_tokens) || !aligned256(ws))
+      !aligned16(n_tokens) || (need > 0 && !aligned256(ws)))
     return MOE_EALIGN;
-  if (ws_bytes < bitffn::route_balance_workspace_bytes(T, E, n_seq)) return MOE_ENOSPC;
+  if (ws_bytes < need) return MOE_ENOSPC;
   return hip_status(bitffn::launch_route_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask,
                                                  balance, z, counts, prob_sum, n_tokens, ws,
                                                  stream));

@@ -13,8 +13,8 @@
 // sequence s meet in at most one run of rows, and along the rows c + s only
 // grows, so c + s numbers the partial results without gaps to search.  The
 // second launch adds a sequence's partials chunk by chunk; the workgroup that
-// finishes a sequence last adds up its loss in expert order.  Nothing depends
-// on which that is.
+// finishes a sequence last adds up its loss, in a fixed order: nothing depends on
+// which that is.
 // Backward, one launch: a wavefront takes runs of consecutive rows, the
 // coefficients of their sequence in registers.
 // Bound: HBM (the logits once; the gradient written once).
@@ -63,28 +63,55 @@ __device__ __forceinline__ int seq_bound(const int32_t* seq, int s, int S, int T
 }
 
 // The sequence of row t: the last s with bound(s) <= t (empty ones before it
-// are passed over), -1 before the first; S where t lies past the last.
+// are passed over), -1 before the first; S where t lies past the last.  All 64
+// lanes of a wavefront, which asks for 64 bounds at a time.
 __device__ __forceinline__ int seq_of_row(const int32_t* seq, int S, int T, int t) {
-  int lo = 0, hi = S + 1;   // bounds 0..S: how many are <= t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_bound(seq, mid, S, T) <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = S + 1;   // bounds lo .. lo + n - 1 may be <= t, all before are
+  while (n > 64) {
+    const int step = (n + 63) / 64;
+    const int at = lo + lane * step;
+    const bool below = lane * step < n && seq_bound(seq, at, S, T) <= t;
+    const int k = __popcll(__ballot(below));   // pivots 0 .. k - 1
+    if (k == 0) return lo - 1;
+    const int end = lo + n;
+    lo += (k - 1) * step;
+    n = min(step, end - lo);
   }
-  return lo - 1;
+  const bool below = lane < n && seq_bound(seq, lo + lane, S, T) <= t;
+  return __builtin_amdgcn_readfirstlane(lo + __popcll(__ballot(below)) - 1);
 }
 
+// Sum and maximum over a wavefront, the same in every lane: the rows of 16
+// lanes by lane permutes inside the vector unit, then the four of them.
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  v = row16_sum_dpp(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                      0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false)));
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-  return v;
+  v = max_dpp<0xB1>(v);    // quad_perm [1,0,3,2]
+  v = max_dpp<0x4E>(v);    // quad_perm [2,3,0,1]
+  v = max_dpp<0x124>(v);   // row_ror:4
+  v = max_dpp<0x128>(v);   // row_ror:8
+  return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+}
+
+// e^d for d <= 0.  The product with log2(e) is carried in two parts, so the
+// result is good to about 2 units in the last place for every d (the hardware's
+// exponential to 1); below -126 it is 0.
+__device__ __forceinline__ float exp_hw(float d) {
+  d = fmaxf(d, -126.0f);
+  const float t = d * 1.44269502f;                                 // log2(e), rounded
+  const float lo = fmaf(d, 1.44269502f, -t) + d * 1.92596303e-8f;   // what both roundings lost
+  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182f, 1.0f);
 }
 
 // Orders this wavefront's LDS accesses for its own lanes (one wavefront's LDS
@@ -134,7 +161,7 @@ struct Row {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float d = v[c][j] == m ? 0.0f : v[c][j] - m;
-        v[c][j] = VEC * (64 * c + lane) < E ? expf(d) : 0.0f;
+        v[c][j] = VEC * (64 * c + lane) < E ? exp_hw(d) : 0.0f;
         sum += v[c][j];
       }
     sum = wave_sum(sum);
@@ -180,10 +207,21 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
     float acc[NC][VEC] = {};
     float zs = 0.0f;
     int n = 0;
+    // the next row is on its way while one is worked on
+    Row<VEC, NC> r, ahead;
+    bool part = false;
+    if (b0 + wave < b1) {
+      ahead.load(a.logits + static_cast<int64_t>(b0 + wave) * E, E, lane);
+      part = !a.mask || a.mask[b0 + wave] != 0;
+    }
     for (int t = b0 + wave; t < b1; t += RB_WAVES) {
-      if (a.mask && !a.mask[t]) continue;
-      Row<VEC, NC> r;
-      r.load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+      r = ahead;
+      const bool now = part;
+      if (t + RB_WAVES < b1) {
+        ahead.load(a.logits + static_cast<int64_t>(t + RB_WAVES) * E, E, lane);
+        part = !a.mask || a.mask[t + RB_WAVES] != 0;
+      }
+      if (!now) continue;
       float lse;
       const float inv = 1.0f / r.exps(E, lane, lse);
 #pragma unroll
@@ -316,13 +354,13 @@ __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(Bala
   zs = wave_sum(zs);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, 64);
-  if (threadIdx.x == 0) {
-    double l = 0.0;
-    for (int i = 0; i < a.n_etiles; ++i)
-      l += __hip_atomic_load(&a.l_part[static_cast<int64_t>(s) * a.n_etiles + i], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-    write_losses(a, s, n, l, zs);
-  }
+  double l = 0.0;   // at most 32 tiles: a lane each
+  if (static_cast<int>(threadIdx.x) < a.n_etiles)
+    l = __hip_atomic_load(&a.l_part[static_cast<int64_t>(s) * a.n_etiles + threadIdx.x], __ATOMIC_RELAXED,
+                          __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+  if (threadIdx.x == 0) write_losses(a, s, n, l, zs);
 }
 
 // ---------------------------------------------------------------------------
@@ -345,6 +383,11 @@ struct BackwardArgs {
   int T, E, k, S, rows;   // rows: consecutive rows per wavefront
 };
 
+struct Pair {   // lane i: pair i of a row
+  int e;
+  float w, dw;
+};
+
 template <int VEC, int NC>
 __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardArgs a) {
   extern __shared__ float lds[];
@@ -364,13 +407,30 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
   float cc[NC][VEC] = {};   // counts of the sequence less their mean
   float kb = 0.0f, kz = 0.0f;
   int loaded = -2;
+  // the next row and its pairs are on their way while one is worked on
+  Row<VEC, NC> ahead;
+  Pair next = {};
+  bool part_next = false;
+  const bool reads = a.g_balance || a.g_z;
+  const auto request = [&](int t) {
+    part_next = !a.mask || a.mask[t] != 0;
+    if (reads) ahead.load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+    if (routed && lane < a.k) {
+      const int64_t at = static_cast<int64_t>(t) * a.k + lane;
+      next = Pair{a.idx[at], a.w[at], a.dw[at]};
+    }
+  };
+  request(t0);
   for (int t = t0; t < t1; ++t) {
     while (t >= s_end && s < a.S) {
       ++s;
       s_end = s < a.S ? seq_bound(a.seq, s + 1, a.S, a.T) : a.T;
     }
+    Row<VEC, NC> r = ahead;
+    const Pair pair = next;
+    const bool part = s >= 0 && s < a.S && part_next;
+    if (t + 1 < t1) request(t + 1);
     float* __restrict__ out = a.dlogits + static_cast<int64_t>(t) * E;
-    const bool part = s >= 0 && s < a.S && (!a.mask || a.mask[t]);
     float d[NC][VEC] = {};
     if (part) {
       if (s != loaded) {
@@ -393,8 +453,6 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
           }
       }
       if (kb != 0.0f || kz != 0.0f) {
-        Row<VEC, NC> r;
-        r.load(a.logits + static_cast<int64_t>(t) * E, E, lane);
         float lse;
         const float inv = 1.0f / r.exps(E, lane, lse);
         float dot = 0.0f;
@@ -411,11 +469,9 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
       }
       if (routed) {
         const bool mine = lane < a.k;
-        const int64_t at = static_cast<int64_t>(t) * a.k + lane;
-        const int e = mine ? a.idx[at] : -1;
-        const float w = mine ? a.w[at] : 0.0f, dw = mine ? a.dw[at] : 0.0f;
-        const float dot = wave_sum(mine ? w * dw : 0.0f);
-        float v = w * (dw - dot);
+        const int e = mine ? pair.e : -1;
+        const float dot = wave_sum(mine ? pair.w * pair.dw : 0.0f);
+        float v = pair.w * (pair.dw - dot);
         const bool ok = mine && e >= 0 && e < E;
         // equal ids in the row: the lane that reads back its own number adds
         // up all of them in order
@@ -458,6 +514,8 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
   }
 }
 
+bool balance_single(int T, int S) { return T <= RB_SINGLE_ROWS && S <= RB_SINGLE_SEQS; }
+
 struct BalanceSpace {
   int chunk_rows, n_chunks, n_etiles;
   int64_t p, c, z, n, l, done, total;
@@ -483,7 +541,7 @@ BalanceSpace balance_space(int T, int E, int S) {
 template <int VEC, int NC>
 hipError_t run_forward(BalanceArgs& a, hipStream_t st) {
   const size_t lds = static_cast<size_t>(RB_HALF + 1) * a.E * 4;
-  if (a.T <= RB_SINGLE_ROWS && a.S <= RB_SINGLE_SEQS) {
+  if (balance_single(a.T, a.S)) {
     a.chunk_rows = RB_SINGLE_ROWS;
     balance_rows_kernel<VEC, NC, true><<<1, RB_THREADS, lds, st>>>(a);
     return hipGetLastError();
@@ -507,6 +565,7 @@ hipError_t run_backward(const BackwardArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t route_balance_workspace_bytes(int T, int E, int S) {
+  if (balance_single(T, S)) return 0;
   return static_cast<size_t>(balance_space(T, E, S).total);
 }
 

@@ -631,7 +631,7 @@ int moe_mxfp4_ffn_decode(const moe_mxfp4* GU, const moe_mxfp4* D, int shared_slo
  * Limits: 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= MOE_MAX_TOPK, 0 <= T < 2^24,
  * 1 <= n_seq <= 65536.
  * ws: at least moe_route_balance_workspace_bytes(T, E, n_seq) bytes, 256-byte
- * aligned (0 for sizes out of range). */
+ * aligned (0 for few rows, then ws may be NULL, and for sizes out of range). */
 size_t moe_route_balance_workspace_bytes(int T, int E, int n_seq);
 int moe_route_balance(const float* logits, const int32_t* idx, int T, int E, int k,
                       const int32_t* seq_offsets, int n_seq, const uint8_t* mask,

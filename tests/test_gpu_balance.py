@@ -369,6 +369,7 @@ def test_device_refusals():
     with pytest.raises(ValueError, match="must be a device tensor"):
         bf.route_balance(lg, ix, mask=torch.zeros(4, dtype=torch.uint8))
     with pytest.raises(bf.MoeError, match="workspace"):
-        bf.route_balance(lg, ix, ws=torch.empty((16,), dtype=torch.uint8, device=dev))
+        bf.route_balance(torch.zeros((100, 8), device=dev), torch.zeros((100, 2), dtype=torch.int32, device=dev),
+                         ws=torch.empty((16,), dtype=torch.uint8, device=dev))
     with pytest.raises(bf.MoeError, match="invalid argument"):
         bf.route_backward(lg, ix, g_balance=torch.ones(1, device=dev))
