@@ -29,7 +29,7 @@ constexpr int RB_HALF = RB_WAVES / 2;
 constexpr int RB_MAX_CHUNKS = 256;    // one workgroup per CU on the largest inputs
 constexpr int RB_SINGLE_ROWS = 64;    // single launch: rows and sequences
 constexpr int RB_SINGLE_SEQS = 4;
-constexpr int RB_ETILE = 32;          // experts per workgroup of the second launch
+constexpr int RB_ETILE = 128;         // experts per workgroup of the second launch
 constexpr int RB_SUBS = 8;
 
 struct BalanceArgs {
@@ -104,16 +104,6 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
 }
 
-// e^d for d <= 0.  The product with log2(e) is carried in two parts, so the
-// result is good to about 2 units in the last place for every d (the hardware's
-// exponential to 1); below -126 it is 0.
-__device__ __forceinline__ float exp_hw(float d) {
-  d = fmaxf(d, -126.0f);
-  const float t = d * 1.44269502f;                                 // log2(e), rounded
-  const float lo = fmaf(d, 1.44269502f, -t) + d * 1.92596303e-8f;   // what both roundings lost
-  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147182f, 1.0f);
-}
-
 // Orders this wavefront's LDS accesses for its own lanes (one wavefront's LDS
 // accesses take effect in program order; this keeps the compiler to it).
 __device__ __forceinline__ void wave_lds_sync() {
@@ -123,6 +113,10 @@ __device__ __forceinline__ void wave_lds_sync() {
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_huge_valf(); }
+
+typedef float rf4 __attribute__((ext_vector_type(4)));
 
 // One row in a wavefront's registers.
 template <int VEC, int NC>
@@ -134,8 +128,8 @@ struct Row {
     for (int c = 0; c < NC; ++c) {
       const int e = VEC * (64 * c + lane);
       if constexpr (VEC == 4) {   // E is a multiple of 4
-        const float4 q = e < E ? *reinterpret_cast<const float4*>(row + e)
-                               : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+        const rf4 q = e < E ? __builtin_nontemporal_load(reinterpret_cast<const rf4*>(row + e))
+                            : rf4{kNegInf, kNegInf, kNegInf, kNegInf};
         v[c][0] = q.x, v[c][1] = q.y, v[c][2] = q.z, v[c][3] = q.w;
       } else {
         v[c][0] = e < E ? row[e] : kNegInf;
@@ -145,32 +139,41 @@ struct Row {
 
   // v becomes exp(v - max), returns their sum; lse = log of the sum of exp(v).
   // NaN as -inf; equal values, infinities too, differ by 0; absent experts 0.
+  // The exponential is 2^((v - max) log2(e)): its argument is rounded twice, a
+  // relative error of at most |v - max| 2^-23 in terms that are e^(v - max) small.
   __device__ __forceinline__ float exps(int E, int lane, float& lse) {
     float m = kNegInf;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        v[c][j] = v[c][j] != v[c][j] ? kNegInf : v[c][j];
+        v[c][j] = fmaxf(v[c][j], kNegInf);   // the number of the two: NaN becomes -inf
         m = fmaxf(m, v[c][j]);
       }
     m = wave_max(m);
     float sum = 0.0f;
+    if (finite(m)) {   // absent experts hold -inf, whose exponential is 0
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = v[c][j] == m ? 0.0f : v[c][j] - m;
-        v[c][j] = VEC * (64 * c + lane) < E ? exp_hw(d) : 0.0f;
-        sum += v[c][j];
-      }
+        for (int j = 0; j < VEC; ++j) {
+          v[c][j] = __builtin_amdgcn_exp2f((v[c][j] - m) * 1.44269504f);
+          sum += v[c][j];
+        }
+    } else {           // only the logits equal to the infinite maximum count
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          v[c][j] = v[c][j] == m && VEC * (64 * c + lane) < E ? 1.0f : 0.0f;
+          sum += v[c][j];
+        }
+    }
     sum = wave_sum(sum);
     lse = m + logf(sum);
     return sum;
   }
 };
-
-__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_huge_valf(); }
 
 // The losses of a sequence from its sums.
 __device__ __forceinline__ void write_losses(const BalanceArgs& a, int s, int n, double cp, float zs) {
@@ -214,6 +217,14 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
       ahead.load(a.logits + static_cast<int64_t>(b0 + wave) * E, E, lane);
       part = !a.mask || a.mask[b0 + wave] != 0;
     }
+    __syncthreads();   // the histogram is clear
+    const int64_t p0 = static_cast<int64_t>(b0) * a.k;
+    const int np = max(b1 - b0, 0) * a.k;
+    for (int p = tid; p < np; p += RB_THREADS) {
+      if (a.mask && !a.mask[b0 + p / a.k]) continue;
+      const int e = a.idx[p0 + p];
+      if (e >= 0 && e < E) atomicAdd(&s_c[e], 1);
+    }
     for (int t = b0 + wave; t < b1; t += RB_WAVES) {
       r = ahead;
       const bool now = part;
@@ -250,14 +261,6 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
     if (lane == 0) {
       s_z[wave] = zs;
       s_n[wave] = n;
-    }
-    __syncthreads();
-    const int64_t p0 = static_cast<int64_t>(b0) * a.k;
-    const int np = max(b1 - b0, 0) * a.k;
-    for (int p = tid; p < np; p += RB_THREADS) {
-      if (a.mask && !a.mask[b0 + p / a.k]) continue;
-      const int e = a.idx[p0 + p];
-      if (e >= 0 && e < E) atomicAdd(&s_c[e], 1);
     }
     __syncthreads();
     double cp = 0.0;
@@ -300,12 +303,22 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
 __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(BalanceArgs a) {
   __shared__ float s_p[RB_SUBS][RB_ETILE];
   __shared__ int32_t s_c[RB_SUBS][RB_ETILE];
-  __shared__ int s_last;
+  __shared__ double s_l[RB_ETILE / 64];
   const int tile = static_cast<int>(blockIdx.x) % a.n_etiles, s = static_cast<int>(blockIdx.x) / a.n_etiles;
-  const int el = threadIdx.x % RB_ETILE, sub = threadIdx.x / RB_ETILE;
+  const int tid = threadIdx.x, el = tid % RB_ETILE, sub = tid / RB_ETILE;
   const int e = tile * RB_ETILE + el;
   const int b0 = seq_bound(a.seq, s, a.S, a.T), b1 = seq_bound(a.seq, s + 1, a.S, a.T);
   const int c0 = b0 / a.chunk_rows, c1 = b1 > b0 ? (b1 - 1) / a.chunk_rows + 1 : c0;
+  // the sequence's z and row count (lanes over its chunks), in the first
+  // wavefront of every workgroup: whichever needs them has them at hand
+  float zs = 0.0f;
+  int n = 0;
+  if (tid < 64) {
+    for (int q = c0 + tid; q < c1; q += 64) {
+      zs += a.z_part[q + s];
+      n += a.n_part[q + s];
+    }
+  }
   float p = 0.0f;
   int32_t c = 0;
   if (e < a.E) {
@@ -319,7 +332,7 @@ __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(Bala
   s_p[sub][el] = p;
   s_c[sub][el] = c;
   __syncthreads();
-  if (sub == 0) {
+  if (sub == 0) {   // whole wavefronts
     for (int i = 1; i < RB_SUBS; ++i) {
       p += s_p[i][el];
       c += s_c[i][el];
@@ -332,35 +345,30 @@ __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(Bala
       cp = static_cast<double>(c) * p;
     }
 #pragma unroll
-    for (int off = RB_ETILE / 2; off >= 1; off >>= 1) cp += __shfl_xor(cp, off, 64);
-    if (el == 0) {
-      __hip_atomic_store(&a.l_part[static_cast<int64_t>(s) * a.n_etiles + tile], cp, __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-      const uint32_t before = __hip_atomic_fetch_add(&a.done[s], 1u, __ATOMIC_ACQ_REL,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-      s_last = before + 1 == static_cast<uint32_t>(a.n_etiles);
-    }
+    for (int off = 32; off >= 1; off >>= 1) cp += __shfl_xor(cp, off, 64);
+    if (tid % 64 == 0) s_l[tid / 64] = cp;
   }
   __syncthreads();
-  if (!s_last || threadIdx.x >= 64) return;
-  // one wavefront: the sequence's z and row count (lanes over its chunks) and
-  // its loss (tiles in order)
-  float zs = 0.0f;
-  int n = 0;
-  for (int q = c0 + static_cast<int>(threadIdx.x); q < c1; q += 64) {
-    zs += a.z_part[q + s];
-    n += a.n_part[q + s];
-  }
+  if (tid >= 64) return;
   zs = wave_sum(zs);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, 64);
-  double l = 0.0;   // at most 32 tiles: a lane each
-  if (static_cast<int>(threadIdx.x) < a.n_etiles)
-    l = __hip_atomic_load(&a.l_part[static_cast<int64_t>(s) * a.n_etiles + threadIdx.x], __ATOMIC_RELAXED,
-                          __HIP_MEMORY_SCOPE_AGENT);
+  double l = 0.0;
+  for (int i = 0; i < RB_ETILE / 64; ++i) l += s_l[i];
+  if (a.n_etiles > 1) {
+    double* part = a.l_part + static_cast<int64_t>(s) * a.n_etiles;
+    uint32_t before = 0;
+    if (tid == 0) {
+      __hip_atomic_store(&part[tile], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      before = __hip_atomic_fetch_add(&a.done[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) + 1 != static_cast<uint32_t>(a.n_etiles)) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    l = tid < a.n_etiles ? __hip_atomic_load(&part[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
-  if (threadIdx.x == 0) write_losses(a, s, n, l, zs);
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+  }
+  if (tid == 0) write_losses(a, s, n, l, zs);
 }
 
 // ---------------------------------------------------------------------------
@@ -506,7 +514,7 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
       const int e = VEC * (64 * c + lane);
       if (e < E) {
         if constexpr (VEC == 4)
-          *reinterpret_cast<float4*>(out + e) = make_float4(d[c][0], d[c][1], d[c][2], d[c][3]);
+          __builtin_nontemporal_store(rf4{d[c][0], d[c][1], d[c][2], d[c][3]}, reinterpret_cast<rf4*>(out + e));
         else
           out[e] = d[c][0];
       }

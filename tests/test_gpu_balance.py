@@ -1,11 +1,12 @@
 """GPU tests of the router's balance and z losses, per-expert counts and logit
 gradients against the fp64 oracle.
 
-Bars, u = 2^-24.  A probability is exp(l - max) / sum: the difference rounds
-once (|d| u absolute, so a relative error |d| u of the exponential, and
-|d| <= 104 wherever the exponential is not 0 in fp32), the exponential and the
-division by a few u more, the sum of E terms by E u at most: relative error at
-most P = (120 + E) u, or absolute 2^-125 where the exponential underflows.
+Bars, u = 2^-24.  A probability is exp(d) / sum, d = l - max: the difference
+and its product with log2(e) round once each, which is a relative error of
+2.2 |d| u of the exponential, and |d| <= 50 in these inputs wherever it is not 0
+in fp32; the exponential and the division add a few u, the sum of E terms E u at
+most: relative error at most P = (120 + E) u, or absolute 2^-125 where the
+exponential underflows.
 Sums over n rows add at most n u (relative to sums of positive terms).  lse
 is max + log(sum): absolute error at most 4 u (|lse| + |max|) + (E + 4) u.
 """
