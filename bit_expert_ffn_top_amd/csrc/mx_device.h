@@ -5,18 +5,13 @@
 
 namespace bitffn {
 
-// The scale byte as a float: 2^(s-127), the subnormal 2^-127 for 0, NaN for 255.
-__device__ __forceinline__ float mx_scale(uint32_t s) {
-  const uint32_t b = s == 0 ? 0x00400000u : s << 23;
-  return __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : b);
-}
-
-// The 8 values of a 32-bit word of codes (value j in bits 4j..4j+3), scaled.
-// v_cvt_scalef32_pk_f32_fp4 reads the scale operand's exponent field, NaN
-// included.
+// The 8 values of a 32-bit word of codes (value j in bits 4j..4j+3), scaled by
+// the scale byte s.  v_cvt_scalef32_pk_f32_fp4 reads its scale operand's exponent
+// field alone: 2^(field - 127) also where a float with that field would be zero
+// or subnormal, and NaN where it would be infinite, which is the byte's meaning.
 __device__ __forceinline__ void mx_values8(uint32_t c, uint32_t s, float (&f)[8]) {
   typedef float f2 __attribute__((ext_vector_type(2)));
-  const float scale = mx_scale(s);
+  const float scale = __builtin_bit_cast(float, s << 23);
   const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0);
   const f2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
   const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2);
