@@ -190,78 +190,195 @@ __device__ __forceinline__ void store_out(uint8_t* p, mf4 v) {
   }
 }
 
-// Few rows per group: a wavefront takes 16 weight rows and MT tiles of 16
-// tokens, everything straight from memory.  SPLIT wavefronts share one
-// 16-row tile, each with its share of the 256-column chunks (chunk c belongs
-// to wavefront c % SPLIT), and their sums meet in LDS in wavefront order.
-template <int MT, int SPLIT, bool GATED, bool BF16>
-__global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a) {
-  constexpr int WAVES = ML_THREADS / 64;
-  constexpr int TILES = WAVES / SPLIT;       // 16-row weight tiles per workgroup
-  const int n_wg = (a.N + 16 * TILES - 1) / (16 * TILES);
-  const RowTile t = find_row_tile(a, -1, static_cast<int>(blockIdx.x) / n_wg, 16 * MT);
-  if (t.rows <= 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, q = lane >> 4;
-  const int n0 = (static_cast<int>(blockIdx.x) % n_wg * TILES + wave / SPLIT) * 16;
-  const bool here = n0 < a.N;                // the last workgroup may have tiles to spare
-  const int nb = a.K / 32;                   // blocks of a row
-  const int64_t crow = a.K / 2;
-  const int64_t wrow = static_cast<int64_t>(t.g) * a.N + min(n0, a.N - 16) + r;
-  const uint8_t* __restrict__ wc = a.wc + wrow * crow;
-  const uint8_t* __restrict__ ws = a.ws + wrow * nb;
-  const uint8_t* xc[MT];
-  const uint8_t* xs[MT];
-  bool ok[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int local = 16 * m + r;
-    const int64_t s = source_row(a, t.r0 + min(local, t.rows - 1), ok[m]);   // widened: offsets may pass 2^32
-    xc[m] = a.ac + s * crow;
-    xs[m] = a.as + s * nb;
+// Place of 16-byte piece p of row r of 128 bytes in LDS: p ^ mg_swz(r).
+__host__ __device__ constexpr int mg_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Keeps the compiler to the program order of this wavefront's LDS accesses
+// (which is the order in which they take effect).
+__device__ __forceinline__ void mg_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Few rows per group: a wavefront takes 16 weight rows and up to 4 tiles of 16
+// tokens.  SPLIT wavefronts share one 16-row tile, each with its share of the
+// 256-column chunks (chunk c belongs to wavefront c % SPLIT), and their sums meet
+// in LDS in wavefront order.  Every chunk of 16 rows is read as it lies, 8 rows
+// of 128 bytes per instruction, the next one while this one is multiplied, and
+// passes through a piece of LDS of the wavefront's own to the lanes that
+// multiply it: read where they want it, 16 bytes a row, it costs the path from
+// the caches 64 bytes for each 16.
+constexpr int MR_TILES = 4;
+constexpr int MR_PIECE = 16 * 128 + 16 * 8;   // LDS of 16 rows of a chunk: codes, scales
+
+// 16 rows of a chunk: 16-byte piece lane % 8 of rows lane / 8 and 8 more, and two
+// scales of row lane / 4.  rows: where the first, the second and the scales' row
+// begin.
+struct MrRows {
+  mi4 c[2];
+  uint32_t s;
+
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const uint8_t* c0, const uint8_t* c1, const uint8_t* sc, int nb, int chunk) {
+    const int lane = threadIdx.x & 63;
+    const int piece = min(8 * chunk + (lane & 7), nb - 1);   // past a row: its last, not used
+    const mi4* p0 = reinterpret_cast<const mi4*>(c0 + 16 * piece);
+    const mi4* p1 = reinterpret_cast<const mi4*>(c1 + 16 * piece);
+    c[0] = STREAM ? __builtin_nontemporal_load(p0) : *p0;
+    c[1] = STREAM ? __builtin_nontemporal_load(p1) : *p1;
+    const int b = 8 * chunk + 2 * (lane & 3);
+    if (nb % 2 == 0)
+      s = *reinterpret_cast<const uint16_t*>(sc + min(b, nb - 2));
+    else
+      s = sc[min(b, nb - 1)] | sc[min(b + 1, nb - 1)] << 8;
   }
-  mf4 acc[MT] = {};
-  const int chunks = (nb + 7) / 8;
-  for (int c = wave % SPLIT; c < chunks; c += SPLIT) {
+
+  __device__ __forceinline__ void put(uint8_t* to) const {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int b = 8 * c + 2 * q + j;
-      const bool in = b < nb;
-      const int bc = in ? b : nb - 1;        // a block past the row: zeros with scale 1
-      mi4 w = *reinterpret_cast<const mi4*>(wc + 16 * bc);
-      const uint32_t sw = in ? ws[bc] : kOne;
-      if (!in) w = mi4{0, 0, 0, 0};
+      const int row = 8 * j + (lane >> 3);
+      *reinterpret_cast<mi4*>(to + 128 * row + 16 * ((lane & 7) ^ mg_swz(row))) = c[j];
+    }
+    *reinterpret_cast<uint16_t*>(to + 16 * 128 + 2 * lane) = static_cast<uint16_t>(s);
+  }
+};
+
+// What lane l multiplies: blocks 2 (l / 16) and the next of row l % 16.
+struct MrOperand {
+  mi4 c[2];
+  uint32_t s[2];
+
+  __device__ __forceinline__ void get(const uint8_t* from, int nb, int chunk, bool weights) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const uint32_t both = *reinterpret_cast<const uint16_t*>(from + 16 * 128 + 8 * r + 2 * q);
+    s[0] = both & 0xFFu;
+    s[1] = both >> 8;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const mi4 x = *reinterpret_cast<const mi4*>(xc[m] + 16 * bc);
-        const uint32_t sx = in ? xs[m][bc] : kOne;
-        acc[m] = mfma_fp4(w, x, acc[m], sw, sx);
+    for (int j = 0; j < 2; ++j) {
+      c[j] = *reinterpret_cast<const mi4*>(from + 128 * r + 16 * ((2 * q + j) ^ mg_swz(r)));
+      if (8 * chunk + 2 * q + j >= nb) {   // past the row: zeros with scale 1
+        s[j] = kOne;
+        if (weights) c[j] = mi4{0, 0, 0, 0};
       }
     }
   }
+};
+
+struct MrAt {
+  const uint8_t* c0;
+  const uint8_t* c1;
+  const uint8_t* s;
+};
+
+// The sums of M token tiles over chunks first, first + step, .., AHEAD of them
+// on their way.
+template <int M, int AHEAD, bool STREAM>
+__device__ __forceinline__ void mr_sums(mf4 (&acc)[MR_TILES], const MrAt& w, const MrAt (&x)[MR_TILES],
+                                        uint8_t* lds, int nb, int first, int step) {
+  const int chunks = (nb + 7) / 8;
+  MrRows nw[AHEAD], nx[AHEAD][M];
+  const auto load = [&](int d, int c) {
+    if (c >= chunks) return;
+    nw[d].template load<STREAM>(w.c0, w.c1, w.s, nb, c);
+#pragma unroll
+    for (int m = 0; m < M; ++m) nx[d][m].template load<false>(x[m].c0, x[m].c1, x[m].s, nb, c);
+  };
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d) load(d, first + d * step);
+  for (int c0 = first; c0 < chunks; c0 += AHEAD * step) {
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) {
+      const int c = c0 + d * step;
+      if (c >= chunks) break;
+      mg_wave_sync();
+      nw[d].put(lds);
+      MrOperand ow, ox;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        nx[d][m].put(lds + MR_PIECE);
+        if (m + 1 == M) load(d, c + AHEAD * step);
+        mg_wave_sync();
+        if (m == 0) ow.get(lds, nb, c, true);
+        ox.get(lds + MR_PIECE, nb, c, false);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[m] = mfma_fp4(ow.c[j], ox.c[j], acc[m], ow.s[j], ox.s[j]);
+        mg_wave_sync();
+      }
+    }
+  }
+}
+
+template <int SPLIT, bool GATED, bool BF16>
+__global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a, int64_t first) {
+  constexpr int WAVES = ML_THREADS / 64;
+  constexpr int TILES = WAVES / SPLIT;       // 16-row weight tiles per workgroup
+  constexpr int kPart = SPLIT > 1 ? TILES * (SPLIT - 1) * MR_TILES * 64 * static_cast<int>(sizeof(mf4)) : 0;
+  __shared__ __align__(16) uint8_t lds[kPart > WAVES * 2 * MR_PIECE ? kPart : WAVES * 2 * MR_PIECE];
+  const int n_wg = (a.N + 16 * TILES - 1) / (16 * TILES);
+  const int64_t at_wg = first + blockIdx.x;
+  const RowTile t = find_row_tile(a, -1, static_cast<int>(at_wg / n_wg), 16 * MR_TILES);
+  if (t.rows <= 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int n0 = (static_cast<int>(at_wg % n_wg) * TILES + wave / SPLIT) * 16;
+  const bool here = n0 < a.N;                // the last workgroup may have tiles to spare
+  const int nb = a.K / 32;                   // blocks of a row
+  const int64_t crow = a.K / 2;
+  const int64_t wrow = static_cast<int64_t>(t.g) * a.N + min(n0, a.N - 16);
+  const MrAt w = {a.wc + (wrow + (lane >> 3)) * crow, a.wc + (wrow + 8 + (lane >> 3)) * crow,
+                  a.ws + (wrow + (lane >> 2)) * nb};
+  // lane i: the source of the tile's row i, complemented where it has none
+  static_assert(16 * MR_TILES == 64, "a row of the tile per lane");
+  bool ok;
+  const int s = source_row(a, t.r0 + min(lane, t.rows - 1), ok);
+  const int src = ok ? s : ~s;
+  MrAt x[MR_TILES];
+#pragma unroll
+  for (int m = 0; m < MR_TILES; ++m) {
+    const auto row = [&](int i) {            // widened: offsets may pass 2^32
+      const int v = __shfl(src, 16 * m + i, 64);
+      return static_cast<int64_t>(v < 0 ? ~v : v);
+    };
+    x[m] = MrAt{a.ac + row(lane >> 3) * crow, a.ac + row(8 + (lane >> 3)) * crow, a.as + row(lane >> 2) * nb};
+  }
+  mf4 acc[MR_TILES] = {};
+  uint8_t* mine = lds + 2 * MR_PIECE * wave;
+  // weights that only this tile reads stream past the caches (16 experts of
+  // 4096 x 4096, a row each: 57 -> 34 us)
+  if (!t.whole)
+    mr_sums<MR_TILES, 1, false>(acc, w, x, mine, nb, wave % SPLIT, SPLIT);
+  else if (t.rows <= 16)
+    mr_sums<1, 4, true>(acc, w, x, mine, nb, wave % SPLIT, SPLIT);
+  else if (t.rows <= 32)
+    mr_sums<2, 2, true>(acc, w, x, mine, nb, wave % SPLIT, SPLIT);
+  else
+    mr_sums<MR_TILES, 1, true>(acc, w, x, mine, nb, wave % SPLIT, SPLIT);
   if constexpr (SPLIT > 1) {
-    __shared__ mf4 part[TILES][SPLIT - 1][MT][64];
+    mf4* part = reinterpret_cast<mf4*>(lds);   // [TILES][SPLIT - 1][MR_TILES][64]
     const int ti = wave / SPLIT, si = wave % SPLIT;
+    __syncthreads();
     if (si > 0) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) part[ti][si - 1][m][lane] = acc[m];
+      for (int m = 0; m < MR_TILES; ++m) part[((ti * (SPLIT - 1) + si - 1) * MR_TILES + m) * 64 + lane] = acc[m];
     }
     __syncthreads();
     if (si > 0) return;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MR_TILES; ++m)
 #pragma unroll
-      for (int i = 0; i < SPLIT - 1; ++i) acc[m] += part[ti][i][m][lane];
+      for (int i = 0; i < SPLIT - 1; ++i) acc[m] += part[((ti * (SPLIT - 1) + i) * MR_TILES + m) * 64 + lane];
   }
   if (!here) return;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < MR_TILES; ++m) {
     const int local = 16 * m + r;
+    const bool has = __shfl(src, local, 64) >= 0;
     if (local < t.rows) {
       const int col = n0 + 4 * q;
       const int64_t at = (t.r0 + local) * (GATED ? a.N / 2 : a.N) + (GATED ? col / 2 : col);
-      store_out<GATED, BF16>(static_cast<uint8_t*>(a.y) + at * (BF16 ? 2 : 4),
-                             ok[m] ? acc[m] : mf4{0, 0, 0, 0});
+      store_out<GATED, BF16>(static_cast<uint8_t*>(a.y) + at * (BF16 ? 2 : 4), has ? acc[m] : mf4{0, 0, 0, 0});
     }
   }
 }
@@ -298,19 +415,9 @@ typedef __attribute__((address_space(3))) mi4 LdsInt4;
 typedef __attribute__((address_space(3))) mf4 LdsFloat4;
 typedef __attribute__((address_space(3))) uint16_t LdsU16;
 
-__host__ __device__ constexpr int mg_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
 __device__ __forceinline__ MgRsrc mg_rsrc(const uint8_t* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
                                            static_cast<int>(static_cast<uint32_t>(bytes)), 0x00020000);
-}
-
-// Keeps the compiler to the program order of this wavefront's LDS accesses
-// (which is the order in which they take effect).
-__device__ __forceinline__ void mg_wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Buffers (a read past one gives zeros) and this lane's byte offsets in them.
@@ -736,13 +843,24 @@ void launch_groups(const LinearArgs& a, hipStream_t s) {
     mx_linear_groups_kernel<CAP, 1, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a, slices);
 }
 
+constexpr int64_t kMaxBlocks = (int64_t{1} << 32) / ML_THREADS - 8;   // of a launch: 32 bits of threads
+
+template <int SPLIT, bool GATED, bool BF16>
+void launch_rows(const LinearArgs& a, int64_t tiles, hipStream_t s) {
+  constexpr int per = 16 * (ML_THREADS / 64) / SPLIT;
+  const int64_t n = tiles * ((a.N + per - 1) / per);
+  for (int64_t first = 0; first < n; first += kMaxBlocks)
+    mx_linear_rows_kernel<SPLIT, GATED, BF16><<<static_cast<unsigned>(min(n - first, kMaxBlocks)), ML_THREADS, 0, s>>>(a, first);
+}
+
 template <bool GATED, bool BF16>
 void launch_rows(const LinearArgs& a, hipStream_t s) {
-  constexpr int MT = 4, SPLIT = 4;
-  const int64_t full = (a.R + 16 * MT - 1) / (16 * MT);
-  const int64_t tiles = a.offsets ? (a.R / (16 * MT)) + min(static_cast<int64_t>(a.G), a.R) : full;
-  const unsigned grid = static_cast<unsigned>(tiles * ((a.N + 15) / 16));
-  mx_linear_rows_kernel<MT, SPLIT, GATED, BF16><<<grid, ML_THREADS, 0, s>>>(a);
+  constexpr int m = 16 * MR_TILES;
+  const int64_t tiles = a.offsets ? a.R / m + min(static_cast<int64_t>(a.G), a.R) : (a.R + m - 1) / m;
+  if (tiles * (a.N / 64) >= device_cus())
+    launch_rows<1, GATED, BF16>(a, tiles, s);
+  else
+    launch_rows<4, GATED, BF16>(a, tiles, s);
 }
 
 template <bool GATED, bool BF16>
