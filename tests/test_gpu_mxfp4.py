@@ -212,6 +212,24 @@ WIDE = [  # enough row tiles and columns for the kernel of full tiles: M, R, G, 
 def test_wide_products(M, R, G, N, K, dtype):
     """Groups of one row and of thousands, several tiles to a group, a last
     step and a last chunk of scales that a row ends inside; both products."""
+    _check_products(M, R, G, N, K, dtype)
+
+
+FEW = [  # too little work for that kernel: one to over 64 rows a group, rows of up to 64 chunks
+    (30, 100, 40, 512, 1312), (50, 900, 40, 512, 2400), (60, 1500, 40, 448, 1056), (16, 40, 40, 448, 4128),
+    (20, 60, 6, 64, 4384), (20, 300, 3, 80, 8448), (9, 33, 1, 32, 16384), (70, 65, 1, 64, 5024),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,R,G,N,K", FEW, ids=[f"M{c[0]}_R{c[1]}_G{c[2]}_N{c[3]}_K{c[4]}" for c in FEW])
+def test_products_of_few_rows(M, R, G, N, K, dtype):
+    """One, two and four token tiles, a tile that shares its group with others,
+    more chunks than are asked for ahead, rows that end inside one."""
+    _check_products(M, R, G, N, K, dtype)
+
+
+def _check_products(M, R, G, N, K, dtype):
     bf = _bf()
     dev = need_gpu()
     rng = np.random.default_rng(M + R + G + N + K)
@@ -300,8 +318,8 @@ def test_products_of_extreme_scales():
 
 
 def test_rows_do_not_depend_on_the_batch():
-    """A row's result has the same bits alone, among few and among many rows
-    of the same matrix, wherever the group begins."""
+    """A call repeated gives the same bits; a row alone, among few and among
+    many rows differs by no more than the order of its sum."""
     bf = _bf()
     rng = np.random.default_rng(6)
     R, N, K = 600, 272, 416
