@@ -170,11 +170,16 @@ def _dev(t: torch.Tensor, dtype, name: str):
 def _shape(t: torch.Tensor, shape, name: str):
     """t must have exactly this shape (None: any extent).  Checked before the
     device checks, so that a wrong size is reported as such."""
-    if t.dim() != len(shape) or any(s is not None and a != s for a, s in zip(t.shape, shape)):
-        parts = ["*" if s is None else str(s) for s in shape]
-        want = "(" + ", ".join(parts) + ("," if len(parts) == 1 else "") + ")"
-        raise ValueError(f"{name}: shape {want} expected, got {tuple(t.shape)}")
-    return t
+    got = t.shape
+    if len(got) == len(shape):
+        for a, s in zip(got, shape):
+            if a != s and s is not None:
+                break
+        else:
+            return t
+    parts = ["*" if s is None else str(s) for s in shape]
+    want = "(" + ", ".join(parts) + ("," if len(parts) == 1 else "") + ")"
+    raise ValueError(f"{name}: shape {want} expected, got {tuple(got)}")
 
 
 def _at_least(t: torch.Tensor, n: int, name: str):
@@ -772,10 +777,13 @@ class Mxfp4:
     @property
     def shape(self):
         """(matrices, rows, cols)"""
-        c = self.codes
-        return (1 if c.dim() == 2 else c.shape[0], c.shape[-2], 2 * c.shape[-1])
+        c = self.codes.shape
+        return (1 if len(c) == 2 else c[0], c[-2], 2 * c[-1])
 
     def check(self, name):
+        c, s = self.codes.shape, self.scales.shape
+        if len(c) in (2, 3) and c[:-1] == s[:-1] and c[-1] == 16 * s[-1]:
+            return self
         if self.codes.dim() not in (2, 3):
             raise ValueError(f"{name}.codes: shape (rows, cols / 2) or (matrices, rows, cols / 2) "
                              f"expected, got {tuple(self.codes.shape)}")
