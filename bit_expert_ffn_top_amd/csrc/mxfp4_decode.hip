@@ -24,7 +24,7 @@
 // the last step's weights and x before the rows, the next expert's rows before
 // the present ones are used.  10 of 512 experts and the shared one, d = 2048,
 // F = 768: one token 6.4 + 4.4 us (27.6 MB: 2.6 TB/s), four tokens over 34
-// experts 17.6 + 12.2 us (86 MB: 2.9 TB/s).  The matrix cores were tried in place
+// experts 15.0 + 12.2 us (86 MB: 3.2 TB/s).  The matrix cores were tried in place
 // of the vector unit (activations as three bfloat16 parts): 10.7 + 13.6 and
 // 22.4 + 30.0 us, for the parts' traffic through LDS.
 #include "moe_internal.h"
@@ -101,31 +101,28 @@ struct Blocks {
     }
   }
 
-  // sum[r] += block it of row r times v, if in
-  __device__ __forceinline__ void dot(int it, bool in, const df4 (&v)[8], float (&sum)[ROWS]) const {
+  // sum[r] += values 16 half .. 16 half + 15 of block it of row r times v
+  __device__ __forceinline__ void dot(int it, int half, const df4 (&v)[4], float (&sum)[ROWS]) const {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      float acc = 0.0f;
       uint32_t scale = s[it][r];
       opaque(scale);   // no wait for it before the activations are asked for
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         float f[8];
-        uint32_t word = c[it][r][q];
+        uint32_t word = c[it][r][2 * half + q];
         opaque(word);   // its values are formed here, not kept over the loop of tokens
         mx_values8(word, scale, f);
         const df4 x = v[2 * q], y = v[2 * q + 1];
-        acc = q ? fmaf(f[0], x.x, acc) : f[0] * x.x;
-        acc = fmaf(f[1], x.y, acc);
-        acc = fmaf(f[2], x.z, acc);
-        acc = fmaf(f[3], x.w, acc);
-        acc = fmaf(f[4], y.x, acc);
-        acc = fmaf(f[5], y.y, acc);
-        acc = fmaf(f[6], y.z, acc);
-        acc = fmaf(f[7], y.w, acc);
+        sum[r] = fmaf(f[0], x.x, sum[r]);
+        sum[r] = fmaf(f[1], x.y, sum[r]);
+        sum[r] = fmaf(f[2], x.z, sum[r]);
+        sum[r] = fmaf(f[3], x.w, sum[r]);
+        sum[r] = fmaf(f[4], y.x, sum[r]);
+        sum[r] = fmaf(f[5], y.y, sum[r]);
+        sum[r] = fmaf(f[6], y.z, sum[r]);
+        sum[r] = fmaf(f[7], y.w, sum[r]);
       }
-      acc = in ? acc : 0.0f;
-      sum[r] = it ? sum[r] + acc : acc;
     }
   }
 };
@@ -178,7 +175,10 @@ __global__ __launch_bounds__(MD_UP_THREADS) void mx_decode_gate_up_kernel(Decode
   constexpr int SUB = 64 / LPR, WAVES = MD_UP_THREADS / 64;
   constexpr int PER = (LPR * ITER * 8 + MD_UP_THREADS - 1) / MD_UP_THREADS;   // 16-byte pieces of x per thread
   __shared__ df4 s_x[LPR * ITER * 8];   // a token's x, 8 pieces per block
-  const int tid = threadIdx.x, lane = tid & 63, l = lane % LPR, n = a.T * a.k, p = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane % LPR, n = a.T * a.k;
+  // the shared expert works for every token and comes first, so that its workgroups
+  // are not the last to end (four tokens: 18.1 -> 15.0 us)
+  const int p = a.shared_slot < 0 ? blockIdx.y : blockIdx.y == 0 ? n : blockIdx.y - 1;
   const int nb = a.d / 32, nf = a.f / 32;
   const auto fetch = [&](int t, df4 (&x)[PER]) {
     const df4* from = reinterpret_cast<const df4*>(a.x + t * a.d);
@@ -210,14 +210,22 @@ __global__ __launch_bounds__(MD_UP_THREADS) void mx_decode_gate_up_kernel(Decode
   for (;;) {
     const int q = __ffsll(static_cast<unsigned long long>(todo)) - 1;
     __syncthreads();
-    float sum[MD_UP_ROWS];
+    float sum[MD_UP_ROWS] = {};
 #pragma unroll
     for (int it = 0; it < ITER; ++it) {
       const int b = l + it * LPR, bc = min(b, nb - 1);
-      df4 v[8];
+      float before[MD_UP_ROWS];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = s_x[8 * bc + (c ^ md_swz(bc))];
-      w.dot(it, b < nb, v, sum);
+      for (int r = 0; r < MD_UP_ROWS; ++r) before[r] = sum[r];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // half a block's activations at a time: registers for six wavefronts
+        df4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = s_x[8 * bc + ((4 * half + c) ^ md_swz(bc))];
+        w.dot(it, half, v, sum);
+      }
+#pragma unroll
+      for (int r = 0; r < MD_UP_ROWS; ++r) sum[r] = b < nb ? sum[r] : before[r];
     }
     const float g = reduce_rows<MD_UP_ROWS, LPR>(sum, l);
     const float u = from8(g);   // the odd row of the pair
@@ -283,15 +291,21 @@ __global__ __launch_bounds__(MD_DOWN_THREADS) void mx_decode_down_kernel(DecodeA
     for (uint64_t todo = job.todo; todo; todo &= todo - 1) {
       const int q = __ffsll(static_cast<unsigned long long>(todo)) - 1;
       const df4* h = reinterpret_cast<const df4*>(a.h + (job.routed ? h_row(a, q) : h_shared(a, q)) * a.f);
-      float sum[MD_DOWN_ROWS];
+      float sum[MD_DOWN_ROWS] = {};
 #pragma unroll
       for (int it = 0; it < ITER; ++it) {
         const int b = l + it * LPR;
         const uint32_t bc = min(b, nf - 1);
-        df4 v[8];
+        float before[MD_DOWN_ROWS];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = (h + c * nf)[bc];
-        w.dot(it, b < nf, v, sum);
+        for (int r = 0; r < MD_DOWN_ROWS; ++r) before[r] = sum[r];
+        df4 v[2][4];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c / 4][c % 4] = (h + c * nf)[bc];
+        w.dot(it, 0, v[0], sum);
+        w.dot(it, 1, v[1], sum);
+#pragma unroll
+        for (int r = 0; r < MD_DOWN_ROWS; ++r) sum[r] = b < nf ? sum[r] : before[r];
       }
       const float r = reduce_rows<MD_DOWN_ROWS, LPR>(sum, l);
       if (l < 4)
