@@ -717,14 +717,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _same_device(what, tensors):
     """The device of the tensors (None entries passed over), which must be one."""
-    dev = None
+    first, at = None, -1
     for t in tensors:
         if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{what}: tensors on {dev} and {t.device}, one device expected")
-    return dev
+            if first is None:
+                first, at = t, t.get_device()
+            elif t.get_device() != at:
+                raise ValueError(f"{what}: tensors on {first.device} and {t.device}, one device expected")
+    return first.device
 
 
 def _on_stream(fn):
@@ -781,25 +781,29 @@ class Mxfp4:
         return (1 if len(c) == 2 else c[0], c[-2], 2 * c[-1])
 
     def check(self, name):
+        """The shape, after a check that codes and scales belong together."""
         c, s = self.codes.shape, self.scales.shape
-        if len(c) in (2, 3) and c[:-1] == s[:-1] and c[-1] == 16 * s[-1]:
-            return self
-        if self.codes.dim() not in (2, 3):
+        n = len(c)
+        if n == len(s) and 2 <= n <= 3 and c[-1] == 16 * s[-1] and c[-2] == s[-2] and c[0] == s[0]:
+            return (1 if n == 2 else c[0], c[-2], 2 * c[-1])
+        if n not in (2, 3):
             raise ValueError(f"{name}.codes: shape (rows, cols / 2) or (matrices, rows, cols / 2) "
-                             f"expected, got {tuple(self.codes.shape)}")
-        cols = 2 * self.codes.shape[-1]
+                             f"expected, got {tuple(c)}")
+        cols = 2 * c[-1]
         if cols % 32:
             raise ValueError(f"{name}.codes: cols a multiple of 32 expected, got {cols}")
-        _shape(self.scales, tuple(self.codes.shape[:-1]) + (cols // 32,), f"{name}.scales")
-        return self
+        _shape(self.scales, tuple(c[:-1]) + (cols // 32,), f"{name}.scales")
+        return self.shape
 
     def on_device(self, name):
-        _dev(self.codes, torch.uint8, f"{name}.codes")
-        _dev(self.scales, torch.uint8, f"{name}.scales")
+        for t, part in ((self.codes, "codes"), (self.scales, "scales")):
+            if not (t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous()):
+                _dev(t, torch.uint8, f"{name}.{part}")
         return self
 
-    def c_struct(self) -> Mxfp4C:
-        n, rows, cols = self.shape
+    def c_struct(self, shape=None) -> Mxfp4C:
+        """shape: the shape, where it is known already."""
+        n, rows, cols = shape or self.shape
         return Mxfp4C(n, rows, cols, 0, self.codes.data_ptr(), self.scales.data_ptr())
 
 
@@ -890,20 +894,17 @@ def mxfp4_dequantize(q: Mxfp4, dtype=torch.float32, y=None, stream=None):
 
 
 @_on_stream
-def _product(dev, stream, name, a, w, offsets, row_src, src_div, R, n_out, y, dtype, y_dtype):
+def _product(dev, stream, name, A, W, offsets, row_src, src_div, R, n_out, y, dtype, y_dtype):
     if y is None:
         y = torch.empty((R, n_out), dtype=dtype, device=dev)
-    A, W = a.c_struct(), w.c_struct()
     _check(getattr(lib(), name)(ctypes.byref(A), ctypes.byref(W), _addr(offsets), _addr(row_src),
                                 int(src_div), R, y.data_ptr(), y_dtype, stream), name)
     return y
 
 
 def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
-    a.check("a")
-    w.check("w")
-    na, ma, K = a.shape
-    G, N, Kw = w.shape
+    na, ma, K = a_shape = a.check("a")
+    G, N, Kw = w_shape = w.check("w")
     if na != 1:
         raise ValueError(f"{what}: a holds one matrix, got {na}")
     if K != Kw:
@@ -928,7 +929,8 @@ def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
     a.on_device("a")
     w.on_device("w")
     return _product(what, stream, (a.codes, a.scales, w.codes, w.scales, offsets, row_src, y),
-                    f"moe_{what}", a, w, offsets, row_src, src_div, R, n_out, y, dtype, y_dtype)
+                    f"moe_{what}", a.c_struct(a_shape), w.c_struct(w_shape), offsets, row_src, src_div, R, n_out,
+                    y, dtype, y_dtype)
 
 
 def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=None,
@@ -955,11 +957,10 @@ def mxfp4_ffn_decode_workspace_bytes(T: int, k: int, d_ff: int) -> int:
 
 
 @_on_stream
-def _mx_decode(dev, stream, gate_up, down, shared_slot, x, T, d, k, f, slot, w, y, ws):
+def _mx_decode(dev, stream, GU, D, shared_slot, x, T, d, k, f, slot, w, y, ws):
     if y is None:
         y = torch.empty((T, d), dtype=torch.float32, device=dev)
     wp, wn, keep = _scratch(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, f), ws, dev)
-    GU, D = gate_up.c_struct(), down.c_struct()
     _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), int(shared_slot),
                                       x.data_ptr(), T, k, slot.data_ptr(), w.data_ptr(),
                                       y.data_ptr(), wp, wn, stream), "moe_mxfp4_ffn_decode")
@@ -971,10 +972,8 @@ def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=
     """Decode / verify FFN of T = 1..4 tokens over 4-bit experts
     (moe_mxfp4_ffn_decode).  gate_up [n, 2 F, d], down [n, d, F]; x fp32 [T, d];
     slot int32 and w fp32 [T, k].  Returns y fp32 [T, d]."""
-    gate_up.check("gate_up")
-    down.check("down")
-    n, f2, d = gate_up.shape
-    if down.shape != (n, d, f2 // 2) or f2 % 2:
+    n, f2, d = gate_up.check("gate_up")
+    if down.check("down") != (n, d, f2 // 2) or f2 % 2:
         raise ValueError(f"down: (matrices, rows, cols) = {(n, d, f2 // 2)} expected, got {down.shape}")
     _shape(x, (None, d), "x")
     T = x.shape[0]
@@ -992,7 +991,8 @@ def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=
     down.on_device("down")
     return _mx_decode("mxfp4_ffn_decode", stream,
                       (x, slot, w, gate_up.codes, gate_up.scales, down.codes, down.scales, y, ws),
-                      gate_up, down, shared_slot, x, T, d, k, f2 // 2, slot, w, y, ws)
+                      gate_up.c_struct((n, f2, d)), down.c_struct((n, d, f2 // 2)), shared_slot, x, T, d, k,
+                      f2 // 2, slot, w, y, ws)
 
 
 class RouteBalance(NamedTuple):
