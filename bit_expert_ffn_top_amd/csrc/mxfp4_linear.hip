@@ -71,7 +71,7 @@ __device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int xcd, i
     return RowTile{0, static_cast<int>(min(static_cast<int64_t>(tile_m), max(a.R - r0, int64_t{0}))), r0,
                    a.R <= tile_m};
   }
-  __shared__ int s_wave[ML_THREADS / 64];
+  __shared__ int s_wave[ML_THREADS / 64], s_top[ML_THREADS / 64], s_bad[ML_THREADS / 64];
   __shared__ int s_g, s_rows, s_r0, s_whole;
   const int tid = threadIdx.x, lane = tid & 63;
   constexpr int kPer = (MOE_MAX_EXPERTS + ML_THREADS - 1) / ML_THREADS;
@@ -82,20 +82,48 @@ __device__ __forceinline__ RowTile find_row_tile(const LinearArgs& a, int xcd, i
     const int v = a.offsets[min(tid * kPer + i, a.G)];
     bound[i] = min(max(v, 0), R);
   }
+  const auto count = [&]() {   // this thread's tiles; their scan over the wavefront, inclusive
+    mine = 0;
+    bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    nt[i] = (max(bound[i + 1] - bound[i], 0) + tile_m - 1) / tile_m;
-    mine += nt[i];
-  }
-  int scan = mine;   // inclusive over the wavefront
+    for (int i = 0; i < kPer; ++i) {
+      bad |= bound[i + 1] < bound[i];
+      nt[i] = (max(bound[i + 1] - bound[i], 0) + tile_m - 1) / tile_m;
+      mine += nt[i];
+    }
+    int scan = mine;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int v = __shfl_up(scan, off, 64);
-    if (lane >= off) scan += v;
-  }
-  if (lane == 63) s_wave[tid >> 6] = scan;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(scan, off, 64);
+      if (lane >= off) scan += v;
+    }
+    bad = __any(bad);
+    if (lane == 63) s_wave[tid >> 6] = scan, s_bad[tid >> 6] = bad;
+    return scan;
+  };
+  int scan = count();
   if (tid == 0) s_rows = 0;
   __syncthreads();
+  bool bad = false;
+#pragma unroll
+  for (int w = 0; w < ML_THREADS / 64; ++w) bad |= s_bad[w] != 0;
+  if (bad) {   // a bound below an earlier one counts as that one: no row is in two groups
+    __syncthreads();
+    int top = bound[0];
+#pragma unroll
+    for (int i = 1; i <= kPer; ++i) top = max(top, bound[i]);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) top = max(top, __shfl_up(top, off, 64));   // lane < off: its own
+    if (lane == 63) s_top[tid >> 6] = top;
+    __syncthreads();
+    int before = __shfl_up(top, 1, 64);
+    if (lane == 0) before = 0;
+    for (int w = 0; w < tid >> 6; ++w) before = max(before, s_top[w]);
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) bound[i] = before = max(before, bound[i]);
+    scan = count();
+    __syncthreads();
+  }
   int at = scan - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < ML_THREADS / 64; ++w) {

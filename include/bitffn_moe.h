@@ -571,7 +571,8 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
  *   y[r][n] = sum_j A[src(r)][j] * W_g[n][j],   offsets[g] <= r < offsets[g+1]
  * A: n_mats = 1, its rows the tokens; W: one matrix per group (n_mats = G,
  * rows a multiple of 16), same cols.  offsets int32 [G+1] ascending (values
- * are clamped to [0, R]); NULL needs G = 1 and makes one group of all R rows.
+ * are clamped to [0, R], and one below an earlier one counts as that one);
+ * NULL needs G = 1 and makes one group of all R rows.
  * src(r) = row_src ? row_src[r] / src_div : r; row_src int32 [R] is for
  * instance moe_group_pairs' row_pair with src_div = k, so that a token's row is
  * stored once.  A row whose src lies outside A gives zeros.  Without row_src,

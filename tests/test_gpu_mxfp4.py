@@ -355,6 +355,27 @@ def test_descending_and_outside_bounds_are_clamped():
     assert (y[R:] == 7).all()
 
 
+@pytest.mark.parametrize("G,R,N,K", [(4, 20, 32, 64), (700, 900, 272, 96), (1024, 3000, 512, 64)])
+def test_descending_bounds_put_no_row_in_two_groups(G, R, N, K):
+    """Bounds in any order: one below an earlier one counts as that one, so
+    the result is that of their running maximum, with the same bits each time."""
+    bf = _bf()
+    dev = need_gpu()
+    rng = np.random.default_rng(G + R)
+    ac, as_, _ = _rand_mx(rng, R, K)
+    wc, ws, _ = _rand_mx(rng, G, N, K)
+    A, W = _dev(ac, as_), _dev(wc, ws)
+    off = np.sort(rng.integers(0, R, G + 1))
+    off[rng.integers(0, G + 1, G // 3 + 1)] = rng.integers(-9, R + 9, G // 3 + 1)
+    top = np.maximum.accumulate(np.clip(off, 0, R))
+    want = torch.full((R, N), 7.0, device=dev)
+    bf.mxfp4_linear(A, W, _i32(top), y=want)
+    for _ in range(3):
+        y = torch.full((R, N), 7.0, device=dev)
+        bf.mxfp4_linear(A, W, _i32(off), y=y)
+        assert torch.equal(y, want)
+
+
 def test_no_rows():
     bf = _bf()
     dev = need_gpu()
