@@ -757,6 +757,22 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(value, name):
+    """value as one of the library's 32-bit integers, which ctypes would cut to
+    its low bits if it were larger."""
+    i = int(value)
+    if i != value or not -0x80000000 <= i <= 0x7FFFFFFF:
+        raise ValueError(f"{name}: a 32-bit integer expected, got {value}")
+    return i
+
+
+def _sizes(what, *extents):
+    """The same for the extents of tensors (not negative): one check of all."""
+    for n in extents:
+        if n >> 31:
+            raise ValueError(f"{what}: sizes that fit 32-bit integers expected, got {n}")
+
+
 def _scratch(need, ws, dev):
     """(address, bytes, tensor to keep until the launch) of a workspace."""
     if ws is None:
@@ -784,6 +800,8 @@ class Mxfp4:
         """The shape, after a check that codes and scales belong together."""
         c, s = self.codes.shape, self.scales.shape
         n = len(c)
+        if n in (2, 3) and (c[0] | c[-2] | c[-1]) >> 30:   # cols is twice the last one
+            _sizes(name, c[0], c[-2], 2 * c[-1])
         if n == len(s) and 2 <= n <= 3 and c[-1] == 16 * s[-1] and c[-2] == s[-2] and c[0] == s[0]:
             return (1 if n == 2 else c[0], c[-2], 2 * c[-1])
         if n not in (2, 3):
@@ -808,7 +826,7 @@ class Mxfp4:
 
 
 def group_workspace_bytes(T: int, E: int) -> int:
-    return int(lib().moe_group_workspace_bytes(T, E))
+    return int(lib().moe_group_workspace_bytes(_c_int(T, "T"), _c_int(E, "E")))
 
 
 @_on_stream
@@ -830,7 +848,8 @@ def group_pairs(idx, n_experts, offsets=None, pair_pos=None, row_pair=None, ws=N
     Returns (offsets [E + 1], pair_pos [T, k], row_pair [T * k])."""
     _shape(idx, (None, None), "idx")
     T, k = idx.shape
-    E = int(n_experts)
+    E = _c_int(n_experts, "n_experts")
+    _sizes("idx", T, k)
     for t, shp, name in ((offsets, (E + 1,), "offsets"), (pair_pos, (T, k), "pair_pos"),
                          (row_pair, (T * k,), "row_pair")):
         if t is not None:
@@ -860,6 +879,7 @@ def mxfp4_quantize(x, out: Optional[Mxfp4] = None, stream=None) -> Mxfp4:
     cols = x.shape[-1]
     if cols % 32:
         raise ValueError(f"x: a last dimension that is a multiple of 32 expected, got {cols}")
+    _sizes("x", cols)
     dtype = _float_dtype(x.dtype, "x")
     lead = tuple(x.shape[:-1])
     if out is not None:
@@ -898,7 +918,7 @@ def _product(dev, stream, name, A, W, offsets, row_src, src_div, R, n_out, y, dt
     if y is None:
         y = torch.empty((R, n_out), dtype=dtype, device=dev)
     _check(getattr(lib(), name)(ctypes.byref(A), ctypes.byref(W), _addr(offsets), _addr(row_src),
-                                int(src_div), R, y.data_ptr(), y_dtype, stream), name)
+                                src_div, R, y.data_ptr(), y_dtype, stream), name)
     return y
 
 
@@ -919,6 +939,7 @@ def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
     if gated and N % 2:
         raise ValueError(f"{what}: an even number of rows of w expected, got {N}")
     n_out = N // 2 if gated else N
+    src_div = _c_int(src_div, "src_div")
     y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
     if y is not None:
         _dev(_shape(y, (R, n_out), "y"), y.dtype, "y")
@@ -953,7 +974,7 @@ def mxfp4_gate_up(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, h=N
 
 
 def mxfp4_ffn_decode_workspace_bytes(T: int, k: int, d_ff: int) -> int:
-    return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, d_ff))
+    return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(_c_int(T, "T"), _c_int(k, "k"), _c_int(d_ff, "d_ff")))
 
 
 @_on_stream
@@ -961,7 +982,7 @@ def _mx_decode(dev, stream, GU, D, shared_slot, x, T, d, k, f, slot, w, y, ws):
     if y is None:
         y = torch.empty((T, d), dtype=torch.float32, device=dev)
     wp, wn, keep = _scratch(lib().moe_mxfp4_ffn_decode_workspace_bytes(T, k, f), ws, dev)
-    _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), int(shared_slot),
+    _check(lib().moe_mxfp4_ffn_decode(ctypes.byref(GU), ctypes.byref(D), shared_slot,
                                       x.data_ptr(), T, k, slot.data_ptr(), w.data_ptr(),
                                       y.data_ptr(), wp, wn, stream), "moe_mxfp4_ffn_decode")
     return y
@@ -980,6 +1001,8 @@ def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=
     _shape(slot, (T, None), "slot")
     k = slot.shape[1]
     _shape(w, (T, k), "w")
+    _sizes("mxfp4_ffn_decode", T, k)
+    shared_slot = _c_int(shared_slot, "shared_slot")
     if y is not None:
         _dev(_shape(y, (T, d), "y"), torch.float32, "y")
     if ws is not None:
@@ -1013,6 +1036,8 @@ def _balance_args(logits, idx, seq_offsets, mask):
         _shape(seq_offsets, (None,), "seq_offsets")
         if seq_offsets.shape[0] < 2:
             raise ValueError("seq_offsets: at least 2 elements expected")
+    k, S = idx.shape[1], 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    _sizes("logits, idx, seq_offsets", T, E, k, S)
     if mask is not None:
         _shape(mask, (T,), "mask")
         if mask.dtype not in (torch.uint8, torch.bool):
@@ -1023,11 +1048,11 @@ def _balance_args(logits, idx, seq_offsets, mask):
         _dev(seq_offsets, torch.int32, "seq_offsets")
     if mask is not None:
         _dev(mask, mask.dtype, "mask")
-    return T, E, idx.shape[1], 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    return T, E, k, S
 
 
 def route_balance_workspace_bytes(T: int, E: int, n_seq: int) -> int:
-    return int(lib().moe_route_balance_workspace_bytes(T, E, n_seq))
+    return int(lib().moe_route_balance_workspace_bytes(_c_int(T, "T"), _c_int(E, "E"), _c_int(n_seq, "n_seq")))
 
 
 @_on_stream
