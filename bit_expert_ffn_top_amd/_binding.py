@@ -22,6 +22,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EFORMAT, MOE_ENOSPC, MOE_EHIP = 0, -1, -2, -3, -4, -5
 FMT_Q2S, FMT_Q2SM, FMT_Q3G = 1, 2, 3
 DTYPE_F32, DTYPE_BF16 = 0, 1
+MAX_MX_OUT = 65536   # rows of the weight matrix of a 4-bit product (MOE_MAX_MX_OUT)
 
 # every symbol the header declares, with its ctypes signature
 _c_int, _c_i64, _c_sz, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -929,6 +930,8 @@ def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
         raise ValueError(f"{what}: a holds one matrix, got {na}")
     if K != Kw:
         raise ValueError(f"{what}: a has {K} columns, w {Kw}")
+    if N > MAX_MX_OUT:
+        raise ValueError(f"w: at most {MAX_MX_OUT} rows expected, got {N}")
     if offsets is not None:
         _shape(offsets, (G + 1,), "offsets")
     elif G != 1:
@@ -958,7 +961,8 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=No
                  dtype=torch.float32, stream=None):
     """y[r] = a[src(r)] . w[g]^T for the rows r of group g (moe_mxfp4_linear).
 
-    a [rows, K]; w [G, N, K] (or [N, K]); offsets int32 [G + 1] bounds of the
+    a [rows, K]; w [G, N, K] (or [N, K]), N a multiple of 16 and at most 65536
+    (a larger matrix goes in slices of its rows); offsets int32 [G + 1] bounds of the
     groups (None: one group); row_src int32 [R] with src(r) = row_src[r] //
     src_div (None: r).  Returns y [R, N] in dtype; rows of no group are left as
     they were (undefined in a y allocated here)."""
@@ -968,7 +972,7 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=No
 def mxfp4_gate_up(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, h=None,
                   dtype=torch.bfloat16, stream=None):
     """h[r] = silu(gate) * up of the product with w [G, 2 F, K], gate rows even,
-    up rows odd (moe_mxfp4_gate_up).  Returns h [R, F]; arguments as
+    up rows odd, 2 F a multiple of 64 and at most 65536 (moe_mxfp4_gate_up).  Returns h [R, F]; arguments as
     mxfp4_linear."""
     return _mx_product("mxfp4_gate_up", True, a, w, offsets, row_src, src_div, h, dtype, stream)
 

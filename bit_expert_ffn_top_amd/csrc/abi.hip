@@ -131,7 +131,7 @@ int mx_product(const moe_mxfp4* A, const moe_mxfp4* W, const int32_t* offsets,
   st = check_mxfp4(W);
   if (st != MOE_OK) return st;
   if (A->n_mats != 1 || A->cols != W->cols || !valid_dtype(y_dtype)) return MOE_EINVAL;
-  if (W->rows > 65536 || W->rows % (gated ? 64 : 16) != 0) return MOE_EINVAL;
+  if (W->rows > MOE_MAX_MX_OUT || W->rows % (gated ? 64 : 16) != 0) return MOE_EINVAL;
   if (R < 0 || R > kMaxMxRows || src_div < 1) return MOE_EINVAL;
   if (!offsets && W->n_mats != 1) return MOE_EINVAL;
   if (!row_src && R > A->rows) return MOE_EINVAL;

@@ -540,6 +540,7 @@ int moe_group_pairs(const int32_t* idx, int T, int k, int E, int32_t* offsets,
  * cols is a multiple of 32 in 32..MOE_MAX_MX_COLS, both pointers are 16-byte
  * aligned device memory.  A host struct, read during the call only. */
 #define MOE_MAX_MX_COLS 16384
+#define MOE_MAX_MX_OUT 65536   /* rows of a product's weight matrix */
 typedef struct moe_mxfp4 {
   int32_t n_mats;     /* 1..MOE_MAX_EXPERTS             */
   int32_t rows;       /* 1..2^24 - 1                    */
@@ -570,7 +571,8 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
  * 4-bit format, sums in fp32, the result rounded once to y_dtype:
  *   y[r][n] = sum_j A[src(r)][j] * W_g[n][j],   offsets[g] <= r < offsets[g+1]
  * A: n_mats = 1, its rows the tokens; W: one matrix per group (n_mats = G,
- * rows a multiple of 16), same cols.  offsets int32 [G+1] ascending (values
+ * rows a multiple of 16, at most MOE_MAX_MX_OUT: a larger matrix in slices of
+ * its rows), same cols.  offsets int32 [G+1] ascending (values
  * are clamped to [0, R], and one below an earlier one counts as that one);
  * NULL needs G = 1 and makes one group of all R rows.
  * src(r) = row_src ? row_src[r] / src_div : r; row_src int32 [R] is for
