@@ -758,7 +758,7 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _c_int(value, name):
+def _int32(value, name):
     """value as one of the library's 32-bit integers, which ctypes would cut to
     its low bits if it were larger."""
     i = int(value)
@@ -827,7 +827,7 @@ class Mxfp4:
 
 
 def group_workspace_bytes(T: int, E: int) -> int:
-    return int(lib().moe_group_workspace_bytes(_c_int(T, "T"), _c_int(E, "E")))
+    return int(lib().moe_group_workspace_bytes(_int32(T, "T"), _int32(E, "E")))
 
 
 @_on_stream
@@ -849,7 +849,7 @@ def group_pairs(idx, n_experts, offsets=None, pair_pos=None, row_pair=None, ws=N
     Returns (offsets [E + 1], pair_pos [T, k], row_pair [T * k])."""
     _shape(idx, (None, None), "idx")
     T, k = idx.shape
-    E = _c_int(n_experts, "n_experts")
+    E = _int32(n_experts, "n_experts")
     _sizes("idx", T, k)
     for t, shp, name in ((offsets, (E + 1,), "offsets"), (pair_pos, (T, k), "pair_pos"),
                          (row_pair, (T * k,), "row_pair")):
@@ -942,7 +942,7 @@ def _mx_product(what, gated, a, w, offsets, row_src, src_div, y, dtype, stream):
     if gated and N % 2:
         raise ValueError(f"{what}: an even number of rows of w expected, got {N}")
     n_out = N // 2 if gated else N
-    src_div = _c_int(src_div, "src_div")
+    src_div = _int32(src_div, "src_div")
     y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
     if y is not None:
         _dev(_shape(y, (R, n_out), "y"), y.dtype, "y")
@@ -978,7 +978,7 @@ def mxfp4_gate_up(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, h=N
 
 
 def mxfp4_ffn_decode_workspace_bytes(T: int, k: int, d_ff: int) -> int:
-    return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(_c_int(T, "T"), _c_int(k, "k"), _c_int(d_ff, "d_ff")))
+    return int(lib().moe_mxfp4_ffn_decode_workspace_bytes(_int32(T, "T"), _int32(k, "k"), _int32(d_ff, "d_ff")))
 
 
 @_on_stream
@@ -1006,7 +1006,7 @@ def mxfp4_ffn_decode(gate_up: Mxfp4, down: Mxfp4, x, slot, w, shared_slot=-1, y=
     k = slot.shape[1]
     _shape(w, (T, k), "w")
     _sizes("mxfp4_ffn_decode", T, k)
-    shared_slot = _c_int(shared_slot, "shared_slot")
+    shared_slot = _int32(shared_slot, "shared_slot")
     if y is not None:
         _dev(_shape(y, (T, d), "y"), torch.float32, "y")
     if ws is not None:
@@ -1056,7 +1056,7 @@ def _balance_args(logits, idx, seq_offsets, mask):
 
 
 def route_balance_workspace_bytes(T: int, E: int, n_seq: int) -> int:
-    return int(lib().moe_route_balance_workspace_bytes(_c_int(T, "T"), _c_int(E, "E"), _c_int(n_seq, "n_seq")))
+    return int(lib().moe_route_balance_workspace_bytes(_int32(T, "T"), _int32(E, "E"), _int32(n_seq, "n_seq")))
 
 
 @_on_stream
