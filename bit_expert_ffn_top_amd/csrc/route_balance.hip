@@ -34,6 +34,7 @@ constexpr int RB_SINGLE_ROWS = 64;    // single launch: rows and sequences
 constexpr int RB_SINGLE_SEQS = 4;
 constexpr int RB_ETILE = 128;         // experts per workgroup of the second launch
 constexpr int RB_SUBS = 8;
+constexpr int RB_FOLD = 64;           // rows a wavefront adds up before they join its total
 
 struct BalanceArgs {
   const float* logits;
@@ -48,7 +49,7 @@ struct BalanceArgs {
   // workspace
   float* p_part;          // [chunks + S][E]
   int32_t* c_part;        // [chunks + S][E]
-  float* z_part;          // [chunks + S]
+  double* z_part;         // [chunks + S]
   int32_t* n_part;        // [chunks + S]
   double* l_part;         // [S][etiles]
   uint32_t* done;         // [S]
@@ -179,20 +180,21 @@ struct Row {
 };
 
 // The losses of a sequence from its sums.
-__device__ __forceinline__ void write_losses(const BalanceArgs& a, int s, int n, double cp, float zs) {
+__device__ __forceinline__ void write_losses(const BalanceArgs& a, int s, int n, double cp, double zs) {
   const double dn = n;
   a.balance[s] = n > 0 ? static_cast<float>(cp * a.E / (dn * dn * a.k)) : 0.0f;
   a.z[s] = n > 0 ? static_cast<float>(zs / dn) : 0.0f;
   a.n_tokens[s] = n;
 }
 
-// SINGLE: one workgroup does everything.
-template <int VEC, int NC, bool SINGLE>
+// SINGLE: one workgroup does everything.  FOLD: a wavefront may have more than
+// RB_FOLD rows.
+template <int VEC, int NC, bool SINGLE, bool FOLD>
 __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a) {
   extern __shared__ float lds[];
   float* s_p = lds;                                                 // [RB_HALF][E]
   int32_t* s_c = reinterpret_cast<int32_t*>(lds + RB_HALF * a.E);   // [E]
-  __shared__ float s_z[RB_WAVES];
+  __shared__ double s_z[RB_WAVES];
   __shared__ int s_n[RB_WAVES];
   __shared__ double s_l[RB_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -210,8 +212,12 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
       if (b0 >= b1) continue;
     }
     for (int e = tid; e < E; e += RB_THREADS) s_c[e] = 0;
-    float acc[NC][VEC] = {};
-    float zs = 0.0f;
+    // Probabilities in fp32: RB_FOLD rows at a time, whose sums join a total, so
+    // that a sum's error does not grow with the rows (16.8 million equal rows of
+    // 37 experts: 936 units of 2^-24 without, 9 with).  Squares of lse in 64 bits: one a row,
+    // and the sum of those whose mean is finite may not be.
+    float acc[NC][VEC] = {}, total[NC][VEC] = {};
+    double zs = 0.0;
     int n = 0;
     // the next row is on its way while one is worked on
     Row<VEC, NC> r, ahead;
@@ -242,8 +248,22 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[c][j] = fmaf(r.v[c][j], inv, acc[c][j]);
-      zs += finite(lse) ? lse * lse : 0.0f;
+      zs += finite(lse) ? static_cast<double>(lse) * lse : 0.0;
       ++n;
+      if constexpr (FOLD) {
+        if (n % RB_FOLD == 0) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) total[c][j] += acc[c][j], acc[c][j] = 0.0f;
+        }
+      }
+    }
+    if constexpr (FOLD) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[c][j] += total[c][j];
     }
     // wavefronts 8..15 hand their sums to 0..7, whose sums then meet below
     // (half the LDS of all sixteen at once: two workgroups fit a CU)
@@ -284,7 +304,7 @@ __global__ __launch_bounds__(RB_THREADS) void balance_rows_kernel(BalanceArgs a)
       __syncthreads();
     }
     if (tid == 0) {
-      float zz = 0.0f;
+      double zz = 0.0;
       int nn = 0;
       for (int w = 0; w < RB_WAVES; ++w) {
         zz += s_z[w];
@@ -314,7 +334,7 @@ __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(Bala
   const int c0 = b0 / a.chunk_rows, c1 = b1 > b0 ? (b1 - 1) / a.chunk_rows + 1 : c0;
   // the sequence's z and row count (lanes over its chunks), in the first
   // wavefront of every workgroup: whichever needs them has them at hand
-  float zs = 0.0f;
+  double zs = 0.0;
   int n = 0;
   if (tid < 64) {
     for (int q = c0 + tid; q < c1; q += 64) {
@@ -353,9 +373,11 @@ __global__ __launch_bounds__(RB_ETILE * RB_SUBS) void balance_reduce_kernel(Bala
   }
   __syncthreads();
   if (tid >= 64) return;
-  zs = wave_sum(zs);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, 64);
+  for (int off = 32; off >= 1; off >>= 1) {
+    zs += __shfl_xor(zs, off, 64);
+    n += __shfl_xor(n, off, 64);
+  }
   double l = 0.0;
   for (int i = 0; i < RB_ETILE / 64; ++i) l += s_l[i];
   if (a.n_etiles > 1) {
@@ -545,7 +567,7 @@ BalanceSpace balance_space(int T, int E, int S) {
   b.p = 0;
   b.c = b.p + align256(np * E * 4);
   b.z = b.c + align256(np * E * 4);
-  b.n = b.z + align256(np * 4);
+  b.n = b.z + align256(np * 8);
   b.l = b.n + align256(np * 4);
   b.done = b.l + align256(static_cast<int64_t>(S) * b.n_etiles * 8);
   b.total = b.done + align256(static_cast<int64_t>(S) * 4);
@@ -557,10 +579,13 @@ hipError_t run_forward(BalanceArgs& a, hipStream_t st) {
   const size_t lds = static_cast<size_t>(RB_HALF + 1) * a.E * 4;
   if (balance_single(a.T, a.S)) {
     a.chunk_rows = RB_SINGLE_ROWS;
-    balance_rows_kernel<VEC, NC, true><<<1, RB_THREADS, lds, st>>>(a);
+    balance_rows_kernel<VEC, NC, true, false><<<1, RB_THREADS, lds, st>>>(a);
     return hipGetLastError();
   }
-  balance_rows_kernel<VEC, NC, false><<<a.n_chunks, RB_THREADS, lds, st>>>(a);
+  if (a.chunk_rows > RB_WAVES * RB_FOLD)   // more than 262,144 rows
+    balance_rows_kernel<VEC, NC, false, true><<<a.n_chunks, RB_THREADS, lds, st>>>(a);
+  else
+    balance_rows_kernel<VEC, NC, false, false><<<a.n_chunks, RB_THREADS, lds, st>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   balance_reduce_kernel<<<static_cast<unsigned>(a.S) * a.n_etiles, RB_ETILE * RB_SUBS, 0, st>>>(a);
@@ -591,7 +616,7 @@ hipError_t launch_route_balance(const float* logits, const int32_t* idx, int T, 
   char* p = static_cast<char*>(ws);
   BalanceArgs a{logits, idx, seq, mask, balance, z, counts, prob_sum, n_tokens,
                 reinterpret_cast<float*>(p + b.p), reinterpret_cast<int32_t*>(p + b.c),
-                reinterpret_cast<float*>(p + b.z), reinterpret_cast<int32_t*>(p + b.n),
+                reinterpret_cast<double*>(p + b.z), reinterpret_cast<int32_t*>(p + b.n),
                 reinterpret_cast<double*>(p + b.l), reinterpret_cast<uint32_t*>(p + b.done),
                 T, E, k, S, b.chunk_rows, b.n_chunks, b.n_etiles};
   if (E % 4 == 0) {
