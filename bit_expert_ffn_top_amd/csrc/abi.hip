@@ -4,6 +4,7 @@
 
 #include "bitffn_moe.h"
 #include <atomic>
+#include <initializer_list>
 
 #include "moe_internal.h"
 
@@ -108,6 +109,19 @@ int check_decode_layer(const moe_layer* L, const float* x, int T, const float* l
 
 bool valid_dtype(int t) { return t == MOE_DTYPE_F32 || t == MOE_DTYPE_BF16; }
 
+// No buffer that a call writes is another of its buffers, written or read (null
+// ones are none).
+bool apart(std::initializer_list<const void*> written, std::initializer_list<const void*> read) {
+  for (const void* const* w = written.begin(); w != written.end(); ++w) {
+    if (!*w) continue;
+    for (const void* const* o = written.begin(); o != w; ++o)
+      if (*o == *w) return false;
+    for (const void* r : read)
+      if (r == *w) return false;
+  }
+  return true;
+}
+
 constexpr int64_t kMaxMxRows = (int64_t{1} << 24) - 1;
 
 bool valid_mx_cols(int cols) { return cols >= 32 && cols <= MOE_MAX_MX_COLS && cols % 32 == 0; }
@@ -136,7 +150,8 @@ int mx_product(const moe_mxfp4* A, const moe_mxfp4* W, const int32_t* offsets,
   if (!offsets && W->n_mats != 1) return MOE_EINVAL;
   if (!row_src && R > A->rows) return MOE_EINVAL;
   if (R == 0) return MOE_OK;
-  if (!y || y == A->codes || y == A->scales || y == W->codes || y == W->scales) return MOE_EINVAL;
+  if (!y || !apart({y}, {A->codes, A->scales, W->codes, W->scales, offsets, row_src}))
+    return MOE_EINVAL;
   if ((offsets && !aligned16(offsets)) || (row_src && !aligned16(row_src)) || !aligned16(y))
     return MOE_EALIGN;
   return hip_status(
@@ -536,6 +551,7 @@ int moe_group_pairs(const int32_t* idx, int T, int k, int E, int32_t* offsets, i
       !aligned16(row_pair) || !aligned256(ws))
     return MOE_EALIGN;
   if (ws_bytes < bitffn::group_workspace_bytes(T, E)) return MOE_ENOSPC;
+  if (!apart({offsets, pair_pos, row_pair, ws}, {idx})) return MOE_EINVAL;
   // the ids themselves as slots: a pair is selected where 0 <= id < E
   const bitffn::GroupWorkspace gws = bitffn::group_workspace(ws, T, E);
   return hip_status(bitffn::launch_group_pairs(idx, idx, nullptr, T, k, E, true, E, gws, offsets,
@@ -550,6 +566,7 @@ int moe_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int cols, uint8
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_EINVAL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_EALIGN;
+  if (!apart({codes, scales}, {x})) return MOE_EINVAL;
   return hip_status(bitffn::launch_mx_quantize(x, x_dtype, rows, cols, codes, scales, stream));
 }
 
@@ -560,6 +577,7 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !y) return MOE_EINVAL;
   if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MOE_EALIGN;
+  if (!apart({y}, {codes, scales})) return MOE_EINVAL;
   return hip_status(bitffn::launch_mx_dequantize(codes, scales, rows, cols, y, y_dtype, stream));
 }
 
@@ -600,6 +618,7 @@ int moe_mxfp4_ffn_decode(const moe_mxfp4* GU, const moe_mxfp4* D, int shared_slo
     return MOE_EALIGN;
   if (!aligned256(ws)) return MOE_EALIGN;
   if (ws_bytes < bitffn::mx_decode_workspace_bytes(T, k, D->cols)) return MOE_ENOSPC;
+  if (!apart({y, ws}, {GU->codes, GU->scales, D->codes, D->scales, x, slot, w})) return MOE_EINVAL;
   return hip_status(bitffn::launch_mx_decode(*GU, *D, shared_slot, x, T, k, slot, w, y, ws, stream));
 }
 
@@ -621,6 +640,9 @@ int moe_route_balance(const float* logits, const int32_t* idx, int T, int E, int
       !aligned16(n_tokens) || (need > 0 && !aligned256(ws)))
     return MOE_EALIGN;
   if (ws_bytes < need) return MOE_ENOSPC;
+  if (!apart({balance, z, counts, prob_sum, n_tokens, need > 0 ? ws : nullptr},
+             {logits, idx, seq_offsets, mask}))
+    return MOE_EINVAL;
   return hip_status(bitffn::launch_route_balance(logits, idx, T, E, k, seq_offsets, n_seq, mask,
                                                  balance, z, counts, prob_sum, n_tokens, ws,
                                                  stream));

@@ -523,7 +523,10 @@ int moe_combine(const void* x, int x_dtype, int T, int d, int k,
  *   row_pair  int32 [T*k]   t*k+i of every row; entries past offsets[E] are
  *                           left as they were
  * Limits: 1 <= T <= 65536, 1 <= k <= MOE_MAX_TOPK, 1 <= E <= MOE_MAX_EXPERTS.
- * ws: at least moe_group_workspace_bytes(T, E) bytes, 256-byte aligned. */
+ * ws: at least moe_group_workspace_bytes(T, E) bytes, 256-byte aligned.
+ * Here and in every call below, what a call writes (its workspace too) may
+ * overlap nothing else that it reads or writes; the same address twice is
+ * refused (MOE_EINVAL). */
 size_t moe_group_workspace_bytes(int T, int E);
 int moe_group_pairs(const int32_t* idx, int T, int k, int E, int32_t* offsets,
                     int32_t* pair_pos, int32_t* row_pair, void* ws,
