@@ -19,12 +19,13 @@
 // load are neighbours.
 // Products and sums in fp32, each in an order that no other token changes.
 //
-// Bound: HBM (the weights, 17/32 byte per value); what is above it is latency, so
-// whatever does not depend on a load is asked for before it: x before the slots,
-// the last step's weights and x before the rows, the next expert's rows before
-// the present ones are used.  10 of 512 experts and the shared one, d = 2048,
-// F = 768: one token 6.4 + 4.4 us (27.6 MB: 2.6 TB/s), four tokens over 34
-// experts 15.0 + 12.2 us (86 MB: 3.2 TB/s).  The matrix cores were tried in place
+// Bound: the reads of the weights (17/32 byte per value); what is above it is
+// latency, so whatever does not depend on a load is asked for before it: x before
+// the slots, the last step's weights and x before the rows, the next expert's rows
+// before the present ones are used.  10 of 128 experts and the shared one, d = 2048,
+// F = 768, the same ones again and again (so from the last-level cache): one
+// token 6.2 + 4.8 us (27.6 MB: 2.5 TB/s), four tokens over 34 experts
+// 14.4 + 11.9 us (86 MB: 3.3 TB/s).  The matrix cores were tried in place
 // of the vector unit (activations as three bfloat16 parts): 10.7 + 13.6 and
 // 22.4 + 30.0 us, for the parts' traffic through LDS.
 #include "moe_internal.h"
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(MD_UP_THREADS) void mx_decode_gate_up_kernel(Decode
 #pragma unroll
       for (int r = 0; r < MD_UP_ROWS; ++r) before[r] = sum[r];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {   // half a block's activations at a time: registers for six wavefronts
+      for (int half = 0; half < 2; ++half) {   // half a block's activations at a time: 90 registers, five wavefronts a SIMD
         df4 v[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] = s_x[8 * bc + ((4 * half + c) ^ md_swz(bc))];

@@ -173,8 +173,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Four consecutive output columns of a row, stored at p.  GATED: the columns
-// are (gate, up, gate, up) and two values are stored.
 // silu(z) = z / (1 + e^-z).  The product with log2(e) is carried in two parts,
 // so the exponential is good to about 2 units in the last place for every z;
 // the hardware's exponential and reciprocal are each good to 1.  Past +-126
@@ -187,6 +185,8 @@ __device__ __forceinline__ float silu_hw(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
+// Four consecutive output columns of a row, put at p in LDS.  GATED: the columns
+// are (gate, up, gate, up) and two values are put there.
 template <bool GATED, bool BF16>
 __device__ __forceinline__ void put_out(__attribute__((address_space(3))) uint8_t* p, mf4 v) {
   typedef float f2 __attribute__((ext_vector_type(2)));
@@ -203,6 +203,7 @@ __device__ __forceinline__ void put_out(__attribute__((address_space(3))) uint8_
   }
 }
 
+// The same, stored at p in memory.
 template <bool GATED, bool BF16>
 __device__ __forceinline__ void store_out(uint8_t* p, mf4 v) {
   if constexpr (GATED) {
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 // The MFMA wants row l % 16 in lane l, so a load straight into its operands
 // would touch 64 places with 16 bytes each, and the path from the caches, which
 // takes 64 contiguous bytes of four neighbouring lanes at a time, would be the
-// bound (measured: its return path busy 92% of the time).  Everything is
+// bound (gate/up of 81,920 rows: 437 us so, 336 as below).  Everything is
 // therefore loaded as it lies, 8 rows of 128 bytes per instruction, and changes
 // lanes in LDS, 16-byte piece p of row r at position p ^ swz(r), which spreads
 // the 16 rows that a read of one piece touches over all banks:
@@ -437,12 +438,18 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 // The products of 2, 4, 6 or 8 token tiles are code of their own.
 //
 // Measured: gate/up of 81,920 rows over 512 experts, 1536 x 2048, bf16 out:
-// 273 us, 1.9 PFLOP/s and 3.6 TB/s; down, 2048 x 768, fp32 out: 296 us, 3.8 TB/s
-// (671 MB of them stores); 640 rows over some 365 of those gate/up experts: 74 us,
-// 8 TB/s, part of it from the last-level cache.  What is left is waits: two
-// wavefronts per SIMD (256 registers each) do not cover a step's loads where
-// rows are short, and a slice's stores are waited for with the loads behind
-// them.
+// 281 us a call, 1.8 PFLOP/s and 3.5 TB/s, the matrix cores busy 22% of the time;
+// down, 2048 x 768, fp32 out: 298 us, 3.8 TB/s (671 MB of them stores), busy 10%;
+// 640 rows over some 365 of those gate/up experts: 77 us, 8 TB/s, part of it from
+// the last-level cache.  Rows of 704 or 2016 columns, whose scales come by bytes:
+// 449 and 621 us where 768 and 2048 take 283 and 281.
+// What is left, by the compiled code and the counters: two wavefronts per SIMD
+// (256 registers each) of which each step waits for the next step's tokens
+// before it asks for the next weights, because the compiler cannot tell the LDS
+// that those loads write from the LDS it reads next; and registers that spill,
+// 23 to 50 of them where a row is a multiple of 128 columns, 185 to 230 where it
+// is not, which go to memory (8192 x 2048 x 768, bf16: 58 MB written for 34 MB of
+// results) and whose reloads wait for the stores of a slice before them.
 constexpr int MG_TILES = 4;              // of 16 weight rows per wavefront
 constexpr int MG_ROWS = 4 * 16 * MG_TILES;
 constexpr int MG_STEP = 256;             // columns per step
@@ -475,9 +482,9 @@ struct MgLane {
   bool stream;           // nobody else reads these weights: they need not stay in the caches
 };
 
-// 16 scale bytes as loaded.  G: the largest power of two up to 8 that divides
-// the blocks of a row, so that a load of G bytes is aligned and lies wholly
-// inside or outside the buffer.
+// 16 scale bytes as loaded, G at a time: 8 or 4 where that divides the blocks of
+// a row, else 1, so that a load is aligned and lies wholly inside or outside the
+// buffer.
 template <int G>
 struct MgScales {
   uint32_t v[G == 1 ? 16 : 4];

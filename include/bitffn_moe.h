@@ -582,7 +582,11 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
  * instance moe_group_pairs' row_pair with src_div = k, so that a token's row is
  * stored once.  A row whose src lies outside A gives zeros.  Without row_src,
  * R may not exceed A's rows.  y [R][W rows] fp32 or bf16; rows in no group are
- * left as they were.  0 <= R < 2^24, src_div >= 1.  y may not alias A or W. */
+ * left as they were.  0 <= R < 2^24, src_div >= 1.  y may not alias A or W.
+ * A call repeated gives the same bits.  The order in which a row is summed (and
+ * with it the last bits) depends on R, on the sizes of A and W and on the device's
+ * number of compute units: a row alone need not have the bits that it has among
+ * others. */
 int moe_mxfp4_linear(const moe_mxfp4* A, const moe_mxfp4* W,
                      const int32_t* offsets, const int32_t* row_src,
                      int src_div, int64_t R, void* y, int y_dtype,
