@@ -438,7 +438,7 @@ __global__ __launch_bounds__(ML_THREADS) void mx_linear_rows_kernel(LinearArgs a
 // The products of 2, 4, 6 or 8 token tiles are code of their own.
 //
 // Measured: gate/up of 81,920 rows over 512 experts, 1536 x 2048, bf16 out:
-// 281 us a call, 1.8 PFLOP/s and 3.5 TB/s, the matrix cores busy 22% of the time;
+// 281 us a call, 1.8 PFLOP/s and 3.5 TB/s, the matrix cores busy 23% of the time;
 // down, 2048 x 768, fp32 out: 298 us, 3.8 TB/s (671 MB of them stores), busy 10%;
 // 640 rows over some 365 of those gate/up experts: 77 us, 8 TB/s, part of it from
 // the last-level cache.  Rows of 704 or 2016 columns, whose scales come by bytes:
