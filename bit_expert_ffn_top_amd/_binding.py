@@ -972,8 +972,8 @@ def mxfp4_linear(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, y=No
 def mxfp4_gate_up(a: Mxfp4, w: Mxfp4, offsets=None, row_src=None, src_div=1, h=None,
                   dtype=torch.bfloat16, stream=None):
     """h[r] = silu(gate) * up of the product with w [G, 2 F, K], gate rows even,
-    up rows odd, 2 F a multiple of 64 and at most 65536 (moe_mxfp4_gate_up).  Returns h [R, F]; arguments as
-    mxfp4_linear."""
+    up rows odd, 2 F a multiple of 64 and at most 65536 (moe_mxfp4_gate_up).
+    Returns h [R, F]; arguments as mxfp4_linear."""
     return _mx_product("mxfp4_gate_up", True, a, w, offsets, row_src, src_div, h, dtype, stream)
 
 
