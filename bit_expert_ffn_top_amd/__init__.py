@@ -14,4 +14,6 @@ from ._binding import (  # noqa: F401
     Mxfp4, RouteBalance, group_pairs, group_workspace_bytes, mxfp4_dequantize, mxfp4_ffn_decode,
     mxfp4_ffn_decode_workspace_bytes, mxfp4_gate_up, mxfp4_linear, mxfp4_quantize, route_backward,
     route_balance, route_balance_workspace_bytes,
+    Dispatch, combine_backward, combine_rows, dispatch, dispatch_backward, dispatch_workspace_bytes, lora,
+    verify_drafts, verify_drafts_workspace_bytes,
 )

@@ -23,6 +23,7 @@ MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EFORMAT, MOE_ENOSPC, MOE_EHIP = 0, -1, -2, -
 FMT_Q2S, FMT_Q2SM, FMT_Q3G = 1, 2, 3
 DTYPE_F32, DTYPE_BF16 = 0, 1
 MAX_MX_OUT = 65536   # rows of the weight matrix of a 4-bit product (MOE_MAX_MX_OUT)
+MAX_DRAFTS = 63      # drafted tokens of a request (MOE_MAX_DRAFTS)
 
 # every symbol the header declares, with its ctypes signature
 _c_int, _c_i64, _c_sz, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -110,6 +111,18 @@ SIGNATURES = {
                                    _vp, _vp, _vp, _vp, _c_sz, _vp]),
     "moe_route_backward": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
                                     _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_dispatch_workspace_bytes": (_c_sz, [_c_int, _c_int, _c_int]),
+    "moe_dispatch": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                              _c_sz, _vp]),
+    "moe_combine_rows": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int,
+                                  _vp, _c_int, _vp]),
+    "moe_combine_backward": (_c_int, [_vp, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _vp,
+                                      _vp, _vp, _vp, _vp]),
+    "moe_lora": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp,
+                          _c_int, _vp, _vp, _vp, _c_int, _vp]),
+    "moe_verify_drafts_workspace_bytes": (_c_sz, [_c_int, _c_int]),
+    "moe_verify_drafts": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _c_sz, _vp]),
 }
 
 _lib = None
@@ -1123,3 +1136,229 @@ def route_backward(logits, idx, counts=None, n_tokens=None, g_balance=None, g_z=
                            (logits, idx, seq_offsets, mask, counts, n_tokens, g_balance, g_z, w, dw, dlogits),
                            logits, idx, T, E, k, seq_offsets, S, mask, counts, n_tokens, g_balance, g_z,
                            w, dw, dlogits)
+
+
+# --- tokens to the experts and back, adapters, drafted tokens --------------------
+
+
+def _tensors(checks):
+    """Checks (tensor or None, shape, type, name): all shapes, then places and types."""
+    for t, shape, _, name in checks:
+        if t is not None and t.shape != shape:
+            _shape(t, shape, name)
+    for t, _, dtype, name in checks:
+        if t is not None and not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+            _dev(t, dtype, name)
+
+
+class Dispatch(NamedTuple):
+    """What dispatch returns."""
+    rows: torch.Tensor        # [T * k, d], x's type
+    offsets: torch.Tensor     # int32 [E + 1]
+    pair_pos: torch.Tensor    # int32 [T, k]
+
+
+def dispatch_workspace_bytes(T: int, k: int, E: int) -> int:
+    return int(lib().moe_dispatch_workspace_bytes(_int32(T, "T"), _int32(k, "k"), _int32(E, "E")))
+
+
+@_on_stream
+def _dispatch(dev, stream, x, dtype, T, d, idx, k, E, rows, offsets, pair_pos, ws):
+    if rows is None:
+        rows = torch.empty((T * k, d), dtype=x.dtype, device=dev)
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    if pair_pos is None:
+        pair_pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    wp, wn, keep = _scratch(lib().moe_dispatch_workspace_bytes(T, k, E), ws, dev)
+    _check(lib().moe_dispatch(x.data_ptr(), dtype, T, d, idx.data_ptr(), k, E, rows.data_ptr(),
+                              offsets.data_ptr(), pair_pos.data_ptr(), wp, wn, stream), "moe_dispatch")
+    return Dispatch(rows, offsets, pair_pos)
+
+
+def dispatch(x, idx, n_experts, rows=None, offsets=None, pair_pos=None, ws=None, stream=None) -> Dispatch:
+    """A row for every pair of idx int32 [T, k], groups ascending by expert: the
+    token's row of x [T, d] (fp32 or bf16) (moe_dispatch).  Pairs whose id lies
+    outside [0, n_experts) have none (pair_pos -1), and the rows past offsets[E]
+    are left as they were (undefined in rows allocated here)."""
+    dtype = _float_dtype(x.dtype, "x")
+    _shape(x, (None, None), "x")
+    T, d = x.shape
+    _shape(idx, (T, None), "idx")
+    k = idx.shape[1]
+    E = _int32(n_experts, "n_experts")
+    _sizes("x, idx", T, d, k, T * k)
+    _tensors(((rows, (T * k, d), x.dtype, "rows"), (offsets, (E + 1,), torch.int32, "offsets"),
+              (pair_pos, (T, k), torch.int32, "pair_pos"), (x, (T, d), x.dtype, "x"), (idx, (T, k), torch.int32, "idx")))
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
+    return _dispatch("dispatch", stream, (x, idx, rows, offsets, pair_pos, ws), x, dtype, T, d, idx, k, E,
+                     rows, offsets, pair_pos, ws)
+
+
+@_on_stream
+def _combine_rows(dev, stream, rows, rows_dtype, R, T, d, k, pair_pos, w, base, base_dtype, y, dtype, y_dtype):
+    if y is None:
+        y = torch.empty((T, d), dtype=dtype, device=dev)
+    _check(lib().moe_combine_rows(rows.data_ptr(), rows_dtype, R, T, d, k, pair_pos.data_ptr(), _addr(w),
+                                  _addr(base), base_dtype, y.data_ptr(), y_dtype, stream), "moe_combine_rows")
+    return y
+
+
+def combine_rows(rows, pair_pos, w=None, base=None, y=None, dtype=None, stream=None):
+    """y[t] = base[t] + sum_i w[t, i] rows[pair_pos[t, i]] (moe_combine_rows).
+
+    rows [R, d], base [T, d] (None: zeros) and y, each fp32 or bf16; pair_pos
+    int32 [T, k] as dispatch returns it (outside [0, R): no row); w fp32 [T, k]
+    (None: ones).  Returns y [T, d] in dtype (None: rows' type); y may be base."""
+    rows_dtype = _float_dtype(rows.dtype, "rows")
+    _shape(rows, (None, None), "rows")
+    R, d = rows.shape
+    _shape(pair_pos, (None, None), "pair_pos")
+    T, k = pair_pos.shape
+    _sizes("rows, pair_pos", R, T, d, k)
+    dtype = rows.dtype if dtype is None else dtype
+    y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
+    base_dtype = y_dtype
+    if base is not None:
+        base_dtype = _float_dtype(base.dtype, "base")
+    _tensors(((base, (T, d), base.dtype if base is not None else None, "base"), (w, (T, k), torch.float32, "w"),
+              (y, (T, d), y.dtype if y is not None else None, "y"), (rows, (R, d), rows.dtype, "rows"),
+              (pair_pos, (T, k), torch.int32, "pair_pos")))
+    return _combine_rows("combine_rows", stream, (rows, pair_pos, w, base, y), rows, rows_dtype, R, T, d, k,
+                         pair_pos, w, base, base_dtype, y, dtype, y_dtype)
+
+
+def dispatch_backward(drows, pair_pos, dx=None, dtype=None, stream=None):
+    """Gradient of dispatch's x from that of its rows: dx[t] = sum_i
+    drows[pair_pos[t, i]], in dtype (None: drows' type) (moe_combine_rows without
+    weights)."""
+    return combine_rows(drows, pair_pos, y=dx, dtype=dtype, stream=stream)
+
+
+@_on_stream
+def _combine_backward(dev, stream, dy, dy_dtype, rows, dtype, rows_dtype, R, T, d, k, pair_pos, w, drows, dw,
+                      need_rows, need_w):
+    if drows is None and need_rows:
+        drows = torch.empty((R, d), dtype=dtype, device=dev)
+    if dw is None and need_w:
+        dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _check(lib().moe_combine_backward(dy.data_ptr(), dy_dtype, _addr(rows), rows_dtype, R, T, d, k,
+                                      pair_pos.data_ptr(), _addr(w), _addr(drows), _addr(dw), stream),
+           "moe_combine_backward")
+    return drows, dw
+
+
+def combine_backward(dy, rows, pair_pos, w=None, drows=None, dw=None, need_rows=True, need_w=True, stream=None):
+    """Gradients of combine_rows (and combine) from that of y (moe_combine_backward).
+
+    dy [T, d], rows [R, d], each fp32 or bf16; pair_pos int32 and w fp32 (None:
+    ones) [T, k] as the forward call took them.  Returns (drows [R, d] in rows'
+    type, dw fp32 [T, k]): the rows' gradients in the groups' order, and what
+    route_backward takes; None for one that is not needed.  Rows that are no
+    pair's are left as they were (undefined in drows allocated here).  Where only
+    drows is needed, it may be given in place of rows with rows None."""
+    like = rows if rows is not None else drows
+    if like is None:
+        raise ValueError("combine_backward: rows, or drows without need_w, expected")
+    if rows is None and need_w:
+        raise ValueError("rows: expected where dw is needed")
+    if not (need_rows or need_w):
+        raise ValueError("combine_backward: drows or dw must be needed")
+    if (drows is not None and not need_rows) or (dw is not None and not need_w):
+        raise ValueError("combine_backward: a buffer given for a gradient that is not needed")
+    dy_dtype, rows_dtype = _float_dtype(dy.dtype, "dy"), _float_dtype(like.dtype, "rows")
+    _shape(dy, (None, None), "dy")
+    T, d = dy.shape
+    _shape(like, (None, d), "rows")
+    R = like.shape[0]
+    _shape(pair_pos, (T, None), "pair_pos")
+    k = pair_pos.shape[1]
+    _sizes("rows, pair_pos", R, T, d, k)
+    _tensors(((rows, (R, d), like.dtype, "rows"), (drows, (R, d), like.dtype, "drows"),
+              (w, (T, k), torch.float32, "w"), (dw, (T, k), torch.float32, "dw"), (dy, (T, d), dy.dtype, "dy"),
+              (pair_pos, (T, k), torch.int32, "pair_pos")))
+    return _combine_backward("combine_backward", stream, (dy, rows, pair_pos, w, drows, dw), dy, dy_dtype, rows,
+                             like.dtype, rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows, need_w)
+
+
+@_on_stream
+def _lora(dev, stream, base, x, x_dtype, T, d_in, d_out, a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype):
+    if y is None:
+        y = torch.empty_like(base)
+    _check(lib().moe_lora(base.data_ptr(), x.data_ptr(), x_dtype, T, d_in, d_out, a.data_ptr(), b.data_ptr(), n,
+                          rank, _addr(seq_offsets), S, adapter.data_ptr(), _addr(scale), y.data_ptr(), y_dtype,
+                          stream), "moe_lora")
+    return y
+
+
+def lora(base, x, a, b, adapter, seq_offsets=None, scale=None, y=None, stream=None):
+    """y[t] = base[t] + scale[m] b[m] (a[m] x[t]) for the rows t of every request,
+    m = adapter[request] (moe_lora).
+
+    x [T, d_in] and base [T, d_out], each fp32 or bf16; a bf16 [n, rank, d_in], b
+    bf16 [n, d_out, rank]; adapter int32 [S] (outside [0, n): none, y = base);
+    seq_offsets int32 [S + 1], the bounds of the requests' rows (None: a row for
+    each); scale fp32 [n] (None: ones).  Returns y in base's type; y may be base.
+    Rows of no request are left as they were (undefined in a y allocated here)."""
+    x_dtype, y_dtype = _float_dtype(x.dtype, "x"), _float_dtype(base.dtype, "base")
+    _shape(x, (None, None), "x")
+    T, d_in = x.shape
+    _shape(base, (T, None), "base")
+    d_out = base.shape[1]
+    _shape(a, (None, None, d_in), "a")
+    n, rank = a.shape[0], a.shape[1]
+    _shape(b, (n, d_out, rank), "b")
+    _shape(adapter, (T if seq_offsets is None else None,), "adapter")
+    S = adapter.shape[0]
+    _sizes("lora", T, d_in, d_out, n, rank, S)
+    _tensors(((seq_offsets, (S + 1,), torch.int32, "seq_offsets"), (scale, (n,), torch.float32, "scale"),
+              (y, (T, d_out), base.dtype, "y"), (x, (T, d_in), x.dtype, "x"), (base, (T, d_out), base.dtype, "base"),
+              (a, (n, rank, d_in), torch.bfloat16, "a"), (b, (n, d_out, rank), torch.bfloat16, "b"),
+              (adapter, (S,), torch.int32, "adapter")))
+    return _lora("lora", stream, (base, x, a, b, seq_offsets, adapter, scale, y), base, x, x_dtype, T, d_in, d_out,
+                 a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype)
+
+
+def verify_drafts_workspace_bytes(B: int, V: int) -> int:
+    return int(lib().moe_verify_drafts_workspace_bytes(_int32(B, "B"), _int32(V, "V")))
+
+
+@_on_stream
+def _verify(dev, stream, p, q, dtype, B, n, V, draft, n_draft, u_accept, u_sample, tokens, n_accepted, ws):
+    if tokens is None:
+        tokens = torch.empty((B, n + 1), dtype=torch.int32, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    wp, wn, keep = _scratch(lib().moe_verify_drafts_workspace_bytes(B, V), ws, dev)
+    _check(lib().moe_verify_drafts(p.data_ptr(), _addr(q), dtype, B, n, V, draft.data_ptr(), _addr(n_draft),
+                                   u_accept.data_ptr(), u_sample.data_ptr(), tokens.data_ptr(),
+                                   n_accepted.data_ptr(), wp, wn, stream), "moe_verify_drafts")
+    return tokens, n_accepted
+
+
+def verify_drafts(p, q, draft, u_accept, u_sample, n_draft=None, tokens=None, n_accepted=None, ws=None, stream=None):
+    """Accept or replace drafted tokens (moe_verify_drafts).
+
+    p [B, n + 1, V] the target's probabilities at the drafts' places and after the
+    last one, q [B, n, V] those the drafts were drawn from (None: drafts that were
+    looked up), both fp32 or both bf16; draft int32 [B, n], n_draft int32 [B] how
+    many of them count (None: all); u_accept fp32 [B, n] and u_sample fp32 [B]
+    random numbers in [0, 1).  Returns (tokens int32 [B, n + 1]: the accepted
+    drafts, the token drawn after them, then -1; n_accepted int32 [B])."""
+    dtype = _float_dtype(p.dtype, "p")
+    _shape(draft, (None, None), "draft")
+    B, n = draft.shape
+    if n > MAX_DRAFTS:
+        raise ValueError(f"draft: at most {MAX_DRAFTS} drafts expected, got {n}")
+    _shape(p, (B, n + 1, None), "p")
+    V = p.shape[2]
+    _sizes("p", B, V)
+    _tensors(((q, (B, n, V), p.dtype, "q"), (u_accept, (B, n), torch.float32, "u_accept"),
+              (u_sample, (B,), torch.float32, "u_sample"), (n_draft, (B,), torch.int32, "n_draft"),
+              (tokens, (B, n + 1), torch.int32, "tokens"), (n_accepted, (B,), torch.int32, "n_accepted"),
+              (draft, (B, n), torch.int32, "draft"), (p, (B, n + 1, V), p.dtype, "p")))
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
+    return _verify("verify_drafts", stream, (p, q, draft, n_draft, u_accept, u_sample, tokens, n_accepted, ws), p, q,
+                   dtype, B, n, V, draft, n_draft, u_accept, u_sample, tokens, n_accepted, ws)

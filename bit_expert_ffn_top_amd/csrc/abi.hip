@@ -124,6 +124,12 @@ bool apart(std::initializer_list<const void*> written, std::initializer_list<con
 
 constexpr int64_t kMaxMxRows = (int64_t{1} << 24) - 1;
 
+// T tokens of k pairs each, and a row of d values, as the dispatch calls take them.
+bool valid_pairs(int64_t T, int64_t most, int k) {
+  return T >= 0 && T <= most && k >= 1 && k <= MOE_MAX_TOPK;
+}
+bool valid_row(int d) { return d >= 4 && d <= MOE_MAX_MX_COLS && d % 4 == 0; }
+
 bool valid_mx_cols(int cols) { return cols >= 32 && cols <= MOE_MAX_MX_COLS && cols % 32 == 0; }
 
 int check_mxfp4(const moe_mxfp4* M) {
@@ -668,6 +674,107 @@ int moe_route_backward(const float* logits, const int32_t* idx, int T, int E, in
   return hip_status(bitffn::launch_route_backward(logits, idx, T, E, k, seq_offsets, n_seq, mask,
                                                   counts, n_tokens, g_balance, g_z, w, dw, dlogits,
                                                   stream));
+}
+
+size_t moe_dispatch_workspace_bytes(int T, int k, int E) {
+  if (!valid_pairs(T, 65536, k) || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+  return bitffn::dispatch_workspace_bytes(T, k, E);
+}
+
+int moe_dispatch(const void* x, int dtype, int T, int d, const int32_t* idx, int k, int E,
+                 void* rows, int32_t* offsets, int32_t* pair_pos, void* ws, size_t ws_bytes,
+                 hipStream_t stream) {
+  if (!valid_dtype(dtype) || !valid_pairs(T, 65536, k) || !valid_row(d)) return MOE_EINVAL;
+  if (E < 1 || E > MOE_MAX_EXPERTS) return MOE_EINVAL;
+  const size_t need = bitffn::dispatch_workspace_bytes(T, k, E);
+  if (!offsets || (need > 0 && !ws)) return MOE_EINVAL;
+  if (T > 0 && (!x || !idx || !rows || !pair_pos)) return MOE_EINVAL;
+  if (!aligned16(x) || !aligned16(idx) || !aligned16(rows) || !aligned16(offsets) ||
+      !aligned16(pair_pos) || (need > 0 && !aligned256(ws)))
+    return MOE_EALIGN;
+  if (need > 0 && ws_bytes < need) return MOE_ENOSPC;
+  if (!apart({rows, offsets, pair_pos, need > 0 ? ws : nullptr}, {x, idx})) return MOE_EINVAL;
+  return hip_status(bitffn::launch_dispatch(x, dtype, T, d, idx, k, E, rows, offsets, pair_pos, ws,
+                                            stream));
+}
+
+int moe_combine_rows(const void* rows, int rows_dtype, int64_t R, int T, int d, int k,
+                     const int32_t* pair_pos, const float* w, const void* base, int base_dtype,
+                     void* y, int y_dtype, hipStream_t stream) {
+  if (!valid_dtype(rows_dtype) || !valid_dtype(base_dtype) || !valid_dtype(y_dtype))
+    return MOE_EINVAL;
+  if (!valid_pairs(T, kMaxMxRows, k) || !valid_row(d) || R < 0 || R > INT32_MAX) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!pair_pos || !y || (R > 0 && !rows)) return MOE_EINVAL;
+  if (!aligned16(rows) || !aligned16(pair_pos) || !aligned16(w) || !aligned16(base) || !aligned16(y))
+    return MOE_EALIGN;
+  const bool in_place = base == y && base_dtype == y_dtype;
+  if (!apart({y}, {rows, pair_pos, w, in_place ? nullptr : base})) return MOE_EINVAL;
+  return hip_status(bitffn::launch_combine_rows(rows, rows_dtype, R, T, d, k, pair_pos, w, base,
+                                                base_dtype, y, y_dtype, stream));
+}
+
+int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int rows_dtype, int64_t R,
+                         int T, int d, int k, const int32_t* pair_pos, const float* w, void* drows,
+                         float* dw, hipStream_t stream) {
+  if (!valid_dtype(dy_dtype) || !valid_dtype(rows_dtype)) return MOE_EINVAL;
+  if (!valid_pairs(T, kMaxMxRows, k) || !valid_row(d) || R < 0 || R > INT32_MAX) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!dy || !pair_pos || (R > 0 && ((!drows && !dw) || (dw && !rows)))) return MOE_EINVAL;
+  if (!aligned16(dy) || !aligned16(rows) || !aligned16(pair_pos) || !aligned16(w) ||
+      !aligned16(drows) || !aligned16(dw))
+    return MOE_EALIGN;
+  if (!apart({drows, dw}, {dy, rows, pair_pos, w})) return MOE_EINVAL;
+  if (!drows && !dw) return MOE_OK;
+  return hip_status(bitffn::launch_combine_backward(dy, dy_dtype, rows, rows_dtype, R, T, d, k,
+                                                    pair_pos, w, drows, dw, stream));
+}
+
+int moe_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
+             const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
+             const int32_t* seq_offsets, int n_seq, const int32_t* adapter, const float* scale,
+             void* y, int y_dtype, hipStream_t stream) {
+  if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return MOE_EINVAL;
+  if (T < 0 || T > kMaxMxRows || !valid_mx_cols(d_in)) return MOE_EINVAL;
+  if (d_out < 16 || d_out > MOE_MAX_MX_COLS || d_out % 16 != 0) return MOE_EINVAL;
+  if (n_adapters < 1 || n_adapters > MOE_MAX_EXPERTS) return MOE_EINVAL;
+  if (rank < 8 || rank > MOE_MAX_RANK || rank % 8 != 0) return MOE_EINVAL;
+  if (seq_offsets ? (n_seq < 1 || n_seq > 65536) : n_seq != T) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!base || !x || !a || !b || !adapter || !y) return MOE_EINVAL;
+  if (!aligned16(base) || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(adapter) ||
+      !aligned16(seq_offsets) || !aligned16(scale) || !aligned16(y))
+    return MOE_EALIGN;
+  if (!apart({y}, {x, a, b, seq_offsets, adapter, scale})) return MOE_EINVAL;
+  return hip_status(bitffn::launch_lora(base, x, x_dtype, T, d_in, d_out, a, b, n_adapters, rank,
+                                        seq_offsets, n_seq, adapter, scale, y, y_dtype, stream));
+}
+
+size_t moe_verify_drafts_workspace_bytes(int B, int V) {
+  if (B < 0 || B > 65536 || V < 1 || V > kMaxMxRows) return 0;
+  return bitffn::verify_workspace_bytes(B, V);
+}
+
+int moe_verify_drafts(const void* p, const void* q, int dtype, int B, int n, int V,
+                      const int32_t* draft, const int32_t* n_draft, const float* u_accept,
+                      const float* u_sample, int32_t* tokens, int32_t* n_accepted, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
+  if (!valid_dtype(dtype) || B < 0 || B > 65536 || n < 0 || n > MOE_MAX_DRAFTS) return MOE_EINVAL;
+  if (V < 1 || V > kMaxMxRows) return MOE_EINVAL;
+  if (B == 0) return MOE_OK;
+  const size_t need = bitffn::verify_workspace_bytes(B, V);
+  if (!p || !u_sample || !tokens || !n_accepted || (need > 0 && !ws)) return MOE_EINVAL;
+  if (n > 0 && (!draft || !u_accept)) return MOE_EINVAL;
+  if (!aligned16(p) || !aligned16(q) || !aligned16(draft) || !aligned16(n_draft) ||
+      !aligned16(u_accept) || !aligned16(u_sample) || !aligned16(tokens) ||
+      !aligned16(n_accepted) || (need > 0 && !aligned256(ws)))
+    return MOE_EALIGN;
+  if (need > 0 && ws_bytes < need) return MOE_ENOSPC;
+  if (!apart({tokens, n_accepted, need > 0 ? ws : nullptr},
+             {p, q, draft, n_draft, u_accept, u_sample}))
+    return MOE_EINVAL;
+  return hip_status(bitffn::launch_verify_drafts(p, q, dtype, B, n, V, draft, n_draft, u_accept,
+                                                 u_sample, tokens, n_accepted, ws, stream));
 }
 
 }  // extern "C"

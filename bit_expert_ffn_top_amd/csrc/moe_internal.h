@@ -154,4 +154,28 @@ hipError_t launch_route_backward(const float* logits, const int32_t* idx, int T,
                                  const float* g_balance, const float* g_z, const float* w,
                                  const float* dw, float* dlogits, hipStream_t s);
 
+// Tokens to the experts and back (dispatch.hip).  rows_dtype is also drows'.
+size_t dispatch_workspace_bytes(int T, int k, int E);
+hipError_t launch_dispatch(const void* x, int dtype, int T, int d, const int32_t* idx, int k, int E,
+                           void* rows, int32_t* offsets, int32_t* pair_pos, void* ws, hipStream_t s);
+hipError_t launch_combine_rows(const void* rows, int rows_dtype, int64_t R, int T, int d, int k,
+                               const int32_t* pair_pos, const float* w, const void* base,
+                               int base_dtype, void* y, int y_dtype, hipStream_t s);
+hipError_t launch_combine_backward(const void* dy, int dy_dtype, const void* rows, int rows_dtype,
+                                   int64_t R, int T, int d, int k, const int32_t* pair_pos,
+                                   const float* w, void* drows, float* dw, hipStream_t s);
+
+// Low-rank adapters of many requests (lora.hip).
+hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
+                       const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
+                       const int32_t* seq, int n_seq, const int32_t* adapter, const float* scale,
+                       void* y, int y_dtype, hipStream_t s);
+
+// Verification of drafted tokens (verify_drafts.hip).
+size_t verify_workspace_bytes(int B, int V);
+hipError_t launch_verify_drafts(const void* p, const void* q, int dtype, int B, int n, int V,
+                                const int32_t* draft, const int32_t* n_draft,
+                                const float* u_accept, const float* u_sample, int32_t* tokens,
+                                int32_t* n_accepted, void* ws, hipStream_t s);
+
 }  // namespace bitffn

@@ -671,6 +671,96 @@ int moe_route_backward(const float* logits, const int32_t* idx, int T, int E, in
                        const float* g_balance, const float* g_z, const float* w,
                        const float* dw, float* dlogits, hipStream_t stream);
 
+/* Tokens to their experts: the pairs grouped as by moe_group_pairs, and a row
+ * of its own for each.
+ *   rows[pair_pos[t*k+i]] = x[t]     (0 <= idx[t*k+i] < E)
+ * x and rows fp32 or bf16 (dtype), x [T][d], rows [T*k][d]; idx int32 [T][k];
+ * offsets int32 [E+1] and pair_pos int32 [T*k] as moe_group_pairs writes them,
+ * but equal ids of a token are in i order.  Rows past offsets[E] are left as
+ * they were.  Limits: 0 <= T <= 65536, 1 <= k <= MOE_MAX_TOPK, 1 <= E <=
+ * MOE_MAX_EXPERTS, d a multiple of 4 in 4..MOE_MAX_MX_COLS.
+ * ws: at least moe_dispatch_workspace_bytes(T, k, E) bytes, 256-byte aligned (0
+ * for few pairs, then ws may be NULL, and for sizes out of range). */
+size_t moe_dispatch_workspace_bytes(int T, int k, int E);
+int moe_dispatch(const void* x, int dtype, int T, int d, const int32_t* idx, int k,
+                 int E, void* rows, int32_t* offsets, int32_t* pair_pos, void* ws,
+                 size_t ws_bytes, hipStream_t stream);
+
+/* The experts' rows back in the tokens' order:
+ *   y[t] = base[t] + sum_{i: 0 <= pair_pos[t*k+i] < R} w[t*k+i] * rows[pair_pos[t*k+i]]
+ * summed in fp32 in i order from base on, rounded once to y_dtype.  rows
+ * [R][d], base [T][d] (NULL: zeros), y [T][d], each fp32 or bf16; w fp32 [T][k]
+ * (NULL: ones, the gradient of moe_dispatch's x from that of its rows).  y may
+ * be base where both have one type.  moe_combine is the same for fp32 rows with
+ * a shared expert's rows beside the residual.
+ * Limits: 0 <= T < 2^24, 0 <= R < 2^31, 1 <= k <= MOE_MAX_TOPK, d as above. */
+int moe_combine_rows(const void* rows, int rows_dtype, int64_t R, int T, int d, int k,
+                     const int32_t* pair_pos, const float* w, const void* base,
+                     int base_dtype, void* y, int y_dtype, hipStream_t stream);
+
+/* Gradients of moe_combine_rows (and of moe_combine) from that of y (dy [T][d],
+ * fp32 or bf16): for every pair with 0 <= pair_pos[t*k+i] < R
+ *   drows[pair_pos[t*k+i]] = w[t*k+i] * dy[t]
+ *   dw[t*k+i]              = sum_j dy[t][j] * rows[pair_pos[t*k+i]][j]
+ * and dw = 0 for the others.  rows and drows have rows_dtype; dw fp32 [T][k],
+ * summed in fp32 in a fixed order; it is what moe_route_backward takes.  Rows of
+ * drows that are no pair's are left as they were.  drows or dw (with rows) may be
+ * NULL, w NULL counts as ones.  base's gradient is dy itself.  Limits as above. */
+int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int rows_dtype,
+                         int64_t R, int T, int d, int k, const int32_t* pair_pos,
+                         const float* w, void* drows, float* dw, hipStream_t stream);
+
+/* Low-rank adapters of many requests beside a projection that they share:
+ *   y[t] = base[t] + scale[m] * B_m (A_m x[t]),   m = adapter[s]
+ * for the rows t of request s: seq_offsets[s] .. seq_offsets[s+1]-1 (int32
+ * [n_seq+1], ascending; values are clamped to [0, T], and one below an earlier
+ * one counts as that one), or row s alone where seq_offsets is NULL (then n_seq
+ * = T).  A request whose adapter lies outside [0, n_adapters) has none: y = base.
+ * Rows of no request are left as they were.
+ *   x [T][d_in] fp32 or bf16 (x_dtype); base, y [T][d_out] fp32 or bf16
+ *   (y_dtype), y may be base; a bf16 [n_adapters][rank][d_in], b bf16
+ *   [n_adapters][d_out][rank]; adapter int32 [n_seq]; scale fp32 [n_adapters]
+ *   (NULL: ones).
+ * base is for instance moe_mxfp4_linear's y.  Sums in fp32 in a fixed order, the
+ * result rounded once; a smaller rank is a larger one padded with zeros.
+ * Limits: 0 <= T < 2^24, 1 <= n_seq <= 65536 (without seq_offsets: n_seq = T),
+ * 1 <= n_adapters <= MOE_MAX_EXPERTS, rank a multiple of 8 in 8..MOE_MAX_RANK,
+ * d_in a multiple of 32 and d_out of 16, both up to MOE_MAX_MX_COLS. */
+#define MOE_MAX_RANK 128
+int moe_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
+             const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
+             const int32_t* seq_offsets, int n_seq, const int32_t* adapter,
+             const float* scale, void* y, int y_dtype, hipStream_t stream);
+
+/* Verification of drafted tokens ("Strata" page, "投機的デコード": a pass over
+ * the layers verifies the drafts).  Request s has m = n_draft[s] drafts
+ * (clamped to 0..n; NULL: n), drawn from q; p are the target's probabilities at
+ * the places of the drafts and after the last one.  Draft i is accepted if all
+ * before it are and u_accept[s][i] * q[s][i][x] < p[s][i][x], x = draft[s][i]
+ * (an x outside [0, V) is not).  With j the number of accepted ones, the token
+ * at place j is drawn from r = max(p[s][j] - q[s][j], 0), or from p[s][j] where
+ * j = m or r is nothing but zeros: the smallest v with
+ *   r[0] + .. + r[v] > u_sample[s] * (sum of r)
+ * (the last v with r[v] > 0 if there is none; -1 if r is nothing but zeros).  So
+ * the tokens are distributed as if each were drawn from p.  q NULL: drafts that
+ * were looked up, not drawn; then q is 1 at the draft and 0 elsewhere.
+ *   p [B][n+1][V], q [B][n][V], both fp32 or bf16 (dtype); draft int32 [B][n],
+ *   n_draft int32 [B]; u_accept fp32 [B][n], u_sample fp32 [B], in [0, 1)
+ *   tokens int32 [B][n+1]   accepted drafts, the token drawn, then -1
+ *   n_accepted int32 [B]
+ * Products, differences and sums are in 64 bits; where r is formed, NaN,
+ * infinities and values below 0 count as 0, as does a u_sample below 0.
+ * Limits: 0 <= B <= 65536, 0 <= n <= MOE_MAX_DRAFTS, 1 <= V < 2^24.
+ * ws: at least moe_verify_drafts_workspace_bytes(B, V) bytes, 256-byte aligned (0
+ * for short rows, then ws may be NULL, and for sizes out of range). */
+#define MOE_MAX_DRAFTS 63
+size_t moe_verify_drafts_workspace_bytes(int B, int V);
+int moe_verify_drafts(const void* p, const void* q, int dtype, int B, int n, int V,
+                      const int32_t* draft, const int32_t* n_draft,
+                      const float* u_accept, const float* u_sample, int32_t* tokens,
+                      int32_t* n_accepted, void* ws, size_t ws_bytes,
+                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
