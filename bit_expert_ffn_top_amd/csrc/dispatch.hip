@@ -9,191 +9,316 @@ namespace {
 constexpr int kMaxE = MOE_MAX_EXPERTS;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kMaxOwn = 2048;   // pairs of one workgroup's tokens
+constexpr int kMaxOwn = 1024;   // pairs of one workgroup's tokens (16 of MOE_MAX_TOPK)
+constexpr int kMaxParts = 128;   // that many tokens are counted in
+constexpr int kPartPairs = 2560;
+
+struct DispatchArgs {
+  const void* x;
+  const int32_t* idx;
+  void* rows;
+  int32_t* offsets;
+  int32_t* pair_pos;
+  uint16_t* counts;   // [parts][counts_row(E)]: pairs of each expert in a part
+  int T, k, E;
+  int nv;             // vectors of a row
+  int tokens;         // of a workgroup
+  int parts;
+  int part_tokens;    // of a part, and its workgroups
+  int subs;
+};
+
+__host__ __device__ inline int counts_row(int E) { return (E + 7) & ~7; }
+
+__device__ __forceinline__ bool is_expert(int e, int E) { return e >= 0 && e < E; }
+
+// Pairs of every expert in one part of the tokens.
+__global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a) {
+  __shared__ int32_t s_count[kMaxE];
+  const int row = counts_row(a.E);
+  for (int e = threadIdx.x; e < row; e += kThreads) s_count[e] = 0;
+  __syncthreads();
+  const int t0 = min(a.T, static_cast<int>(blockIdx.x) * a.part_tokens);
+  const int t1 = min(a.T, t0 + a.part_tokens);
+  for (int p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += kThreads) {
+    const int e = a.idx[p];
+    if (is_expert(e, a.E)) atomicAdd(&s_count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < row; e += kThreads)
+    a.counts[static_cast<int>(blockIdx.x) * row + e] = static_cast<uint16_t>(s_count[e]);
+}
 
 // The row of a pair = pairs of smaller experts + earlier pairs of its expert.
-// Every workgroup counts all pairs in LDS, those before its own tokens first,
-// so the call is one launch; ranks among its own pairs are counted directly,
-// which keeps equal ids of a token in order.  A wavefront then reads a token's
-// row once and writes it to its k places.
-template <typename V>   // uint4 or uint2: the part of a row one lane moves
-__global__ __launch_bounds__(kThreads) void dispatch_kernel(
-    const V* __restrict__ x, int T, int nv, const int32_t* __restrict__ idx, int k, int E,
-    int tokens, V* __restrict__ rows, int32_t* __restrict__ offsets,
-    int32_t* __restrict__ pair_pos) {
-  __shared__ int32_t s_count[kMaxE];
-  __shared__ int32_t s_before[kMaxE];
-  __shared__ int32_t s_sum[kThreads];
-  __shared__ int32_t s_own[kMaxOwn];
-  const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * tokens, t1 = min(T, t0 + tokens);
-  const int n = T * k, p0 = t0 * k, own = (t1 - t0) * k;
-  for (int e = tid; e < kMaxE; e += kThreads) s_count[e] = 0;
-  __syncthreads();
-  for (int p = tid; p < p0; p += kThreads) {
-    const int e = idx[p];
-    if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
+// Every workgroup finds both for its own tokens, so no launch waits for a sort.
+// Few pairs: it counts all of them in LDS.  Many (COUNTED): it adds up the parts
+// that an earlier launch counted, and counts what its own part holds before its
+// tokens.  Ranks among its own pairs are counted directly, which keeps equal ids
+// of a token in order.  Then it reads its tokens' rows once and writes each to
+// its k places.
+typedef uint32_t nu4 __attribute__((ext_vector_type(4)));
+typedef uint32_t nu2 __attribute__((ext_vector_type(2)));
+
+template <typename V, bool COUNTED>   // V: the part of a row that one lane moves
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
+  __shared__ int32_t s_total[kMaxE];
+  __shared__ int32_t s_before[kMaxE];   // then each expert's row for the next own pair
+  __shared__ int32_t s_wave[kWaves];
+  __shared__ __align__(16) int32_t s_own[kMaxOwn];
+  __shared__ int32_t s_pos[kMaxOwn];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int E = a.E, k = a.k;
+  int t0, t1, part = 0;
+  if (COUNTED) {
+    part = blockIdx.x / a.subs;
+    const int sub = blockIdx.x - part * a.subs;
+    t0 = min(a.T, part * a.part_tokens + sub * a.tokens);
+    t1 = min(min(a.T, t0 + a.tokens), (part + 1) * a.part_tokens);
+  } else {
+    t0 = blockIdx.x * a.tokens;
+    t1 = min(a.T, t0 + a.tokens);
+  }
+  const int p0 = t0 * k, own = (t1 - t0) * k;
+  const int32_t* idx = a.idx;
+  for (int e = tid; e < kMaxE; e += kThreads) s_total[e] = s_before[e] = 0;
+  for (int q = tid; q < own; q += kThreads) {
+    const int e = idx[p0 + q];
+    s_own[q] = is_expert(e, E) ? e : -1;
   }
   __syncthreads();
-  for (int e = tid; e < kMaxE; e += kThreads) s_before[e] = s_count[e];
-  __syncthreads();
-  for (int p = p0 + tid; p < n; p += kThreads) {
-    const int e = idx[p];
-    if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
-    if (p < p0 + own) s_own[p - p0] = e >= 0 && e < E ? e : -1;
+  if (COUNTED) {
+    // eight experts' counts per load, the parts dealt to groups of threads
+    const int vecs = counts_row(E) / 8, groups = kThreads / vecs;
+    const int g = tid / vecs, j = tid - g * vecs;
+    if (g < groups) {
+      int total[8], before[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) total[i] = before[i] = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(a.counts) + j;
+#pragma unroll 8
+      for (int c = g; c < a.parts; c += groups) {
+        const uint4 v = src[c * vecs];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int n = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+          total[i] += n;
+          before[i] += c < part ? n : 0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (total[i]) atomicAdd(&s_total[8 * j + i], total[i]);
+        if (before[i]) atomicAdd(&s_before[8 * j + i], before[i]);
+      }
+    }
+    for (int p = part * a.part_tokens * k + tid; p < p0; p += kThreads) {
+      const int e = idx[p];
+      if (is_expert(e, E)) atomicAdd(&s_before[e], 1);
+    }
+  } else {
+    const int n = a.T * k;
+#pragma unroll 4
+    for (int p = tid; p < n; p += kThreads) {
+      const int e = idx[p];
+      if (is_expert(e, E)) {
+        atomicAdd(&s_total[e], 1);
+        if (p < p0) atomicAdd(&s_before[e], 1);
+      }
+    }
   }
   __syncthreads();
-  // exclusive scan over the experts, four per thread
+  // the experts' first rows: an exclusive scan, four experts per thread
   constexpr int kPer = kMaxE / kThreads;
   int c[kPer], sum = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     c[j] = sum;
-    sum += s_count[tid * kPer + j];
+    sum += s_total[tid * kPer + j];
   }
-  s_sum[tid] = sum;
+  int scan = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int up = __shfl_up(scan, off);
+    if (lane >= off) scan += up;
+  }
+  if (lane == 63) s_wave[wave] = scan;
   __syncthreads();
-  for (int off = 1; off < kThreads; off <<= 1) {
-    const int v = tid >= off ? s_sum[tid - off] : 0;
-    __syncthreads();
-    s_sum[tid] += v;
-    __syncthreads();
-  }
-  const int base = s_sum[tid] - sum;
+  int first = scan - sum;
+  for (int w = 0; w < wave; ++w) first += s_wave[w];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = tid * kPer + j;
-    s_before[e] += base + c[j];
-    if (blockIdx.x == 0 && e < E) offsets[e] = base + c[j];
+    s_before[e] += first + c[j];
+    if (blockIdx.x == 0 && e < E) a.offsets[e] = first + c[j];
   }
-  if (blockIdx.x == 0 && tid == kThreads - 1) offsets[E] = s_sum[tid];
+  if (blockIdx.x == 0 && tid == kThreads - 1) a.offsets[E] = first + sum;
   __syncthreads();
-  for (int q0 = 0; q0 < own; q0 += kThreads) {
-    const int q = q0 + tid;
+  for (int q = tid; q < own; q += kThreads) {
+    const int e = s_own[q];
     int at = -1;
-    if (q < own) {
-      const int e = s_own[q];
-      if (e >= 0) {
-        at = s_before[e];
-        for (int r = 0; r < q; ++r) at += s_own[r] == e;
-      }
-      pair_pos[p0 + q] = at;
+    if (e >= 0) {
+      at = s_before[e];
+      for (int r = 0; r < q; ++r) at += s_own[r] == e;
     }
+    s_pos[q] = at;
+    a.pair_pos[p0 + q] = at;
   }
-  __syncthreads();   // pair_pos of this workgroup is read back below
-  const int lane = tid & 63;
-  for (int t = t0 + (tid >> 6); t < t1; t += kWaves) {
-    const V* src = x + static_cast<int64_t>(t) * nv;
-    for (int j = lane; j < nv; j += 64) {
-      const V v = src[j];
-      for (int i = 0; i < k; ++i) {
-        const int at = pair_pos[t * k + i];
-        if (at >= 0) rows[static_cast<int64_t>(at) * nv + j] = v;
-      }
+  __syncthreads();
+  const V* x = static_cast<const V*>(a.x) + static_cast<int64_t>(t0) * a.nv;
+  V* rows = static_cast<V*>(a.rows);
+  const int items = (t1 - t0) * a.nv;
+  for (int i = tid; i < items; i += kThreads) {
+    const V v = x[i];
+    const int t = i / a.nv, j = i - t * a.nv;
+    for (int q = t * k; q < t * k + k; ++q) {
+      const int at = s_pos[q];
+      if (at >= 0) __builtin_nontemporal_store(v, &rows[static_cast<int64_t>(at) * a.nv + j]);
     }
   }
 }
 
 __device__ __forceinline__ bool has_row(int p, int R) { return p >= 0 && p < R; }
 
-// One thread per N consecutive columns of one token, the k terms in i order.
+// One thread per N consecutive columns of one token (the last one of a row may
+// have half of them), the k terms in i order.
 template <typename RT, typename YT, int N>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(
     const RT* __restrict__ rows, int R, int T, int d, int k, const int32_t* __restrict__ pair_pos,
     const float* __restrict__ w, const void* base, int base_dtype, YT* y) {
-  const int dn = d / N;
+  const int dn = (d + N - 1) / N;
   const int64_t gid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (gid >= static_cast<int64_t>(T) * dn) return;
   const int t = static_cast<int>(gid / dn);
   const int c = static_cast<int>(gid - static_cast<int64_t>(t) * dn) * N;
   const int64_t at = static_cast<int64_t>(t) * d + c;
+  const bool half = c + N > d;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.0f;
   if (base && base_dtype == MOE_DTYPE_F32) {
     RowPart<float, N> b;
-    b.load(static_cast<const float*>(base) + at);
+    b.load(static_cast<const float*>(base) + at, half);
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = b.get(j);
   } else if (base) {
     RowPart<uint16_t, N> b;
-    b.load(static_cast<const uint16_t*>(base) + at);
+    b.load(static_cast<const uint16_t*>(base) + at, half);
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = b.get(j);
   }
-  for (int i = 0; i < k; ++i) {
-    const int64_t q = static_cast<int64_t>(t) * k + i;
-    const int p = pair_pos[q];
-    if (!has_row(p, R)) continue;
-    const float wi = w ? w[q] : 1.0f;
-    RowPart<RT, N> r;
-    r.load(rows + static_cast<int64_t>(p) * d + c);
+  // the terms in batches: all places of a batch, then all its rows (one that is
+  // missing re-reads one that is there, so that no load waits for a comparison)
+  constexpr int KC = 10;
+  const int64_t q0 = static_cast<int64_t>(t) * k;
+  for (int i0 = 0; i0 < k; i0 += KC) {
+    int p[KC];
+    float wi[KC];
+    RowPart<RT, N> r[KC];
+    int any = -1;
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = fmaf(wi, r.get(j), acc[j]);
+    for (int j = 0; j < KC; ++j) {
+      const int64_t q = q0 + min(i0 + j, k - 1);
+      p[j] = i0 + j < k ? pair_pos[q] : -1;
+      wi[j] = w ? w[q] : 1.0f;
+    }
+#pragma unroll
+    for (int j = KC - 1; j >= 0; --j) any = has_row(p[j], R) ? p[j] : any;
+    if (any < 0) continue;
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+      if (i0 + j < k)   // uniform
+        r[j].template load<true>(rows + static_cast<int64_t>(has_row(p[j], R) ? p[j] : any) * d + c, half);
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
+      if (!has_row(p[j], R)) continue;
+#pragma unroll
+      for (int n = 0; n < N; ++n) acc[n] = fmaf(wi[j], r[j].get(n), acc[n]);
+    }
   }
   RowPart<YT, N> out;
   out.set(acc);
-  out.store(y + at);
+  out.template store<true>(y + at, half);
 }
 
+constexpr int kBackWaves = 16;
+
 // One workgroup per token, one wavefront per pair at a time: the product with
-// dy for dw, and dy times the weight for drows.
-template <typename GT, typename RT, int N>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(
+// dy for dw, and dy times the weight for drows.  NC > 0: a row has at most NC
+// parts per lane, and dy's stay in registers; 0: rows of any length.
+template <typename GT, typename RT, int N, int NC>
+__global__ __launch_bounds__(64 * kBackWaves) void combine_backward_kernel(
     const GT* __restrict__ dy, const RT* __restrict__ rows, int R, int d, int k,
     const int32_t* __restrict__ pair_pos, const float* __restrict__ w, RT* __restrict__ drows,
     float* __restrict__ dw) {
+  constexpr int H = NC > 0 ? NC : 1;
   const int lane = threadIdx.x & 63;
   const int64_t t = blockIdx.x;
-  for (int i = threadIdx.x >> 6; i < k; i += kWaves) {
+  const int c0 = lane * N;
+  RowPart<GT, N> g[H];
+  if (NC > 0) {
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+      if (c0 + 64 * N * j < d) g[j].load(dy + t * d + c0 + 64 * N * j, c0 + 64 * N * j + N > d);
+  }
+  for (int i = threadIdx.x >> 6; i < k; i += blockDim.x >> 6) {
     const int64_t q = t * k + i;
     const int p = pair_pos[q];
     float sum = 0.0f;
     if (has_row(p, R)) {
       const float wi = w ? w[q] : 1.0f;
-      for (int c = lane * N; c < d; c += 64 * N) {
-        RowPart<GT, N> g;
-        g.load(dy + t * d + c);
-        const int64_t at = static_cast<int64_t>(p) * d + c;
+      const int64_t row = static_cast<int64_t>(p) * d;
+      for (int b = c0; b < d; b += 64 * N * H) {
+        RowPart<RT, N> r[H];
         if (dw) {
-          RowPart<RT, N> r;
-          r.load(rows + at);
 #pragma unroll
-          for (int j = 0; j < N; ++j) sum = fmaf(g.get(j), r.get(j), sum);
+          for (int j = 0; j < H; ++j)
+            if (b + 64 * N * j < d) r[j].load(rows + row + b + 64 * N * j, b + 64 * N * j + N > d);
         }
-        if (drows) {
-          float f[N];
 #pragma unroll
-          for (int j = 0; j < N; ++j) f[j] = wi * g.get(j);
-          RowPart<RT, N> out;
-          out.set(f);
-          out.store(drows + at);
+        for (int j = 0; j < H; ++j) {
+          const int c = b + 64 * N * j;
+          if (c >= d) break;
+          if (NC == 0) g[j].load(dy + t * d + c, c + N > d);
+          if (drows) {
+            float f[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) f[n] = wi * g[j].get(n);
+            RowPart<RT, N> out;
+            out.set(f);
+            out.template store<true>(drows + row + c, c + N > d);
+          }
+          if (dw) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) sum = fmaf(g[j].get(n), r[j].get(n), sum);
+          }
         }
       }
     }
     if (dw) {
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+      sum = row16_sum_dpp(sum);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
       if (lane == 0) dw[q] = sum;
     }
   }
+}
+
+// A lane's part of a row: 16 bytes of the narrower type.
+template <typename A, typename B>
+constexpr int part_of() {
+  return sizeof(A) == 4 && sizeof(B) == 4 ? 4 : 8;
 }
 
 template <typename RT, typename YT>
 hipError_t combine_rows_as(const void* rows, int64_t R, int T, int d, int k,
                            const int32_t* pair_pos, const float* w, const void* base,
                            int base_dtype, void* y, hipStream_t s) {
-  const int n = d % 8 == 0 ? 8 : 4;
-  const int64_t blocks = (static_cast<int64_t>(T) * (d / n) + kThreads - 1) / kThreads;
-  const auto go = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-        static_cast<const RT*>(rows), static_cast<int>(R), T, d, k, pair_pos, w, base, base_dtype,
-        static_cast<YT*>(y));
-  };
-  if (n == 8)
-    go(combine_rows_kernel<RT, YT, 8>);
-  else
-    go(combine_rows_kernel<RT, YT, 4>);
+  constexpr int N = part_of<RT, YT>();
+  const int64_t blocks = (static_cast<int64_t>(T) * ((d + N - 1) / N) + kThreads - 1) / kThreads;
+  combine_rows_kernel<RT, YT, N><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+      static_cast<const RT*>(rows), static_cast<int>(R), T, d, k, pair_pos, w, base, base_dtype,
+      static_cast<YT*>(y));
   return hipGetLastError();
 }
 
@@ -201,35 +326,72 @@ template <typename GT, typename RT>
 hipError_t combine_backward_as(const void* dy, const void* rows, int64_t R, int T, int d, int k,
                                const int32_t* pair_pos, const float* w, void* drows, float* dw,
                                hipStream_t s) {
+  // few tokens: a wavefront for every pair; many: four per token, which share dy
+  const int waves = T <= 512 ? min(k, kBackWaves) : min(k, 4);
   const auto go = [&](auto kernel) {
-    kernel<<<T, kThreads, 0, s>>>(static_cast<const GT*>(dy), static_cast<const RT*>(rows),
+    kernel<<<T, 64 * waves, 0, s>>>(static_cast<const GT*>(dy), static_cast<const RT*>(rows),
                                   static_cast<int>(R), d, k, pair_pos, w, static_cast<RT*>(drows),
                                   dw);
   };
-  if (d % 8 == 0)
-    go(combine_backward_kernel<GT, RT, 8>);
+  constexpr int W = part_of<GT, RT>();
+  if (d <= 64 * W)
+    go(combine_backward_kernel<GT, RT, W, 1>);
+  else if (d <= 256 * W)
+    go(combine_backward_kernel<GT, RT, W, 4>);
+  else if (d <= 2048)
+    go(combine_backward_kernel<GT, RT, W, 2048 / (64 * W)>);
   else
-    go(combine_backward_kernel<GT, RT, 4>);
+    go(combine_backward_kernel<GT, RT, W, 0>);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t dispatch_workspace_bytes(int, int, int) { return 0; }
+namespace {
+
+// Pairs up to which every workgroup counts all of them.
+constexpr int kFewPairs = 8192;
+
+// Parts of at most 32,768 pairs (T <= 65536), so that counts have 16 bits.
+int count_parts(int T, int k) {
+  return max(1, min(kMaxParts, (T * k + kPartPairs - 1) / kPartPairs));
+}
+
+template <typename V>
+void dispatch_as(DispatchArgs a, hipStream_t s) {
+  if (!a.counts) {
+    a.tokens = max(1, min((a.T + 511) / 512, kMaxOwn / a.k));
+    dispatch_kernel<V, false><<<max(1, (a.T + a.tokens - 1) / a.tokens), kThreads, 0, s>>>(a);
+    return;
+  }
+  a.parts = count_parts(a.T, a.k);
+  a.part_tokens = (a.T + a.parts - 1) / a.parts;
+  a.tokens = min(16, (a.T + 1023) / 1024);
+  a.subs = (a.part_tokens + a.tokens - 1) / a.tokens;
+  dispatch_count_kernel<<<a.parts, kThreads, 0, s>>>(a);
+  dispatch_kernel<V, true><<<a.parts * a.subs, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+size_t dispatch_workspace_bytes(int T, int k, int E) {
+  if (T * k <= kFewPairs) return 0;
+  return static_cast<size_t>(align256(int64_t{count_parts(T, k)} * counts_row(E) * 2));
+}
 
 hipError_t launch_dispatch(const void* x, int dtype, int T, int d, const int32_t* idx, int k, int E,
-                           void* rows, int32_t* offsets, int32_t* pair_pos, void*, hipStream_t s) {
+                           void* rows, int32_t* offsets, int32_t* pair_pos, void* ws,
+                           hipStream_t s) {
   const int bytes = d * (dtype == MOE_DTYPE_F32 ? 4 : 2);
-  const int tokens = max(1, min((T + 1023) / 1024, kMaxOwn / k));
-  const int blocks = max(1, (T + tokens - 1) / tokens);
-  if (bytes % 16 == 0)
-    dispatch_kernel<uint4><<<blocks, kThreads, 0, s>>>(static_cast<const uint4*>(x), T, bytes / 16,
-                                                       idx, k, E, tokens, static_cast<uint4*>(rows),
-                                                       offsets, pair_pos);
-  else
-    dispatch_kernel<uint2><<<blocks, kThreads, 0, s>>>(static_cast<const uint2*>(x), T, bytes / 8,
-                                                       idx, k, E, tokens, static_cast<uint2*>(rows),
-                                                       offsets, pair_pos);
+  DispatchArgs a{x, idx, rows, offsets, pair_pos, nullptr, T, k, E, 0, 0, 0, 0, 0};
+  if (dispatch_workspace_bytes(T, k, E) > 0) a.counts = static_cast<uint16_t*>(ws);
+  if (bytes % 16 == 0) {
+    a.nv = bytes / 16;
+    dispatch_as<nu4>(a, s);
+  } else {
+    a.nv = bytes / 8;
+    dispatch_as<nu2>(a, s);
+  }
   return hipGetLastError();
 }
 
