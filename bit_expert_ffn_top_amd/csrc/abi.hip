@@ -739,7 +739,7 @@ int moe_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, 
   if (d_out < 16 || d_out > MOE_MAX_MX_COLS || d_out % 16 != 0) return MOE_EINVAL;
   if (n_adapters < 1 || n_adapters > MOE_MAX_EXPERTS) return MOE_EINVAL;
   if (rank < 8 || rank > MOE_MAX_RANK || rank % 8 != 0) return MOE_EINVAL;
-  if (seq_offsets ? (n_seq < 1 || n_seq > 65536) : n_seq != T) return MOE_EINVAL;
+  if (n_seq < 0 || n_seq > 65536 || (seq_offsets ? n_seq < 1 : n_seq != T)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
   if (!base || !x || !a || !b || !adapter || !y) return MOE_EINVAL;
   if (!aligned16(base) || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(adapter) ||

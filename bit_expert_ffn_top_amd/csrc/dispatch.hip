@@ -56,9 +56,6 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a
 // tokens.  Ranks among its own pairs are counted directly, which keeps equal ids
 // of a token in order.  Then it reads its tokens' rows once and writes each to
 // its k places.
-typedef uint32_t nu4 __attribute__((ext_vector_type(4)));
-typedef uint32_t nu2 __attribute__((ext_vector_type(2)));
-
 template <typename V, bool COUNTED>   // V: the part of a row that one lane moves
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
   __shared__ int32_t s_total[kMaxE];

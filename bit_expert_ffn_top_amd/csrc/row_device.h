@@ -12,6 +12,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 typedef float nf4 __attribute__((ext_vector_type(4)));
+typedef uint32_t nu4 __attribute__((ext_vector_type(4)));
+typedef uint32_t nu2 __attribute__((ext_vector_type(2)));
 
 // N (4 or 8) values of a row: fp32 in 16-byte parts, bfloat16 in one part of 2N
 // bytes that needs only 8-byte alignment (rows of an odd number of fours).
