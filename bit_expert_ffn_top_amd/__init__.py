@@ -15,5 +15,6 @@ from ._binding import (  # noqa: F401
     mxfp4_ffn_decode_workspace_bytes, mxfp4_gate_up, mxfp4_linear, mxfp4_quantize, route_backward,
     route_balance, route_balance_workspace_bytes,
     Dispatch, combine_backward, combine_rows, dispatch, dispatch_backward, dispatch_workspace_bytes, lora,
+    lora_workspace_bytes,
     verify_drafts, verify_drafts_workspace_bytes,
 )

@@ -118,8 +118,9 @@ SIGNATURES = {
                                   _vp, _c_int, _vp]),
     "moe_combine_backward": (_c_int, [_vp, _c_int, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _vp,
                                       _vp, _vp, _vp, _vp]),
+    "moe_lora_workspace_bytes": (_c_sz, [_c_i64, _c_int, _c_int]),
     "moe_lora": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp,
-                          _c_int, _vp, _vp, _vp, _c_int, _vp]),
+                          _c_int, _vp, _vp, _vp, _c_int, _vp, _c_sz, _vp]),
     "moe_verify_drafts_workspace_bytes": (_c_sz, [_c_int, _c_int]),
     "moe_verify_drafts": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _c_sz, _vp]),
@@ -1282,17 +1283,23 @@ def combine_backward(dy, rows, pair_pos, w=None, drows=None, dw=None, need_rows=
                              like.dtype, rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows, need_w)
 
 
+def lora_workspace_bytes(T: int, rank: int, n_seq: int) -> int:
+    return int(lib().moe_lora_workspace_bytes(_int32(T, "T"), _int32(rank, "rank"), _int32(n_seq, "n_seq")))
+
+
 @_on_stream
-def _lora(dev, stream, base, x, x_dtype, T, d_in, d_out, a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype):
+def _lora(dev, stream, base, x, x_dtype, T, d_in, d_out, a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype,
+          ws):
     if y is None:
         y = torch.empty_like(base)
+    wp, wn, keep = _scratch(lib().moe_lora_workspace_bytes(T, rank, 0 if seq_offsets is None else S), ws, dev)
     _check(lib().moe_lora(base.data_ptr(), x.data_ptr(), x_dtype, T, d_in, d_out, a.data_ptr(), b.data_ptr(), n,
                           rank, _addr(seq_offsets), S, adapter.data_ptr(), _addr(scale), y.data_ptr(), y_dtype,
-                          stream), "moe_lora")
+                          wp, wn, stream), "moe_lora")
     return y
 
 
-def lora(base, x, a, b, adapter, seq_offsets=None, scale=None, y=None, stream=None):
+def lora(base, x, a, b, adapter, seq_offsets=None, scale=None, y=None, ws=None, stream=None):
     """y[t] = base[t] + scale[m] b[m] (a[m] x[t]) for the rows t of every request,
     m = adapter[request] (moe_lora).
 
@@ -1316,8 +1323,10 @@ def lora(base, x, a, b, adapter, seq_offsets=None, scale=None, y=None, stream=No
               (y, (T, d_out), base.dtype, "y"), (x, (T, d_in), x.dtype, "x"), (base, (T, d_out), base.dtype, "base"),
               (a, (n, rank, d_in), torch.bfloat16, "a"), (b, (n, d_out, rank), torch.bfloat16, "b"),
               (adapter, (S,), torch.int32, "adapter")))
-    return _lora("lora", stream, (base, x, a, b, seq_offsets, adapter, scale, y), base, x, x_dtype, T, d_in, d_out,
-                 a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype)
+    if ws is not None:
+        _dev(ws, torch.uint8, "ws")
+    return _lora("lora", stream, (base, x, a, b, seq_offsets, adapter, scale, y, ws), base, x, x_dtype, T, d_in,
+                 d_out, a, b, n, rank, seq_offsets, S, adapter, scale, y, y_dtype, ws)
 
 
 def verify_drafts_workspace_bytes(B: int, V: int) -> int:

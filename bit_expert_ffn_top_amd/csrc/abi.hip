@@ -128,6 +128,7 @@ constexpr int64_t kMaxMxRows = (int64_t{1} << 24) - 1;
 bool valid_pairs(int64_t T, int64_t most, int k) {
   return T >= 0 && T <= most && k >= 1 && k <= MOE_MAX_TOPK;
 }
+bool valid_rank(int r) { return r >= 8 && r <= MOE_MAX_RANK && r % 8 == 0; }
 bool valid_row(int d) { return d >= 4 && d <= MOE_MAX_MX_COLS && d % 4 == 0; }
 
 bool valid_mx_cols(int cols) { return cols >= 32 && cols <= MOE_MAX_MX_COLS && cols % 32 == 0; }
@@ -730,24 +731,32 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
                                                     pair_pos, w, drows, dw, stream));
 }
 
+size_t moe_lora_workspace_bytes(int64_t T, int rank, int n_seq) {
+  if (T < 0 || T > kMaxMxRows || !valid_rank(rank) || n_seq < 0 || n_seq > 65536) return 0;
+  return bitffn::lora_workspace_bytes(T, rank, n_seq);
+}
+
 int moe_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
              const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
              const int32_t* seq_offsets, int n_seq, const int32_t* adapter, const float* scale,
-             void* y, int y_dtype, hipStream_t stream) {
+             void* y, int y_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return MOE_EINVAL;
   if (T < 0 || T > kMaxMxRows || !valid_mx_cols(d_in)) return MOE_EINVAL;
   if (d_out < 16 || d_out > MOE_MAX_MX_COLS || d_out % 16 != 0) return MOE_EINVAL;
   if (n_adapters < 1 || n_adapters > MOE_MAX_EXPERTS) return MOE_EINVAL;
-  if (rank < 8 || rank > MOE_MAX_RANK || rank % 8 != 0) return MOE_EINVAL;
+  if (!valid_rank(rank)) return MOE_EINVAL;
   if (n_seq < 0 || n_seq > 65536 || (seq_offsets ? n_seq < 1 : n_seq != T)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
-  if (!base || !x || !a || !b || !adapter || !y) return MOE_EINVAL;
+  const size_t need = bitffn::lora_workspace_bytes(T, rank, seq_offsets ? n_seq : 0);
+  if (!base || !x || !a || !b || !adapter || !y || (need > 0 && !ws)) return MOE_EINVAL;
   if (!aligned16(base) || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(adapter) ||
-      !aligned16(seq_offsets) || !aligned16(scale) || !aligned16(y))
+      !aligned16(seq_offsets) || !aligned16(scale) || !aligned16(y) || (need > 0 && !aligned256(ws)))
     return MOE_EALIGN;
-  if (!apart({y}, {x, a, b, seq_offsets, adapter, scale})) return MOE_EINVAL;
+  if (need > 0 && ws_bytes < need) return MOE_ENOSPC;
+  void* const work = need > 0 ? ws : nullptr;
+  if (!apart({y, work}, {x, a, b, seq_offsets, adapter, scale}) || (work && work == base)) return MOE_EINVAL;
   return hip_status(bitffn::launch_lora(base, x, x_dtype, T, d_in, d_out, a, b, n_adapters, rank,
-                                        seq_offsets, n_seq, adapter, scale, y, y_dtype, stream));
+                                        seq_offsets, n_seq, adapter, scale, y, y_dtype, ws, stream));
 }
 
 size_t moe_verify_drafts_workspace_bytes(int B, int V) {

@@ -1,16 +1,20 @@
 // Low-rank adapters of many requests beside a projection that they share:
 //   y[t] = base[t] + scale[m] * B_m (A_m x[t]),   m the adapter of t's request
 //
-// A workgroup takes 16 or 32 consecutive rows of one request (a row alone where
-// every row is a request) and a slice of the output columns, in one launch: the
-// product with A needs all of x before B can start, but A is small (64 KB at rank
-// 16 and 2048 columns), so that a slice's repeating it costs less than a second
-// launch.  Both products are on the matrix cores, with the adapter's rows as the
-// first operand, so that a lane of the result holds consecutive ranks or columns
-// of one token:
-//   h = A x    the eight wavefronts split the columns; their sums meet in LDS in
-//              a fixed order
-//   y = B h    the wavefronts split the slice's columns
+// Both products are on the matrix cores, with the adapter's rows as the first
+// operand:
+//   h = A x    16 or 32 consecutive rows of one request (a row alone where every
+//              row is a request); the eight wavefronts of a workgroup split the
+//              columns, and their sums meet in LDS in a fixed order
+//   y = B h    64 columns per wavefront
+// Few rows: both in one launch.  A workgroup repeats h for its slice of y's
+// columns; A is small (64 KB at rank 16 and 2048 columns), and a second launch
+// would cost more.  Many rows: two launches, with h in the workspace in the order
+// in which the second one's lanes read it.
+// Operands are read as their rows lie and change lanes in LDS: an operand's layout
+// read directly has 16 bytes of 16 rows in each quarter of a wavefront, and the
+// path to the cache then moves 16 bytes per cycle and CU instead of 64 (8,192
+// rows at rank 64: 45 us where this takes XX).  y leaves the same way.
 // fp32 values enter as sums of bfloat16 parts: x as three (exact but for its
 // smallest values), h as two where the results are bfloat16 (off by 2^-16 of it,
 // where they round by 2^-8) and three where they are fp32.  A row has the same
@@ -24,7 +28,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kGroup = 64;   // output columns that a wavefront takes at a time
+constexpr int kGroup = 64;   // output columns that belong together
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
@@ -38,7 +42,10 @@ struct LoraArgs {
   const float* scale;
   void* y;
   int T, d_in, d_out, n_adapters, rank, n_seq;
-  int slice;   // output columns of a workgroup, a multiple of kGroup
+  int slice;     // output columns of a workgroup, a multiple of kGroup
+  int4* tiles;   // in the workspace (many rows)
+  nu4* h;
+  int n_tiles;
 };
 
 __device__ __forceinline__ nf4 mfma(nu4 a, nu4 b, nf4 c) {
@@ -46,34 +53,27 @@ __device__ __forceinline__ nf4 mfma(nu4 a, nu4 b, nf4 c) {
                                                  c, 0, 0, 0);
 }
 
-// Eight consecutive values of x as bfloat16 parts.
+// Eight consecutive values of x, as they lie in LDS, as bfloat16 parts.
 template <typename XT>
-struct XPart;
+struct XParts;
 
 template <>
-struct XPart<uint16_t> {
+struct XParts<uint16_t> {
   static constexpr int kParts = 1;
-  nu4 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const nu4*>(p); }
-  __device__ __forceinline__ void split(nu4 (&out)[1]) const { out[0] = v; }
+  static __device__ __forceinline__ void split(const nu4 (&v)[1], nu4 (&out)[1]) { out[0] = v[0]; }
 };
 
 // The high halves of two words.
-__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
-  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
 template <>
-struct XPart<float> {
+struct XParts<float> {
   static constexpr int kParts = 3;
-  nf4 v[2];
-  __device__ __forceinline__ void load(const float* p) {
-    v[0] = reinterpret_cast<const nf4*>(p)[0];
-    v[1] = reinterpret_cast<const nf4*>(p)[1];
-  }
   // Each part takes the highest eight bits that are left: 24 in all.
-  __device__ __forceinline__ void split(nu4 (&out)[3]) const {
-    float r[8];
+  static __device__ __forceinline__ void split(const nu4 (&v)[2], nu4 (&out)[3]) {
+    uint32_t r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = v[i / 4][i % 4];
 #pragma unroll
@@ -82,22 +82,18 @@ struct XPart<float> {
       for (int i = 0; i < 4; ++i) out[part][i] = high_halves(r[2 * i], r[2 * i + 1]);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        r[i] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r[i]) & 0xFFFF0000u);
+        r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, r[i]) -
+                                                __builtin_bit_cast(float, r[i] & 0xFFFF0000u));
     }
   }
 };
 
 // Rows [row0, row1) and request of one tile of `rows` rows; false if there are
 // fewer tiles.  A request's rows end at the largest bound so far, clamped to the
-// rows there are.  Every wavefront searches for itself, eight bounds per lane.
-__device__ __forceinline__ bool find_tile(const LoraArgs& g, int tile, int rows, int& row0, int& row1,
-                                          int& request) {
-  if (!g.seq) {
-    row0 = request = tile;
-    row1 = tile + 1;
-    return tile < g.T;
-  }
-  constexpr int kPer = 8;
+// rows there are.  Every wavefront searches for itself, kPer bounds per lane.
+template <int kPer>
+__device__ __forceinline__ bool search_tile(const LoraArgs& g, int tile, int rows, int& row0, int& row1,
+                                            int& request) {
   const int lane = threadIdx.x & 63;
   int low = min(max(g.seq[0], 0), g.T);   // largest bound so far
   int before = 0;                         // tiles of the requests so far
@@ -149,198 +145,534 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& g, int tile, int rows,
   return false;
 }
 
-// MT: 16-rank tiles (rank <= 16 MT); NT: 16-row tiles.
-template <typename XT, typename YT, int MT, int NT>
-__global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
-  constexpr int XP = XPart<XT>::kParts;
-  constexpr int HP = sizeof(YT) == 4 ? 3 : 2;   // parts of h
-  constexpr int RS = (MT + 1) / 2;              // 32-rank steps of the second product
-  constexpr int kPartRow = 16 * MT + 4;         // LDS rows, padded against bank conflicts
-  constexpr int kHRow = 32 * RS + 8;
-  __shared__ __align__(16) float s_part[kWaves][16 * NT][kPartRow];
-  __shared__ __align__(16) uint16_t s_h[HP][16 * NT][kHRow];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l16 = lane & 15, quad = lane >> 4;
-  int row0, row1, request;
-  if (!find_tile(g, blockIdx.x, 16 * NT, row0, row1, request)) return;
-  const int m = g.adapter[request];
-  const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
+__device__ __forceinline__ bool find_tile(const LoraArgs& g, int tile, int rows, int& row0, int& row1,
+                                          int& request) {
+  if (!g.seq) {
+    row0 = request = tile;
+    row1 = tile + 1;
+    return tile < g.T;
+  }
+  return g.n_seq <= 64 ? search_tile<1>(g, tile, rows, row0, row1, request)
+                       : search_tile<8>(g, tile, rows, row0, row1, request);
+}
+
+// Rows of a tile without an adapter: columns [n0, n1) of base.
+template <typename YT>
+__device__ __forceinline__ void copy_base(const LoraArgs& g, int row0, int row1, int n0, int n1) {
   const YT* base = static_cast<const YT*>(g.base);
   YT* y = static_cast<YT*>(g.y);
-  if (m < 0 || m >= g.n_adapters) {   // no adapter
-    if (y == base) return;
-    const int parts = (n1 - n0) / 8;
-    for (int i = tid; i < (row1 - row0) * parts; i += kThreads) {
-      const int t = i / parts;
-      const int64_t at = static_cast<int64_t>(row0 + t) * g.d_out + n0 + 8 * (i - t * parts);
-      RowPart<YT, 8> v;
-      v.load(base + at);
-      v.store(y + at);
+  if (y == base) return;
+  const int parts = (n1 - n0) / 8;
+  for (int i = threadIdx.x; i < (row1 - row0) * parts; i += blockDim.x) {
+    const int t = i / parts;
+    const int64_t at = static_cast<int64_t>(row0 + t) * g.d_out + n0 + 8 * (i - t * parts);
+    RowPart<YT, 8> v;
+    v.load(base + at);
+    v.store(y + at);
+  }
+}
+
+// 16 rows of 128 bytes of a matrix: a lane holds chunk lane % 8 (16 bytes) of rows
+// lane / 8 and lane / 8 + 8.  In LDS a row's chunks are exchanged by its number, so
+// that eight lanes that read one chunk of eight rows meet no bank twice.
+constexpr int kUnitBytes = 2048;
+
+struct UnitRows {
+  uint32_t at[2];   // the lane's rows and chunk, bytes from the matrix's start
+  __device__ __forceinline__ void set(int row, int last, uint32_t row_bytes) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) at[h] = min(row + (lane >> 3) + 8 * h, last) * row_bytes + 16 * (lane & 7);
+  }
+};
+
+// Order between the LDS accesses of one wavefront's lanes, which take effect as
+// they are issued: for the compiler only.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ void put_unit(char* lds, const nu4 (&v)[2]) {
+  const int lane = threadIdx.x & 63, row = lane >> 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)   // rows 8 apart have one exchange
+    *reinterpret_cast<nu4*>(lds + 128 * (row + 8 * h) + 16 * ((lane & 7) ^ row)) = v[h];
+}
+
+__device__ __forceinline__ nu4 get_chunk(const char* lds, int row, int chunk) {
+  return *reinterpret_cast<const nu4*>(lds + 128 * row + 16 * (chunk ^ (row & 7)));
+}
+
+// Shared memory of one wavefront, in its three uses.
+template <typename XT, int MT, int NT>
+struct Down {
+  static constexpr int kUnits = sizeof(XT) / 2;   // of x, for 64 columns
+  static constexpr int kRanks = MT < 4 ? MT : 4;  // 16-rank tiles of a pass
+  static constexpr int kPartRow = 16 * kRanks + 4;
+  static constexpr int kStage = (NT * kUnits + 2) * kUnitBytes;
+  static constexpr int kPart = 16 * NT * kPartRow * 4;
+  static constexpr int kBytes = kStage > kPart ? kStage : kPart;
+  // 64-column units asked for at a time
+  static constexpr int kAhead = kRanks * NT <= 1 ? 4 : kRanks * NT <= 2 ? 2 : 1;
+};
+
+// A wavefront's share of h = A x for 16 NT rows and the ranks from 64 pass on,
+// left in its part of LDS: [row][rank].
+template <typename XT, int MT, int NT>
+__device__ __forceinline__ void down_product(const LoraArgs& g, int m, int row0, int row1, int pass,
+                                             char* lds) {
+  using D = Down<XT, MT, NT>;
+  constexpr int MP = D::kRanks, XU = D::kUnits, XP = XParts<XT>::kParts, U = D::kAhead;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15, quad = lane >> 4;
+  const char* a = reinterpret_cast<const char*>(g.a + static_cast<int64_t>(m) * g.rank * g.d_in);
+  const char* x = reinterpret_cast<const char*>(static_cast<const XT*>(g.x) + static_cast<int64_t>(row0) * g.d_in);
+  UnitRows ar[MP], xr[NT];
+#pragma unroll
+  for (int i = 0; i < MP; ++i) ar[i].set(64 * pass + 16 * i, g.rank - 1, g.d_in * 2);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) xr[j].set(16 * j, row1 - row0 - 1, g.d_in * sizeof(XT));
+  nf4 acc[MP][NT];
+#pragma unroll
+  for (int i = 0; i < MP; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = nf4{0.0f, 0.0f, 0.0f, 0.0f};
+  char* xs = lds;
+  char* as = lds + NT * XU * kUnitBytes;
+  const int units = (g.d_in + 63) / 64;
+  for (int u0 = wave; u0 < units; u0 += kWaves * U) {
+    nu4 av[U][MP][2], xv[U][NT][XU][2];
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int u = min(u0 + kWaves * n, units - 1);
+      // the last unit of bfloat16 rows may end after 32 columns
+      const uint32_t c = 128 * u, back = c + 16 * (lane & 7) >= static_cast<uint32_t>(g.d_in) * 2 ? 64 : 0;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int w = 0; w < XU; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t cx = XU == 1 ? c - back : min(256 * u + 128 * w, g.d_in * 4 - 128);
+            xv[n][j][w][h] = *reinterpret_cast<const nu4*>(x + (xr[j].at[h] + cx));
+          }
+#pragma unroll
+      for (int i = 0; i < MP; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) av[n][i][h] = *reinterpret_cast<const nu4*>(a + (ar[i].at[h] + (c - back)));
     }
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int u = u0 + kWaves * n;
+      if (u >= units) break;   // uniform
+      wave_order();
+      const bool whole = 64 * u + 32 < g.d_in;
+      nu4 xp[2][NT][XP];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int w = 0; w < XU; ++w) put_unit(xs + (j * XU + w) * kUnitBytes, xv[n][j][w]);
+        wave_order();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          nu4 v[XU];
+#pragma unroll
+          for (int w = 0; w < XU; ++w)
+            v[w] = XU == 1 ? get_chunk(xs + j * kUnitBytes, l16, 4 * s + quad)
+                           : get_chunk(xs + (j * XU + s) * kUnitBytes, l16, 2 * quad + w);
+          XParts<XT>::split(v, xp[s][j]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MP; ++i) {
+        char* at = as + (i & 1) * kUnitBytes;
+        put_unit(at, av[n][i]);
+        wave_order();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s == 1 && !whole) break;   // uniform
+          const nu4 af = get_chunk(at, l16, 4 * s + quad);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int p = 0; p < XP; ++p) acc[i][j] = mfma(af, xp[s][j][p], acc[i][j]);
+        }
+      }
+    }
+  }
+  wave_order();
+  float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < MP; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<nf4*>(part + (16 * j + l16) * D::kPartRow + 16 * i + 4 * quad) = acc[i][j];
+}
+
+// The next bfloat16 part of h, which keeps the rest (an infinity has none).
+__device__ __forceinline__ float take_part(float& h) {
+  const float v = bf16_bits_to_float(pack_bf16(h, 0.0f) & 0xFFFFu);
+  h = __builtin_isfinite(v) ? h - v : 0.0f;
+  return v;
+}
+
+// Eight ranks (64 pass + 32 step + 8 quad ..) of token t: the wavefronts' sums in
+// order, scaled, as bfloat16 parts; zeros past the adapter's rank.
+template <typename D, int HP, int STRIDE>   // STRIDE: from one wavefront's sums to the next one's
+__device__ __forceinline__ void join_sums(const char* lds, int t, int r, int ranks, float scale, nu4 (&out)[HP]) {
+  float h[8];
+  if (r < ranks) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float* part = reinterpret_cast<const float*>(lds + w * STRIDE) + t * D::kPartRow + r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] += part[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] *= scale;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+  }
+#pragma unroll
+  for (int p = 0; p < HP; ++p)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = take_part(h[2 * e]), hi = take_part(h[2 * e + 1]);
+      out[p][e] = pack_bf16(lo, hi);
+    }
+}
+
+template <typename YT>
+constexpr int h_parts() {
+  return sizeof(YT) == 4 ? 3 : 2;
+}
+
+// Rows c .. c + COLS - 1 of B, which follow each other in memory, 16 bytes per
+// lane and load; in LDS a row has an odd number of chunks, so that eight lanes that
+// read one chunk of eight rows meet no bank twice.
+template <int RS, int COLS, int THREADS>
+struct BRows {
+  static constexpr int kLoads = (COLS * 4 * RS + THREADS - 1) / THREADS;   // at the largest rank
+  static constexpr int kBytes = COLS * (4 * RS + 1) * 16;
+  nu4 v[kLoads];
+  __device__ __forceinline__ void load(const LoraArgs& g, const uint16_t* b, int c, int thread) {
+    const int chunks = min(COLS, g.d_out - c) * (g.rank / 8);
+    const nu4* src = reinterpret_cast<const nu4*>(b + static_cast<int64_t>(c) * g.rank);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n)
+      if (n * THREADS < chunks) v[n] = src[min(n * THREADS + thread, chunks - 1)];   // uniform
+  }
+  __device__ __forceinline__ void put(const LoraArgs& g, int c, char* lds, int thread) const {
+    const int per = g.rank / 8, chunks = min(COLS, g.d_out - c) * per;
+    const uint32_t over = (65535u + per) / per;   // i / per = i * over >> 16 for i * per < 2^16
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int i = n * THREADS + thread;
+      if (i < chunks) {
+        const int row = i * over >> 16;
+        *reinterpret_cast<nu4*>(lds + 16 * (row * (per | 1) + (i - row * per))) = v[n];
+      }
+    }
+  }
+  // Lane's chunk of row `row`: ranks 32 s + 8 quad .., zeros past the adapter's.
+  static __device__ __forceinline__ nu4 get(const LoraArgs& g, const char* lds, int row, int s) {
+    const int per = g.rank / 8, chunk = 4 * s + ((threadIdx.x & 63) >> 4);
+    const nu4 b = *reinterpret_cast<const nu4*>(lds + 16 * (row * (per | 1) + min(chunk, per - 1)));
+    return chunk < per ? b : nu4{0, 0, 0, 0};
+  }
+};
+
+// A wavefront's 16 rows of COLS columns of base and y as they lie: a lane holds
+// eight columns of each of kLoads rows.
+template <typename YT, int COLS>
+struct YRows {
+  static constexpr int kPerRow = COLS / 8, kRows = 64 / kPerRow, kLoads = 16 / kRows;
+  RowPart<YT, 8> v[kLoads];
+  __device__ __forceinline__ void load(const LoraArgs& g, int row0, int row1, int c) {
+    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int t = row0 + n * kRows + lane / kPerRow;
+      if (t < row1 && col < g.d_out)
+        v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(t) * g.d_out + col);
+    }
+  }
+  __device__ __forceinline__ void copy(const LoraArgs& g, int row0, int row1, int c) const {
+    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int t = row0 + n * kRows + lane / kPerRow;
+      if (t < row1 && col < g.d_out)
+        v[n].template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(t) * g.d_out + col);
+    }
+  }
+  // y = base + the results in LDS, [row][COLS + 4]
+  __device__ __forceinline__ void store(const LoraArgs& g, int row0, int row1, int c, const float* lds) {
+    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int t = n * kRows + lane / kPerRow;
+      const nf4* d = reinterpret_cast<const nf4*>(lds + t * (COLS + 4) + 8 * (lane % kPerRow));
+      const nf4 lo = d[0], hi = d[1];
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = v[n].get(e) + (e < 4 ? lo[e % 4] : hi[e % 4]);
+      if (row0 + t < row1 && col < g.d_out) {
+        RowPart<YT, 8> out;
+        out.set(f);
+        out.template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(row0 + t) * g.d_out + col);
+      }
+    }
+  }
+};
+
+// B h of 16 columns per row tile of B and 16 tokens, to LDS [token][COLS + 4].
+template <int RS, int HP, int COLS>
+__device__ __forceinline__ void up_product(const nu4 (&bv)[RS], const nu4 (&hv)[HP][RS], float* lds, int tile) {
+  const int lane = threadIdx.x & 63;
+  nf4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < RS; ++s)
+#pragma unroll
+    for (int p = 0; p < HP; ++p) acc = mfma(bv[s], hv[p][s], acc);
+  *reinterpret_cast<nf4*>(lds + (lane & 15) * (COLS + 4) + 16 * tile + 4 * (lane >> 4)) = acc;
+}
+
+__device__ __forceinline__ int adapter_of(const LoraArgs& g, int request) {
+  return __builtin_amdgcn_readfirstlane(g.adapter[request]);
+}
+
+// Few rows, one launch.  MT: 16-rank tiles (rank <= 16 MT).
+template <typename XT, typename YT, int MT>
+__global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
+  using D = Down<XT, MT, 1>;
+  constexpr int HP = h_parts<YT>();
+  constexpr int RS = (MT + 1) / 2;   // 32-rank steps of the second product
+  constexpr int kCols = 32;          // columns that a wavefront takes at a time
+  using B = BRows<RS, kCols, 64>;
+  constexpr int kUp = B::kBytes + 16 * (kCols + 4) * 4;
+  constexpr int kWaveBytes = D::kBytes > kUp ? D::kBytes : kUp;
+  static_assert(kWaveBytes % 16 == 0, "");
+  __shared__ __align__(16) char s_wave[kWaves * kWaveBytes];
+  __shared__ nu4 s_h[HP][RS][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int row0, row1, request;
+  if (!find_tile(g, blockIdx.x, 16, row0, row1, request)) return;
+  const int m = adapter_of(g, request);
+  const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
+  if (m < 0 || m >= g.n_adapters) {
+    copy_base<YT>(g, row0, row1, n0, n1);
     return;
   }
   const float scale = g.scale ? g.scale[m] : 1.0f;
-
-  // h = A x: lane (l16, quad) reads 8 columns of row l16 of each operand
-  {
-    const uint16_t* a = g.a + static_cast<int64_t>(m) * g.rank * g.d_in + 8 * quad;
-    const XT* x = static_cast<const XT*>(g.x) + 8 * quad;
-    const uint16_t* ar[MT];
-    const XT* xr[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) ar[i] = a + static_cast<int64_t>(min(16 * i + l16, g.rank - 1)) * g.d_in;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = x + static_cast<int64_t>(min(row0 + 16 * i + l16, row1 - 1)) * g.d_in;
-    nf4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = nf4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = g.d_in / 32, per = (steps + kWaves - 1) / kWaves;
-    const int k0 = min(steps, wave * per), k1 = min(steps, k0 + per);
-    constexpr int U = MT * NT <= 2 ? 8 : MT * NT <= 4 ? 4 : 2;
-    for (int k = k0; k < k1; k += U) {
-      nu4 av[U][MT];
-      XPart<XT> xv[U][NT];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = 32 * min(k + u, k1 - 1);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) av[u][i] = *reinterpret_cast<const nu4*>(ar[i] + c);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) xv[u][j].load(xr[j] + c);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k + u < k1) {   // uniform
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            nu4 xp[XP];
-            xv[u][j].split(xp);
-#pragma unroll
-            for (int part = 0; part < XP; ++part)
-#pragma unroll
-              for (int i = 0; i < MT; ++i) acc[i][j] = mfma(av[u][i], xp[part], acc[i][j]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        *reinterpret_cast<nf4*>(&s_part[wave][16 * j + l16][16 * i + 4 * quad]) = acc[i][j];
-  }
-  __syncthreads();
-  for (int i = tid; i < 16 * NT * 32 * RS; i += kThreads) {
-    const int t = i / (32 * RS), r = i - t * (32 * RS);
-    float h = 0.0f;
-    if (r < g.rank) {
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) h += s_part[w][t][r];
-      h *= scale;
-    }
-#pragma unroll
-    for (int part = 0; part < HP; ++part) {
-      const uint32_t p = pack_bf16(h, 0.0f) & 0xFFFFu;
-      s_h[part][t][r] = static_cast<uint16_t>(p);
-      const float v = bf16_bits_to_float(p);
-      h = __builtin_isfinite(v) ? h - v : 0.0f;   // an infinity has no rest
-    }
-  }
-  __syncthreads();
-
-  // y = base + B h: rows of B are dealt to the two results of 32 columns so that
-  // a lane holds columns 8 quad .. 8 quad + 7 of token l16
-  nu4 hv[HP][RS][NT];
-#pragma unroll
-  for (int part = 0; part < HP; ++part)
-#pragma unroll
-    for (int s = 0; s < RS; ++s)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        hv[part][s][j] = *reinterpret_cast<const nu4*>(&s_h[part][16 * j + l16][32 * s + 8 * quad]);
+  char* mine = s_wave + wave * kWaveBytes;
   const uint16_t* b = g.b + static_cast<int64_t>(m) * g.d_out * g.rank;
-  const int column = 8 * (l16 >> 2) + (l16 & 3);   // of this lane's row of B, the second result's 4 further
-  const int groups = (n1 - n0 + kGroup - 1) / kGroup, per = (groups + kWaves - 1) / kWaves;
-  for (int k = wave * per; k < min(groups, (wave + 1) * per); ++k) {
-    const int c0 = n0 + k * kGroup;
+  const int blocks = (n1 - n0 + kCols - 1) / kCols, per = (blocks + kWaves - 1) / kWaves;
+  const int k0 = min(blocks, wave * per), k1 = min(blocks, k0 + per);
+  // the first block's rows of B and base are on their way meanwhile
+  B bl;
+  YRows<YT, kCols> yr;
+  if (k0 < k1) {
+    bl.load(g, b, n0 + k0 * kCols, lane);
+    yr.load(g, row0, row1, n0 + k0 * kCols);
+  }
+  for (int pass = 0; pass < MT / D::kRanks; ++pass) {
+    down_product<XT, MT, 1>(g, m, row0, row1, pass, mine);
+    __syncthreads();
+    constexpr int kSteps = (D::kRanks + 1) / 2;
+    if (tid < 64 * kSteps) {
+      const int r = 32 * wave + 8 * (lane >> 4);
+      nu4 h[HP];
+      join_sums<D, HP, kWaveBytes>(s_wave, lane & 15, r, min(g.rank - 64 * pass, 16 * D::kRanks), scale, h);
 #pragma unroll
-    for (int blk = 0; blk < kGroup / 32; ++blk) {
-      const int c = c0 + 32 * blk;
-      if (c >= n1) break;   // uniform
-      nu4 bv[2][RS];
+      for (int p = 0; p < HP; ++p) s_h[p][2 * pass + wave][lane] = h[p];
+    }
+    __syncthreads();
+  }
+  nu4 hv[HP][RS];
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+  for (int p = 0; p < HP; ++p)
 #pragma unroll
-        for (int s = 0; s < RS; ++s) {
-          const int r = 32 * s + 8 * quad;
-          const int64_t at = static_cast<int64_t>(min(c + column + 4 * half, g.d_out - 1)) * g.rank;
-          const nu4 v = *reinterpret_cast<const nu4*>(b + at + min(r, g.rank - 8));
-          bv[half][s] = r < g.rank ? v : nu4{0, 0, 0, 0};
-        }
+    for (int s = 0; s < RS; ++s) hv[p][s] = s_h[p][s][lane];
+  float* res = reinterpret_cast<float*>(mine + B::kBytes);
+  for (int k = k0; k < k1; ++k) {
+    const int c = n0 + k * kCols;
+    wave_order();
+    bl.put(g, c, mine, lane);
+    wave_order();
+    if (k + 1 < k1) bl.load(g, b, c + kCols, lane);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int t = row0 + 16 * j + l16;
-        const bool there = t < row1 && c + 8 * quad < n1;
-        const int64_t at = static_cast<int64_t>(t) * g.d_out + c + 8 * quad;
-        RowPart<YT, 8> v;
-        if (there) v.load(base + at);
-        nf4 acc[2];
+    for (int tile = 0; tile < kCols / 16; ++tile) {
+      nu4 bv[RS];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          acc[half] = nf4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int s = 0; s < RS; ++s) bv[s] = B::get(g, mine, 16 * tile + (lane & 15), s);
+      up_product<RS, HP, kCols>(bv, hv, res, tile);
+    }
+    wave_order();
+    yr.store(g, row0, row1, c, res);
+    if (k + 1 < k1) yr.load(g, row0, row1, c + kCols);
+  }
+}
+
+// Many rows, two launches.  The workspace holds a table of the first one's tiles
+// (rows, request, adapter or -1), which spares the second one the search, and h by
+// 16 rows in the order of the second product's operand:
+// [tile][16 rows][part][step][lane][8].
+constexpr int kTileRows = 32;
+constexpr int kTiles16 = kTileRows / 16;
+constexpr int kUpWaves = 2;    // tiles of a workgroup
+
+template <typename XT, typename YT, int MT>
+__global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
+  using D = Down<XT, MT, kTiles16>;
+  constexpr int HP = h_parts<YT>(), RS = (MT + 1) / 2;
+  __shared__ __align__(16) char s_wave[kWaves * D::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int row0 = 0, row1 = 0, request, m = -1;
+  if (find_tile(g, blockIdx.x, kTileRows, row0, row1, request)) m = adapter_of(g, request);
+  if (m >= g.n_adapters) m = -1;
+  if (tid == 0) g.tiles[blockIdx.x] = make_int4(row0, row1, m, 0);
+  if (m < 0) return;
+  const float scale = g.scale ? g.scale[m] : 1.0f;
+  for (int pass = 0; pass < MT / D::kRanks; ++pass) {
+    if (pass) __syncthreads();   // the sums have been read
+    down_product<XT, MT, kTiles16>(g, m, row0, row1, pass, s_wave + wave * D::kBytes);
+    __syncthreads();
+    constexpr int kSteps = (D::kRanks + 1) / 2;
+    if (wave < kSteps * kTiles16) {
+      const int part16 = wave / kSteps, step = wave - part16 * kSteps;
+      nu4 h[HP];
+      join_sums<D, HP, D::kBytes>(s_wave, 16 * part16 + (lane & 15), 32 * step + 8 * (lane >> 4),
+                                  min(g.rank - 64 * pass, 16 * D::kRanks), scale, h);
+      nu4* out = g.h + (static_cast<int64_t>(blockIdx.x) * kTiles16 + part16) * (HP * RS * 64) + lane;
 #pragma unroll
-          for (int s = 0; s < RS; ++s)
-#pragma unroll
-            for (int part = 0; part < HP; ++part)
-              acc[half] = mfma(bv[half][s], hv[part][s][j], acc[half]);
-        }
-        if (there) {
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = v.get(i) + acc[i / 4][i % 4];
-          v.set(f);
-          v.store(y + at);
-        }
-      }
+      for (int p = 0; p < HP; ++p) out[(p * RS + 2 * pass + step) * 64] = h[p];
     }
   }
 }
 
-template <typename XT, typename YT, int NT>
-void launch_tiles(LoraArgs g, hipStream_t s) {
-  const int rows = 16 * NT;
-  // ceil(n / rows) summed over the requests is at most this
-  const int64_t tiles = g.seq ? (g.T + static_cast<int64_t>(rows - 1) * min(g.n_seq, g.T)) / rows : g.T;
+// A workgroup takes 64 columns of two tiles, one per wavefront.  B goes through
+// LDS for all of them, adapter by adapter where the tiles' requests have different
+// ones.
+template <typename YT, int RS>
+__global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
+  constexpr int HP = h_parts<YT>();
+  using B = BRows<RS, kGroup, 64 * kUpWaves>;
+  __shared__ __align__(16) char s_b[B::kBytes];
+  __shared__ __align__(16) float s_res[kUpWaves][16 * (kGroup + 4)];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tile = blockIdx.x * kUpWaves + wave, c = blockIdx.y * kGroup;
+  const int4 mine = tile < g.n_tiles ? g.tiles[tile] : make_int4(0, 0, -1, 0);
+  const int row0 = mine.x, row1 = mine.y, m = mine.z;
+  int all[kUpWaves];   // the tiles' adapters
+#pragma unroll
+  for (int w = 0; w < kUpWaves; ++w) {
+    const int t = blockIdx.x * kUpWaves + w;
+    all[w] = t < g.n_tiles ? g.tiles[t].z : -1;
+  }
+  YRows<YT, kGroup> yr[kTiles16];
+#pragma unroll
+  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, row0 + 16 * j, row1, c);
+  nu4 hv[kTiles16][HP][RS];
+  if (m >= 0) {
+    const nu4* h = g.h + static_cast<int64_t>(tile) * kTiles16 * (HP * RS * 64) + lane;
+#pragma unroll
+    for (int j = 0; j < kTiles16; ++j)
+#pragma unroll
+      for (int p = 0; p < HP; ++p)
+#pragma unroll
+        for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
+  } else if (g.y != g.base) {   // no adapter
+#pragma unroll
+    for (int j = 0; j < kTiles16; ++j) yr[j].copy(g, row0 + 16 * j, row1, c);
+  }
+  bool first = true;
+  for (int w = 0; w < kUpWaves; ++w) {
+    const int who = all[w];
+    bool again = who < 0;
+    for (int v = 0; v < w; ++v) again |= all[v] == who;
+    if (again) continue;   // uniform
+    if (!first) __syncthreads();   // the last adapter's rows have been read
+    first = false;
+    {
+      B bl;
+      bl.load(g, g.b + static_cast<int64_t>(who) * g.d_out * g.rank, c, tid);
+      bl.put(g, c, s_b, tid);
+    }
+    __syncthreads();
+    if (m != who) continue;
+#pragma unroll
+    for (int j = 0; j < kTiles16; ++j) {
+#pragma unroll
+      for (int t = 0; t < kGroup / 16; ++t) {
+        nu4 bv[RS];
+#pragma unroll
+        for (int s = 0; s < RS; ++s) bv[s] = B::get(g, s_b, 16 * t + (lane & 15), s);
+        up_product<RS, HP, kGroup>(bv, hv[j], s_res[wave], t);
+      }
+      wave_order();
+      yr[j].store(g, row0 + 16 * j, row1, c, s_res[wave]);
+      wave_order();
+    }
+  }
+}
+
+// ceil(n / rows) summed over the requests is at most this.
+int most_tiles(int64_t T, int n_seq, int rows) {
+  return static_cast<int>((T + (rows - 1) * min(static_cast<int64_t>(n_seq), T)) / rows);
+}
+
+template <typename XT, typename YT, int MT>
+hipError_t launch_rank(LoraArgs g, hipStream_t s) {
   const int groups = (g.d_out + kGroup - 1) / kGroup;
-  const int slices = static_cast<int>(max(int64_t{1}, min(int64_t{(groups + kWaves - 1) / kWaves}, 512 / tiles)));
+  if (g.h) {
+    lora_down_kernel<XT, YT, MT><<<g.n_tiles, kThreads, 0, s>>>(g);
+    const dim3 grid((g.n_tiles + kUpWaves - 1) / kUpWaves, groups);
+    lora_up_kernel<YT, (MT + 1) / 2><<<grid, 64 * kUpWaves, 0, s>>>(g);
+    return hipGetLastError();
+  }
+  const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
+  const int slices = static_cast<int>(max(int64_t{1}, min(int64_t{groups}, 192 / tiles)));
   g.slice = (groups + slices - 1) / slices * kGroup;
   const dim3 grid(static_cast<unsigned>(tiles), (g.d_out + g.slice - 1) / g.slice);
-  if (g.rank <= 16)
-    lora_kernel<XT, YT, 1, NT><<<grid, kThreads, 0, s>>>(g);
-  else if (g.rank <= 32)
-    lora_kernel<XT, YT, 2, NT><<<grid, kThreads, 0, s>>>(g);
-  else if (g.rank <= 64)
-    lora_kernel<XT, YT, 4, NT><<<grid, kThreads, 0, s>>>(g);
-  else
-    lora_kernel<XT, YT, 8, NT><<<grid, kThreads, 0, s>>>(g);
+  lora_kernel<XT, YT, MT><<<grid, kThreads, 0, s>>>(g);
+  return hipGetLastError();
 }
 
 template <typename XT, typename YT>
 hipError_t launch_as(const LoraArgs& g, hipStream_t s) {
-  launch_tiles<XT, YT, 1>(g, s);
-  return hipGetLastError();
+  if (g.rank <= 16) return launch_rank<XT, YT, 1>(g, s);
+  if (g.rank <= 32) return launch_rank<XT, YT, 2>(g, s);
+  if (g.rank <= 64) return launch_rank<XT, YT, 4>(g, s);
+  return launch_rank<XT, YT, 8>(g, s);
 }
 
+// Rows from which two launches are made.
+constexpr int64_t kManyRows = 1024;
+
 }  // namespace
+
+size_t lora_workspace_bytes(int64_t T, int rank, int n_seq) {
+  if (n_seq == 0 || T < kManyRows) return 0;   // 0: a row for every request
+  const int64_t tiles = most_tiles(T, n_seq, kTileRows), steps = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
+  return static_cast<size_t>(align256(tiles * 16) + tiles * kTiles16 * 3 * steps * 1024);
+}
 
 hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
                        const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
                        const int32_t* seq, int n_seq, const int32_t* adapter, const float* scale,
-                       void* y, int y_dtype, hipStream_t s) {
-  const LoraArgs g{base, x, a, b, seq, adapter, scale, y, static_cast<int>(T),
-                   d_in, d_out, n_adapters, rank, n_seq, 0};
+                       void* y, int y_dtype, void* ws, hipStream_t s) {
+  LoraArgs g{base, x, a, b, seq, adapter, scale, y, static_cast<int>(T),
+             d_in, d_out, n_adapters, rank, n_seq, 0, nullptr, nullptr, 0};
+  if (lora_workspace_bytes(T, rank, seq ? n_seq : 0) > 0) {
+    g.n_tiles = most_tiles(T, n_seq, kTileRows);
+    g.tiles = static_cast<int4*>(ws);
+    g.h = reinterpret_cast<nu4*>(static_cast<char*>(ws) + align256(int64_t{g.n_tiles} * 16));
+  }
   const bool xf = x_dtype == MOE_DTYPE_F32, yf = y_dtype == MOE_DTYPE_F32;
   const auto f = xf ? (yf ? launch_as<float, float> : launch_as<float, uint16_t>)
                     : (yf ? launch_as<uint16_t, float> : launch_as<uint16_t, uint16_t>);

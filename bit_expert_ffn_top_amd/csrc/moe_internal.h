@@ -165,11 +165,12 @@ hipError_t launch_combine_backward(const void* dy, int dy_dtype, const void* row
                                    int64_t R, int T, int d, int k, const int32_t* pair_pos,
                                    const float* w, void* drows, float* dw, hipStream_t s);
 
-// Low-rank adapters of many requests (lora.hip).
+// Low-rank adapters of many requests (lora.hip).  n_seq = 0: without bounds.
+size_t lora_workspace_bytes(int64_t T, int rank, int n_seq);
 hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
                        const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
                        const int32_t* seq, int n_seq, const int32_t* adapter, const float* scale,
-                       void* y, int y_dtype, hipStream_t s);
+                       void* y, int y_dtype, void* ws, hipStream_t s);
 
 // Verification of drafted tokens (verify_drafts.hip).
 size_t verify_workspace_bytes(int B, int V);

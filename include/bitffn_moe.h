@@ -728,12 +728,17 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
  * one padded with zeros.
  * Limits: 0 <= T < 2^24, 1 <= n_seq <= 65536 (n_seq = T = 0 without seq_offsets),
  * 1 <= n_adapters <= MOE_MAX_EXPERTS, rank a multiple of 8 in 8..MOE_MAX_RANK,
- * d_in a multiple of 32 and d_out of 16, both up to MOE_MAX_MX_COLS. */
+ * d_in a multiple of 32 and d_out of 16, both up to MOE_MAX_MX_COLS.
+ * ws: at least moe_lora_workspace_bytes(T, rank, n_seq) bytes (n_seq = 0 without
+ * seq_offsets), 256-byte aligned (0 for few rows, then ws may be NULL, and for
+ * sizes out of range). */
 #define MOE_MAX_RANK 128
+size_t moe_lora_workspace_bytes(int64_t T, int rank, int n_seq);
 int moe_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
              const uint16_t* a, const uint16_t* b, int n_adapters, int rank,
              const int32_t* seq_offsets, int n_seq, const int32_t* adapter,
-             const float* scale, void* y, int y_dtype, hipStream_t stream);
+             const float* scale, void* y, int y_dtype, void* ws, size_t ws_bytes,
+             hipStream_t stream);
 
 /* Verification of drafted tokens ("Strata" page, "投機的デコード": a pass over
  * the layers verifies the drafts).  Request s has m = n_draft[s] drafts

@@ -41,9 +41,9 @@ def _backward(p, gt=1, rt=1, R=200, T=100, d=64, k=2):
                                        p["dw"], None)
 
 
-def _lora(p, xt=1, T=100, d_in=64, d_out=48, n=4, rank=16, S=7, yt=1):
+def _lora(p, xt=1, T=100, d_in=64, d_out=48, n=4, rank=16, S=7, yt=1, nb=1 << 40):
     return _lib().moe_lora(p["base"], p["x"], xt, T, d_in, d_out, p["a"], p["b"], n, rank, p["seq"], S, p["adapter"],
-                           p["scale"], p["y"], yt, None)
+                           p["scale"], p["y"], yt, p["ws"], nb, None)
 
 
 def _verify(p, dtype=0, B=3, n=4, V=1000, nb=1 << 30):
@@ -162,7 +162,10 @@ def test_workspaces():
         assert lib.moe_dispatch_workspace_bytes(*bad) == 0, bad
     for bad in ((-1, 10), (65537, 10), (1, 0), (1, 1 << 24), (INT_MAX, INT_MAX)):
         assert lib.moe_verify_drafts_workspace_bytes(*bad) == 0, bad
-    cases = [(_dispatch, lib.moe_dispatch_workspace_bytes(60000, 64, 1000), dict(T=60000, k=64, E=1000)),
+    for bad in ((-1, 16, 4), (1 << 24, 16, 4), (9999, 12, 4), (9999, 136, 4), (9999, 16, -1), (9999, 16, 65537)):
+        assert lib.moe_lora_workspace_bytes(*bad) == 0, bad
+    cases = [(_lora, lib.moe_lora_workspace_bytes(1 << 20, 128, 7), dict(T=1 << 20, rank=128)),
+             (_dispatch, lib.moe_dispatch_workspace_bytes(60000, 64, 1000), dict(T=60000, k=64, E=1000)),
              (_verify, lib.moe_verify_drafts_workspace_bytes(1, 1 << 20), dict(B=1, V=1 << 20))]
     for call, need, kw in cases:
         p = _ptrs(call)

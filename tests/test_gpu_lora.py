@@ -214,3 +214,31 @@ def test_far_adapters():
     for t, sign in ((0, 1.0), (1, -1.0), (2, 0.0)):
         r = ol.lora(_np(base)[t:t + 1], _np(x)[t:t + 1], _np(al), sign * _np(bl), [0], None, None)
         assert (np.abs(_np(y)[t:t + 1] - r["y"]) <= _bound(r, d, rank, F32)).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rank,d_in,d_out", [(8, 96, 80), (24, 64, 64), (64, 512, 144), (72, 160, 96), (128, 288, 336)])
+def test_many_rows(rank, d_in, d_out, types):
+    """1,024 rows and more take two launches: bounds that leave rows out at both
+    ends, requests without rows and without an adapter, tiles that end inside a
+    request, neighbouring tiles of several adapters; and the bits that each
+    request has alone, in one launch."""
+    bf = _bf()
+    T, n = 1300, 4
+    base, x, a, b, scale = _inputs(T, n, rank, d_in, d_out, *types)
+    seq = np.array([5, 105, 105, 110, 141, 173, 174, 500, 700, 1023, 1024, 1290])
+    who = np.array([1, 0, 3, -1, 2, 0, 0, 1, n, 3, 2])
+    y = _check(base, x, a, b, who, seq, scale)
+    for s in range(len(who)):
+        r0, r1 = seq[s], seq[s + 1]
+        if r1 > r0:
+            one = bf.lora(base[r0:r1].clone(), x[r0:r1].clone(), a, b, _i32(who[s:s + 1]), seq_offsets=_i32([0, r1 - r0]),
+                          scale=scale)
+            assert torch.equal(one, y[r0:r1]), s
+
+
+def test_many_rows_of_one_request():
+    base, x, a, b, scale = _inputs(5000, 2, 16, 64, 48, BF16, BF16)
+    _check(base, x, a, b, np.array([1]), [0, 5000], scale)
+    _check(base, x, a, b, np.array([7]), [0, 5000], scale)
+    _check(base, x, a, b, np.array([0, 1]), [4999, 5000, 5000], scale)
