@@ -726,6 +726,7 @@ def combine(x, rows, pair_pos, w, shared=None, y=None, stream=None):
 # the call is done with it.
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -749,8 +750,10 @@ def _on_stream(fn):
     device is refused."""
     def run(what, stream, tensors, *args):
         dev = _same_device(what, tensors)
-        if stream is None and dev.index == torch.cuda.current_device():
-            return fn(dev, _raw_stream(dev.index), *args)
+        if stream is None:
+            at = dev.index
+            if at == _get_device():
+                return fn(dev, _raw_stream(at), *args)
         with torch.cuda.device(dev):
             s = torch.cuda.current_stream() if stream is None else stream
             if s.device != dev:
@@ -760,12 +763,14 @@ def _on_stream(fn):
     return run
 
 
+_FLOAT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
 def _float_dtype(dtype, name):
-    if dtype == torch.float32:
-        return DTYPE_F32
-    if dtype == torch.bfloat16:
-        return DTYPE_BF16
-    raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    code = _FLOAT_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return code
 
 
 def _addr(t):
@@ -1144,11 +1149,16 @@ def route_backward(logits, idx, counts=None, n_tokens=None, g_balance=None, g_z=
 
 def _tensors(checks):
     """Checks (tensor or None, shape, type, name): all shapes, then places and types."""
+    for t, shape, dtype, _ in checks:
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+            break
+    else:
+        return
     for t, shape, _, name in checks:
-        if t is not None and t.shape != shape:
+        if t is not None:
             _shape(t, shape, name)
     for t, _, dtype, name in checks:
-        if t is not None and not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        if t is not None:
             _dev(t, dtype, name)
 
 
@@ -1166,11 +1176,11 @@ def dispatch_workspace_bytes(T: int, k: int, E: int) -> int:
 @_on_stream
 def _dispatch(dev, stream, x, dtype, T, d, idx, k, E, rows, offsets, pair_pos, ws):
     if rows is None:
-        rows = torch.empty((T * k, d), dtype=x.dtype, device=dev)
+        rows = x.new_empty((T * k, d))
     if offsets is None:
-        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        offsets = idx.new_empty((E + 1,))
     if pair_pos is None:
-        pair_pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+        pair_pos = torch.empty_like(idx)
     wp, wn, keep = _scratch(lib().moe_dispatch_workspace_bytes(T, k, E), ws, dev)
     _check(lib().moe_dispatch(x.data_ptr(), dtype, T, d, idx.data_ptr(), k, E, rows.data_ptr(),
                               offsets.data_ptr(), pair_pos.data_ptr(), wp, wn, stream), "moe_dispatch")
@@ -1238,10 +1248,10 @@ def dispatch_backward(drows, pair_pos, dx=None, dtype=None, stream=None):
 
 
 @_on_stream
-def _combine_backward(dev, stream, dy, dy_dtype, rows, dtype, rows_dtype, R, T, d, k, pair_pos, w, drows, dw,
-                      need_rows, need_w):
+def _combine_backward(dev, stream, dy, dy_dtype, rows, rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows,
+                      need_w):
     if drows is None and need_rows:
-        drows = torch.empty((R, d), dtype=dtype, device=dev)
+        drows = torch.empty_like(rows)
     if dw is None and need_w:
         dw = torch.empty((T, k), dtype=torch.float32, device=dev)
     _check(lib().moe_combine_backward(dy.data_ptr(), dy_dtype, _addr(rows), rows_dtype, R, T, d, k,
@@ -1280,7 +1290,7 @@ def combine_backward(dy, rows, pair_pos, w=None, drows=None, dw=None, need_rows=
               (w, (T, k), torch.float32, "w"), (dw, (T, k), torch.float32, "dw"), (dy, (T, d), dy.dtype, "dy"),
               (pair_pos, (T, k), torch.int32, "pair_pos")))
     return _combine_backward("combine_backward", stream, (dy, rows, pair_pos, w, drows, dw), dy, dy_dtype, rows,
-                             like.dtype, rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows, need_w)
+                             rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows, need_w)
 
 
 def lora_workspace_bytes(T: int, rank: int, n_seq: int) -> int:
@@ -1336,9 +1346,9 @@ def verify_drafts_workspace_bytes(B: int, V: int) -> int:
 @_on_stream
 def _verify(dev, stream, p, q, dtype, B, n, V, draft, n_draft, u_accept, u_sample, tokens, n_accepted, ws):
     if tokens is None:
-        tokens = torch.empty((B, n + 1), dtype=torch.int32, device=dev)
+        tokens = draft.new_empty((B, n + 1))
     if n_accepted is None:
-        n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        n_accepted = draft.new_empty((B,))
     wp, wn, keep = _scratch(lib().moe_verify_drafts_workspace_bytes(B, V), ws, dev)
     _check(lib().moe_verify_drafts(p.data_ptr(), _addr(q), dtype, B, n, V, draft.data_ptr(), _addr(n_draft),
                                    u_accept.data_ptr(), u_sample.data_ptr(), tokens.data_ptr(),

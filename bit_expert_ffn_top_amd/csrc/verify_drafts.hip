@@ -12,6 +12,7 @@
 // nothing be left of p, p itself is drawn from: its sums are formed beside r's.
 #include "moe_internal.h"
 #include "row_device.h"
+#include "scan_device.h"
 
 namespace bitffn {
 namespace {
@@ -20,7 +21,6 @@ constexpr int kLane = 16;               // values of a lane
 constexpr int kChunk = 64 * kLane;
 constexpr int kShortWaves = 16;         // chunks of a row that one workgroup takes
 constexpr int kSumWaves = 4;            // chunks per workgroup of the first launch
-constexpr int kPickThreads = 256;
 
 struct VerifyArgs {
   const void* p;
@@ -133,11 +133,8 @@ struct ChunkValues {
   }
 };
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
-}
+// The sum over the wavefront, the same for all lanes.
+__device__ __forceinline__ double wave_sum(double v) { return lane_value(wave_scan_add(v), 63); }
 
 // (sum of r, sum of p's own values) of a wavefront's chunk, in every lane.
 template <typename PT>
@@ -160,36 +157,31 @@ __device__ __forceinline__ void chunk_sums(const ChunkValues<PT>& c, const Rest<
 template <typename PT>
 __device__ __forceinline__ int pick_in_chunk(const ChunkValues<PT>& c, const Rest<PT>& r,
                                              double before, double want) {
-  const int lane = threadIdx.x & 63;
+  constexpr int G = kLane / 4;
+  double s[G][4], scan[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[g][j] = sum += c.left(r, g, j);
+    scan[g] = wave_scan_add(sum);
+  }
   int last = -1;
 #pragma unroll
-  for (int g = 0; g < kLane / 4; ++g) {
-    double s[4], sum = 0.0;
-    int mine = -1;
+  for (int g = 0; g < G; ++g) {
+    const double lower = before + lane_before(scan[g]);
+    int at = -1, mine = -1;   // this lane's first value that passes the border; its last above 0
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const double v = c.left(r, g, j);
-      sum += v;
-      s[j] = sum;
-      if (v > 0.0) mine = c.v0 + 256 * g + j;
+    for (int j = 3; j >= 0; --j) {
+      if (!(c.left(r, g, j) > 0.0)) continue;
+      if (lower + s[g][j] > want) at = c.v0 + 256 * g + j;
+      mine = max(mine, c.v0 + 256 * g + j);
     }
-    double scan = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double up = __shfl_up(scan, off);
-      if (lane >= off) scan += up;
-    }
-    double lower = __shfl_up(scan, 1);
-    if (lane == 0) lower = 0.0;
-    int at = -1;   // first value of this lane that passes the border
-#pragma unroll
-    for (int j = 3; j >= 0; --j)
-      if (c.left(r, g, j) > 0.0 && before + (lower + s[j]) > want) at = c.v0 + 256 * g + j;
     const uint64_t hit = __ballot(at >= 0);
-    if (hit) return __shfl(at, __builtin_ctzll(hit));
+    if (hit) return lane_value(at, __builtin_ctzll(hit));
     const uint64_t some = __ballot(mine >= 0);
-    if (some) last = __shfl(mine, 63 - __builtin_clzll(some));
-    before += __shfl(scan, 63);
+    if (some) last = lane_value(mine, 63 - __builtin_clzll(some));
+    before += lane_value(scan[g], 63);
   }
   return last;
 }
@@ -275,90 +267,72 @@ __global__ __launch_bounds__(64 * kSumWaves) void verify_sums_kernel(VerifyArgs 
   if (chunk == 0) put_accepted(a, b, m, x);
 }
 
-// Sums over the threads before this one (fixed order), and the total.
-__device__ __forceinline__ double block_before(double mine, double* s_wave, double& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double scan = mine;
+// The chunk whose sums pass the border, or else the last that adds anything (-1:
+// none does), and the sum before it.  Each lane owns a run of consecutive chunks,
+// four of them in registers.
+__device__ __forceinline__ int find_chunk(const double* sums, int chunks, float u, double& before,
+                                          double& want) {
+  constexpr int kHeld = 4;
+  const int lane = threadIdx.x & 63;
+  const int per = (chunks + 63) / 64;
+  const int c0 = min(chunks, lane * per), c1 = min(chunks, c0 + per);
+  double held[kHeld], mine = 0.0;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double up = __shfl_up(scan, off);
-    if (lane >= off) scan += up;
-  }
-  if (lane == 63) s_wave[wave] = scan;
-  double lower = __shfl_up(scan, 1);
-  if (lane == 0) lower = 0.0;
-  __syncthreads();
-  double before = 0.0;
-  total = 0.0;
-  for (int w = 0; w < kPickThreads / 64; ++w) {
-    if (w == wave) before = total;
-    total += s_wave[w];
-  }
-  return before + lower;
-}
-
-template <typename PT>
-__global__ __launch_bounds__(kPickThreads) void verify_pick_kernel(VerifyArgs a) {
-  __shared__ double s_wave[2][kPickThreads / 64];
-  __shared__ int s_first, s_last;
-  __shared__ double s_first_before, s_last_before;
-  const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x;
-  const int given = drafts_given(a, b);
-  const int m = a.n_accepted[b];
-  const float u = a.u_sample[b];
-  const int x = m < given ? a.draft[b * a.n + m] : -1;
-  Rest<PT> r = rest_of<PT>(a, b, m, m >= given, x);
-  // each thread owns a run of consecutive chunks
-  const int per = (a.chunks + kPickThreads - 1) / kPickThreads;
-  const int c0 = min(a.chunks, tid * per), c1 = min(a.chunks, c0 + per);
-  if (tid == 0) {
-    s_first = 1 << 30;
-    s_last = -1;
-  }
-  const double* sums = a.sums + b * a.chunks;
-  double mine = 0.0, total;
-  for (int c = c0; c < c1; ++c) mine += sums[c];
-  double before = block_before(mine, s_wave[0], total);
-  if (!(total > 0.0)) {   // uniform
-    r.q = nullptr;
-    r.gone = -1;
-    sums += static_cast<int64_t>(a.B) * a.chunks;
-    mine = 0.0;
-    for (int c = c0; c < c1; ++c) mine += sums[c];
-    before = block_before(mine, s_wave[1], total);
-  }
-  const double want = border(u, total);
-  int first = 1 << 30, last = -1;
-  double first_before = 0.0, last_before = 0.0, sum = before;
-  for (int c = c0; c < c1; ++c) {
-    const double add = sums[c];
+  for (int i = 0; i < kHeld; ++i) held[i] = c0 + i < c1 ? sums[c0 + i] : 0.0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) mine += held[i];
+  for (int c = c0 + kHeld; c < c1; ++c) mine += sums[c];
+  const double scan = wave_scan_add(mine);
+  const double total = lane_value(scan, 63);
+  want = border(u, total);
+  int first = -1, last = -1;
+  double first_before = 0.0, last_before = 0.0, sum = lane_before(scan);
+  const auto look = [&](int c, double add) {
     if (add > 0.0) {
       last = c;
       last_before = sum;
-      if (first == 1 << 30 && sum + add > want) {
+      if (first < 0 && sum + add > want) {
         first = c;
         first_before = sum;
       }
     }
     sum += add;
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (c0 + i < c1) look(c0 + i, held[i]);
+  for (int c = c0 + kHeld; c < c1; ++c) look(c, sums[c]);
+  const uint64_t hit = __ballot(first >= 0), some = __ballot(last >= 0);
+  if (hit) {
+    const int who = __builtin_ctzll(hit);
+    before = lane_value(first_before, who);
+    return lane_value(first, who);
   }
-  if (first < 1 << 30) atomicMin(&s_first, first);
-  if (last >= 0) atomicMax(&s_last, last);
-  __syncthreads();
-  if (first < 1 << 30 && first == s_first) s_first_before = first_before;
-  if (last >= 0 && last == s_last) s_last_before = last_before;
-  __syncthreads();
-  if (tid >= 64) return;
-  const bool found = s_first < 1 << 30;
-  const int at = found ? s_first : s_last;
+  if (!some) return -1;
+  const int who = 63 - __builtin_clzll(some);
+  before = lane_value(last_before, who);
+  return lane_value(last, who);
+}
+
+// One wavefront per request.
+template <typename PT>
+__global__ __launch_bounds__(64) void verify_pick_kernel(VerifyArgs a) {
+  const int64_t b = blockIdx.x;
+  const int given = drafts_given(a, b);
+  const int m = __builtin_amdgcn_readfirstlane(a.n_accepted[b]);
+  const float u = a.u_sample[b];
+  double before = 0.0, want;
+  int at = find_chunk(a.sums + b * a.chunks, a.chunks, u, before, want);
+  const bool all = m >= given || at < 0;
+  if (at < 0) at = find_chunk(a.sums + (a.B + b) * a.chunks, a.chunks, u, before, want);
   int pick = -1;
   if (at >= 0) {
+    const Rest<PT> r = rest_of<PT>(a, b, m, all, all || a.q ? -1 : a.draft[b * a.n + m]);
     ChunkValues<PT> c;
     c.load(r, at, a.V);
-    pick = pick_in_chunk(c, r, found ? s_first_before : s_last_before, want);
+    pick = pick_in_chunk(c, r, before, want);
   }
-  if (tid == 0) a.tokens[b * (a.n + 1) + m] = pick;
+  if (threadIdx.x == 0) a.tokens[b * (a.n + 1) + m] = pick;
 }
 
 template <typename PT>
@@ -372,7 +346,7 @@ hipError_t launch_as(VerifyArgs a, void* ws, hipStream_t s) {
   for (; a.b0 < a.B; a.b0 += kMost)
     verify_sums_kernel<PT><<<dim3((a.chunks + kSumWaves - 1) / kSumWaves, min(kMost, a.B - a.b0)),
                              64 * kSumWaves, 0, s>>>(a);
-  verify_pick_kernel<PT><<<a.B, kPickThreads, 0, s>>>(a);
+  verify_pick_kernel<PT><<<a.B, 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
