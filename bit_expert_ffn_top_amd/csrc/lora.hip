@@ -43,6 +43,7 @@ struct LoraArgs {
   void* y;
   int T, d_in, d_out, n_adapters, rank, n_seq;
   int slice;     // output columns of a workgroup, a multiple of kGroup
+  int together;  // rows of one adapter share a workgroup (a row for every request)
   int4* tiles;   // in the workspace (many rows)
   nu4* h;
   int n_tiles;
@@ -156,14 +157,51 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& g, int tile, int rows,
                        : search_tile<8>(g, tile, rows, row0, row1, request);
 }
 
+// The rows of a tile: row0 and those after it, or (LISTED) those that a list in
+// LDS has, counted from row0.
+template <bool LISTED>
+struct Rows {
+  int row0, n;
+  const int* list;
+  __device__ __forceinline__ int after(int i) const { return LISTED ? list[i] : i; }   // i < n
+  // The same with the last one in place of those that are missing.
+  __device__ __forceinline__ int held(int i) const { return after(min(i, n - 1)); }
+  __device__ __forceinline__ Rows from(int i) const { return {row0 + i, n - i, nullptr}; }   // not LISTED
+};
+
+// Where every row is a request: row t and the next rows with its adapter, 16 in
+// all, if a whole number of sixteens of them comes before t; else false, they are
+// other workgroups'.  A row without an adapter is alone.
+__device__ __forceinline__ bool rows_of_adapter(const LoraArgs& g, int t, int m, int* list, int& n) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int i = 0; i < t; i += 64) {
+    const int s = i + lane;
+    before += __popcll(__ballot(s < t && g.adapter[min(s, g.T - 1)] == m));
+  }
+  if (before % 16) return false;
+  n = 1;
+  if (lane == 0) list[0] = 0;
+  for (int i = t + 1; i < g.T && n < 16; i += 64) {
+    const int s = i + lane;
+    const bool same = s < g.T && g.adapter[min(s, g.T - 1)] == m;
+    const uint64_t all = __ballot(same);
+    const int at = n + __popcll(all & ((uint64_t{1} << lane) - 1));
+    if (same && at < 16) list[at] = s - t;
+    n += __popcll(all);
+  }
+  n = min(n, 16);
+  return true;
+}
+
 // Rows of a tile without an adapter: columns [n0, n1) of base.
 template <typename YT>
-__device__ __forceinline__ void copy_base(const LoraArgs& g, int row0, int row1, int n0, int n1) {
+__device__ __forceinline__ void copy_base(const LoraArgs& g, int row0, int rows, int n0, int n1) {
   const YT* base = static_cast<const YT*>(g.base);
   YT* y = static_cast<YT*>(g.y);
   if (y == base) return;
   const int parts = (n1 - n0) / 8;
-  for (int i = threadIdx.x; i < (row1 - row0) * parts; i += blockDim.x) {
+  for (int i = threadIdx.x; i < rows * parts; i += blockDim.x) {
     const int t = i / parts;
     const int64_t at = static_cast<int64_t>(row0 + t) * g.d_out + n0 + 8 * (i - t * parts);
     RowPart<YT, 8> v;
@@ -179,10 +217,11 @@ constexpr int kUnitBytes = 2048;
 
 struct UnitRows {
   uint32_t at[2];   // the lane's rows and chunk, bytes from the matrix's start
-  __device__ __forceinline__ void set(int row, int last, uint32_t row_bytes) {
+  template <bool LISTED>
+  __device__ __forceinline__ void set(const Rows<LISTED>& rows, int row, uint32_t row_bytes) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) at[h] = min(row + (lane >> 3) + 8 * h, last) * row_bytes + 16 * (lane & 7);
+    for (int h = 0; h < 2; ++h) at[h] = rows.held(row + (lane >> 3) + 8 * h) * row_bytes + 16 * (lane & 7);
   }
 };
 
@@ -219,20 +258,20 @@ struct Down {
 
 // A wavefront's share of h = A x for 16 NT rows and the ranks from 64 pass on,
 // left in its part of LDS: [row][rank].
-template <typename XT, int MT, int NT>
-__device__ __forceinline__ void down_product(const LoraArgs& g, int m, int row0, int row1, int pass,
+template <typename XT, int MT, int NT, bool LISTED>
+__device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Rows<LISTED>& rows, int pass,
                                              char* lds) {
   using D = Down<XT, MT, NT>;
   constexpr int MP = D::kRanks, XU = D::kUnits, XP = XParts<XT>::kParts, U = D::kAhead;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, quad = lane >> 4;
   const char* a = reinterpret_cast<const char*>(g.a + static_cast<int64_t>(m) * g.rank * g.d_in);
-  const char* x = reinterpret_cast<const char*>(static_cast<const XT*>(g.x) + static_cast<int64_t>(row0) * g.d_in);
+  const char* x = reinterpret_cast<const char*>(static_cast<const XT*>(g.x) + static_cast<int64_t>(rows.row0) * g.d_in);
   UnitRows ar[MP], xr[NT];
 #pragma unroll
-  for (int i = 0; i < MP; ++i) ar[i].set(64 * pass + 16 * i, g.rank - 1, g.d_in * 2);
+  for (int i = 0; i < MP; ++i) ar[i].set(Rows<false>{0, g.rank, nullptr}, 64 * pass + 16 * i, g.d_in * 2);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) xr[j].set(16 * j, row1 - row0 - 1, g.d_in * sizeof(XT));
+  for (int j = 0; j < NT; ++j) xr[j].set(rows, 16 * j, g.d_in * sizeof(XT));
   nf4 acc[MP][NT];
 #pragma unroll
   for (int i = 0; i < MP; ++i)
@@ -392,26 +431,28 @@ template <typename YT, int COLS>
 struct YRows {
   static constexpr int kPerRow = COLS / 8, kRows = 64 / kPerRow, kLoads = 16 / kRows;
   RowPart<YT, 8> v[kLoads];
-  __device__ __forceinline__ void load(const LoraArgs& g, int row0, int row1, int c) {
+  template <bool LISTED>
+  __device__ __forceinline__ void load(const LoraArgs& g, const Rows<LISTED>& rows, int c) {
     const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int t = row0 + n * kRows + lane / kPerRow;
-      if (t < row1 && col < g.d_out)
-        v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(t) * g.d_out + col);
+      const int t = n * kRows + lane / kPerRow;
+      if (t < rows.n && col < g.d_out)
+        v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out + col);
     }
   }
-  __device__ __forceinline__ void copy(const LoraArgs& g, int row0, int row1, int c) const {
+  __device__ __forceinline__ void copy(const LoraArgs& g, const Rows<false>& rows, int c) const {
     const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int t = row0 + n * kRows + lane / kPerRow;
-      if (t < row1 && col < g.d_out)
-        v[n].template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(t) * g.d_out + col);
+      const int t = n * kRows + lane / kPerRow;
+      if (t < rows.n && col < g.d_out)
+        v[n].template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(rows.row0 + t) * g.d_out + col);
     }
   }
   // y = base + the results in LDS, [row][COLS + 4]
-  __device__ __forceinline__ void store(const LoraArgs& g, int row0, int row1, int c, const float* lds) {
+  template <bool LISTED>
+  __device__ __forceinline__ void store(const LoraArgs& g, const Rows<LISTED>& rows, int c, const float* lds) {
     const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
@@ -421,10 +462,11 @@ struct YRows {
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = v[n].get(e) + (e < 4 ? lo[e % 4] : hi[e % 4]);
-      if (row0 + t < row1 && col < g.d_out) {
+      if (t < rows.n && col < g.d_out) {
         RowPart<YT, 8> out;
         out.set(f);
-        out.template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(row0 + t) * g.d_out + col);
+        out.template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out +
+                                 col);
       }
     }
   }
@@ -459,15 +501,23 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   static_assert(kWaveBytes % 16 == 0, "");
   __shared__ __align__(16) char s_wave[kWaves * kWaveBytes];
   __shared__ nu4 s_h[HP][RS][64];
+  __shared__ int s_list[kWaves][16];   // each wavefront's own: no barrier
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int row0, row1, request;
   if (!find_tile(g, blockIdx.x, 16, row0, row1, request)) return;
   const int m = adapter_of(g, request);
   const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
   if (m < 0 || m >= g.n_adapters) {
-    copy_base<YT>(g, row0, row1, n0, n1);
+    copy_base<YT>(g, row0, row1 - row0, n0, n1);
     return;
   }
+  Rows<true> rows{row0, row1 - row0, s_list[wave]};
+  if (g.together) {
+    if (!rows_of_adapter(g, row0, m, s_list[wave], rows.n)) return;
+  } else if (lane < 16) {
+    s_list[wave][lane] = lane;
+  }
+  wave_order();
   const float scale = g.scale ? g.scale[m] : 1.0f;
   char* mine = s_wave + wave * kWaveBytes;
   const uint16_t* b = g.b + static_cast<int64_t>(m) * g.d_out * g.rank;
@@ -478,10 +528,10 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   YRows<YT, kCols> yr;
   if (k0 < k1) {
     bl.load(g, b, n0 + k0 * kCols, lane);
-    yr.load(g, row0, row1, n0 + k0 * kCols);
+    yr.load(g, rows, n0 + k0 * kCols);
   }
   for (int pass = 0; pass < MT / D::kRanks; ++pass) {
-    down_product<XT, MT, 1>(g, m, row0, row1, pass, mine);
+    down_product<XT, MT, 1>(g, m, rows, pass, mine);
     __syncthreads();
     constexpr int kSteps = (D::kRanks + 1) / 2;
     if (tid < 64 * kSteps) {
@@ -513,8 +563,8 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
       up_product<RS, HP, kCols>(bv, hv, res, tile);
     }
     wave_order();
-    yr.store(g, row0, row1, c, res);
-    if (k + 1 < k1) yr.load(g, row0, row1, c + kCols);
+    yr.store(g, rows, c, res);
+    if (k + 1 < k1) yr.load(g, rows, c + kCols);
   }
 }
 
@@ -540,7 +590,7 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
   const float scale = g.scale ? g.scale[m] : 1.0f;
   for (int pass = 0; pass < MT / D::kRanks; ++pass) {
     if (pass) __syncthreads();   // the sums have been read
-    down_product<XT, MT, kTiles16>(g, m, row0, row1, pass, s_wave + wave * D::kBytes);
+    down_product<XT, MT, kTiles16>(g, m, Rows<false>{row0, row1 - row0, nullptr}, pass, s_wave + wave * D::kBytes);
     __syncthreads();
     constexpr int kSteps = (D::kRanks + 1) / 2;
     if (wave < kSteps * kTiles16) {
@@ -567,7 +617,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tile = blockIdx.x * kUpWaves + wave, c = blockIdx.y * kGroup;
   const int4 mine = tile < g.n_tiles ? g.tiles[tile] : make_int4(0, 0, -1, 0);
-  const int row0 = mine.x, row1 = mine.y, m = mine.z;
+  const Rows<false> rows{mine.x, mine.y - mine.x, nullptr};
+  const int m = mine.z;
   int all[kUpWaves];   // the tiles' adapters
 #pragma unroll
   for (int w = 0; w < kUpWaves; ++w) {
@@ -576,7 +627,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   }
   YRows<YT, kGroup> yr[kTiles16];
 #pragma unroll
-  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, row0 + 16 * j, row1, c);
+  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, rows.from(16 * j), c);
   nu4 hv[kTiles16][HP][RS];
   if (m >= 0) {
     const nu4* h = g.h + static_cast<int64_t>(tile) * kTiles16 * (HP * RS * 64) + lane;
@@ -588,7 +639,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
         for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
   } else if (g.y != g.base) {   // no adapter
 #pragma unroll
-    for (int j = 0; j < kTiles16; ++j) yr[j].copy(g, row0 + 16 * j, row1, c);
+    for (int j = 0; j < kTiles16; ++j) yr[j].copy(g, rows.from(16 * j), c);
   }
   bool first = true;
   for (int w = 0; w < kUpWaves; ++w) {
@@ -615,7 +666,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
         up_product<RS, HP, kGroup>(bv, hv[j], s_res[wave], t);
       }
       wave_order();
-      yr[j].store(g, row0 + 16 * j, row1, c, s_res[wave]);
+      yr[j].store(g, rows.from(16 * j), c, s_res[wave]);
       wave_order();
     }
   }
@@ -625,6 +676,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
 int most_tiles(int64_t T, int n_seq, int rows) {
   return static_cast<int>((T + (rows - 1) * min(static_cast<int64_t>(n_seq), T)) / rows);
 }
+
+// Where every row is a request: from how many rows on those of one adapter share a
+// workgroup, and up to how many (each looks through all adapters).
+constexpr int kTogether = 1024, kMostTogether = 4096;
 
 template <typename XT, typename YT, int MT>
 hipError_t launch_rank(LoraArgs g, hipStream_t s) {
@@ -636,7 +691,10 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
-  const int slices = static_cast<int>(max(int64_t{1}, min(int64_t{groups}, 192 / tiles)));
+  g.together = !g.seq && tiles >= kTogether && tiles <= kMostTogether;
+  // those that are left after rows have joined others, if these are spread evenly
+  const int64_t left = g.together ? min(tiles, tiles / 16 + g.n_adapters) : tiles;
+  const int slices = static_cast<int>(max(int64_t{1}, min(int64_t{groups}, 256 / left)));
   g.slice = (groups + slices - 1) / slices * kGroup;
   const dim3 grid(static_cast<unsigned>(tiles), (g.d_out + g.slice - 1) / g.slice);
   lora_kernel<XT, YT, MT><<<grid, kThreads, 0, s>>>(g);
@@ -667,7 +725,7 @@ hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, 
                        const int32_t* seq, int n_seq, const int32_t* adapter, const float* scale,
                        void* y, int y_dtype, void* ws, hipStream_t s) {
   LoraArgs g{base, x, a, b, seq, adapter, scale, y, static_cast<int>(T),
-             d_in, d_out, n_adapters, rank, n_seq, 0, nullptr, nullptr, 0};
+             d_in, d_out, n_adapters, rank, n_seq, 0, 0, nullptr, nullptr, 0};
   if (lora_workspace_bytes(T, rank, seq ? n_seq : 0) > 0) {
     g.n_tiles = most_tiles(T, n_seq, kTileRows);
     g.tiles = static_cast<int4*>(ws);

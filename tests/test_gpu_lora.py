@@ -242,3 +242,17 @@ def test_many_rows_of_one_request():
     _check(base, x, a, b, np.array([1]), [0, 5000], scale)
     _check(base, x, a, b, np.array([7]), [0, 5000], scale)
     _check(base, x, a, b, np.array([0, 1]), [4999, 5000, 5000], scale)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("T,n", [(1024, 1), (1024, 40), (1500, 3), (4096, 200), (4097, 3)])
+def test_many_single_rows(T, n, types):
+    """From 1,024 rows on, rows of one adapter share a workgroup, wherever they
+    lie; rows without one among them; and the bits that bounds between all rows
+    give, which take other launches."""
+    bf = _bf()
+    base, x, a, b, scale = _inputs(T, n, 24, 96, 48, *types)
+    who = np.random.default_rng(T + n).integers(-1, n + 1, T)
+    who[:40] = np.where(np.arange(40) % 3, 0, -1)
+    y = _check(base, x, a, b, who, None, scale)
+    assert torch.equal(bf.lora(base, x, a, b, _i32(who), seq_offsets=_i32(np.arange(T + 1)), scale=scale), y)
