@@ -1,5 +1,7 @@
 // Tokens to the experts and back: the pairs' rows in group order, the weighted
 // sum of them in the tokens' order, and the gradients of both.
+#include <algorithm>
+
 #include "moe_internal.h"
 #include "row_device.h"
 
@@ -312,10 +314,18 @@ hipError_t combine_rows_as(const void* rows, int64_t R, int T, int d, int k,
                            const int32_t* pair_pos, const float* w, const void* base,
                            int base_dtype, void* y, hipStream_t s) {
   constexpr int N = part_of<RT, YT>();
-  const int64_t blocks = (static_cast<int64_t>(T) * ((d + N - 1) / N) + kThreads - 1) / kThreads;
-  combine_rows_kernel<RT, YT, N><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const RT*>(rows), static_cast<int>(R), T, d, k, pair_pos, w, base, base_dtype,
-      static_cast<YT*>(y));
+  const int per = (d + N - 1) / N;
+  // a launch has fewer than 2^32 threads (std::min: min alone may be that of 32 bits)
+  const int most = static_cast<int>(std::min(int64_t{T}, (int64_t{1} << 31) / per));
+  const int64_t base_bytes = static_cast<int64_t>(d) * (base_dtype == MOE_DTYPE_F32 ? 4 : 2);
+  for (int t = 0; t < T; t += most) {
+    const int n = min(most, T - t);
+    const int64_t blocks = (static_cast<int64_t>(n) * per + kThreads - 1) / kThreads;
+    combine_rows_kernel<RT, YT, N><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
+        static_cast<const RT*>(rows), static_cast<int>(R), n, d, k, pair_pos + int64_t{t} * k,
+        w ? w + int64_t{t} * k : nullptr, base ? static_cast<const char*>(base) + t * base_bytes : nullptr,
+        base_dtype, static_cast<YT*>(y) + int64_t{t} * d);
+  }
   return hipGetLastError();
 }
 

@@ -19,6 +19,8 @@
 // smallest values), h as two where the results are bfloat16 (off by 2^-16 of it,
 // where they round by 2^-8) and three where they are fp32.  A row has the same
 // bits whatever other rows there are.
+#include <algorithm>
+
 #include "moe_internal.h"
 #include "row_device.h"
 #include "scan_device.h"
@@ -575,6 +577,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
 constexpr int kTileRows = 32;
 constexpr int kTiles16 = kTileRows / 16;
 constexpr int kUpWaves = 2;    // tiles of a workgroup
+constexpr int kUpGridRows = 32768;
 
 template <typename XT, typename YT, int MT>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
@@ -615,14 +618,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   __shared__ __align__(16) char s_b[B::kBytes];
   __shared__ __align__(16) float s_res[kUpWaves][16 * (kGroup + 4)];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tile = blockIdx.x * kUpWaves + wave, c = blockIdx.y * kGroup;
+  // neighbouring workgroups take neighbouring columns of the same rows
+  const int c = blockIdx.x * kGroup, tile0 = (blockIdx.z * kUpGridRows + blockIdx.y) * kUpWaves;
+  const int tile = tile0 + wave;
   const int4 mine = tile < g.n_tiles ? g.tiles[tile] : make_int4(0, 0, -1, 0);
   const Rows<false> rows{mine.x, mine.y - mine.x, nullptr};
   const int m = mine.z;
   int all[kUpWaves];   // the tiles' adapters
 #pragma unroll
   for (int w = 0; w < kUpWaves; ++w) {
-    const int t = blockIdx.x * kUpWaves + w;
+    const int t = tile0 + w;
     all[w] = t < g.n_tiles ? g.tiles[t].z : -1;
   }
   YRows<YT, kGroup> yr[kTiles16];
@@ -674,7 +679,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
 
 // ceil(n / rows) summed over the requests is at most this.
 int most_tiles(int64_t T, int n_seq, int rows) {
-  return static_cast<int>((T + (rows - 1) * min(static_cast<int64_t>(n_seq), T)) / rows);
+  return static_cast<int>((T + (rows - 1) * std::min(static_cast<int64_t>(n_seq), T)) / rows);
 }
 
 // Where every row is a request: from how many rows on those of one adapter share a
@@ -686,15 +691,16 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
   const int groups = (g.d_out + kGroup - 1) / kGroup;
   if (g.h) {
     lora_down_kernel<XT, YT, MT><<<g.n_tiles, kThreads, 0, s>>>(g);
-    const dim3 grid((g.n_tiles + kUpWaves - 1) / kUpWaves, groups);
+    const int rows = (g.n_tiles + kUpWaves - 1) / kUpWaves;
+    const dim3 grid(groups, min(rows, kUpGridRows), (rows + kUpGridRows - 1) / kUpGridRows);
     lora_up_kernel<YT, (MT + 1) / 2><<<grid, 64 * kUpWaves, 0, s>>>(g);
     return hipGetLastError();
   }
   const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
   g.together = !g.seq && tiles >= kTogether && tiles <= kMostTogether;
   // those that are left after rows have joined others, if these are spread evenly
-  const int64_t left = g.together ? min(tiles, tiles / 16 + g.n_adapters) : tiles;
-  const int slices = static_cast<int>(max(int64_t{1}, min(int64_t{groups}, 256 / left)));
+  const int64_t left = g.together ? std::min(tiles, tiles / 16 + g.n_adapters) : tiles;
+  const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / left)));
   g.slice = (groups + slices - 1) / slices * kGroup;
   const dim3 grid(static_cast<unsigned>(tiles), (g.d_out + g.slice - 1) / g.slice);
   lora_kernel<XT, YT, MT><<<grid, kThreads, 0, s>>>(g);

@@ -702,7 +702,8 @@ int moe_combine_rows(const void* rows, int rows_dtype, int64_t R, int T, int d, 
  * fp32 or bf16): for every pair with 0 <= pair_pos[t*k+i] < R
  *   drows[pair_pos[t*k+i]] = w[t*k+i] * dy[t]
  *   dw[t*k+i]              = sum_j dy[t][j] * rows[pair_pos[t*k+i]][j]
- * and dw = 0 for the others.  rows and drows have rows_dtype; dw fp32 [T][k],
+ * and dw = 0 for the others (the pairs' rows are distinct, as moe_dispatch makes
+ * them).  rows and drows have rows_dtype; dw fp32 [T][k],
  * summed in fp32 in a fixed order; it is what moe_route_backward takes.  Rows of
  * drows that are no pair's are left as they were.  drows or dw (with rows) may be
  * NULL, w NULL counts as ones.  base's gradient is dy itself.  Limits as above. */

@@ -271,3 +271,37 @@ def test_repeated_calls_give_the_same_bits():
         if first is not None:
             assert all(torch.equal(a, b) for a, b in zip(out, first))
         first = out
+
+
+def test_no_rows():
+    """Experts without any row: combine gives base, its gradient zeros."""
+    bf = _bf()
+    dev = need_gpu()
+    pos, base, w = _dev(np.full((5, 3), -1, np.int32)), _randn(1, (5, 64), BF16), _randn(2, (5, 3), F32)
+    rows = torch.empty((0, 64), dtype=BF16, device=dev)
+    assert torch.equal(bf.combine_rows(rows, pos, w, base=base), base)
+    assert torch.equal(bf.dispatch_backward(rows, pos, dtype=F32), torch.zeros((5, 64), device=dev))
+    drows, dw = bf.combine_backward(base, rows, pos, w)
+    assert drows.shape == (0, 64) and torch.equal(dw, torch.zeros_like(w))
+    assert bf.combine_backward(base, rows, pos, w, need_w=False)[0].shape == (0, 64)
+    pos0 = torch.empty((0, 3), dtype=torch.int32, device=dev)
+    assert bf.combine_rows(_randn(3, (4, 64), F32), pos0).shape == (0, 64)
+    drows, dw = bf.combine_backward(base[:0], _randn(3, (4, 64), F32), pos0)
+    assert drows.shape == (4, 64) and dw.shape == (0, 3)
+
+
+def test_more_threads_than_a_launch_has():
+    """2.2 million tokens of 16,384 columns, 4.5 billion lanes' parts: rows from
+    all over y, both ends and the seam between two launches among them."""
+    bf = _bf()
+    dev = need_gpu()
+    T, d = 2_200_000, 16384
+    assert T * (d // 8) > 2 ** 32
+    rows = _randn(1, (3, d), BF16)
+    w = torch.full((T, 1), 2.0, device=dev)
+    pos = (torch.arange(T, device=dev) % 4).int()[:, None].contiguous()     # 3: no row
+    y = bf.combine_rows(rows, pos, w)
+    want = torch.cat([rows * 2, torch.zeros_like(rows[:1])])
+    seam = 2 ** 31 // (d // 8)
+    at = torch.tensor([0, 1, 2, 3, seam - 1, seam, seam + 1, 2 * seam - 1, 2 * seam, 2 * seam + 1, T - 2, T - 1], device=dev)
+    assert torch.equal(y[at], want[(at % 4)])
