@@ -1162,6 +1162,14 @@ def _tensors(checks):
             _dev(t, dtype, name)
 
 
+def _dims(t, n, name):
+    """t's shape, which must have n dimensions."""
+    shape = t.shape
+    if len(shape) != n:
+        _shape(t, (None,) * n, name)
+    return shape
+
+
 class Dispatch(NamedTuple):
     """What dispatch returns."""
     rows: torch.Tensor        # [T * k, d], x's type
@@ -1193,12 +1201,11 @@ def dispatch(x, idx, n_experts, rows=None, offsets=None, pair_pos=None, ws=None,
     outside [0, n_experts) have none (pair_pos -1), and the rows past offsets[E]
     are left as they were (undefined in rows allocated here)."""
     dtype = _float_dtype(x.dtype, "x")
-    _shape(x, (None, None), "x")
-    T, d = x.shape
-    _shape(idx, (T, None), "idx")
-    k = idx.shape[1]
+    T, d = _dims(x, 2, "x")
+    k = _dims(idx, 2, "idx")[1]
     E = _int32(n_experts, "n_experts")
-    _sizes("x, idx", T, d, k, T * k)
+    if (T | d | T * k) >> 31:
+        _sizes("x, idx", T, d, T * k)
     _tensors(((rows, (T * k, d), x.dtype, "rows"), (offsets, (E + 1,), torch.int32, "offsets"),
               (pair_pos, (T, k), torch.int32, "pair_pos"), (x, (T, d), x.dtype, "x"), (idx, (T, k), torch.int32, "idx")))
     if ws is not None:
@@ -1210,7 +1217,7 @@ def dispatch(x, idx, n_experts, rows=None, offsets=None, pair_pos=None, ws=None,
 @_on_stream
 def _combine_rows(dev, stream, rows, rows_dtype, R, T, d, k, pair_pos, w, base, base_dtype, y, dtype, y_dtype):
     if y is None:
-        y = torch.empty((T, d), dtype=dtype, device=dev)
+        y = rows.new_empty((T, d)) if y_dtype == rows_dtype else torch.empty((T, d), dtype=dtype, device=dev)
     _check(lib().moe_combine_rows(rows.data_ptr(), rows_dtype, R, T, d, k, pair_pos.data_ptr(), _addr(w),
                                   _addr(base), base_dtype, y.data_ptr(), y_dtype, stream), "moe_combine_rows")
     return y
@@ -1222,20 +1229,21 @@ def combine_rows(rows, pair_pos, w=None, base=None, y=None, dtype=None, stream=N
     rows [R, d], base [T, d] (None: zeros) and y, each fp32 or bf16; pair_pos
     int32 [T, k] as dispatch returns it (outside [0, R): no row); w fp32 [T, k]
     (None: ones).  Returns y [T, d] in dtype (None: rows' type); y may be base."""
-    rows_dtype = _float_dtype(rows.dtype, "rows")
-    _shape(rows, (None, None), "rows")
-    R, d = rows.shape
-    _shape(pair_pos, (None, None), "pair_pos")
-    T, k = pair_pos.shape
-    _sizes("rows, pair_pos", R, T, d, k)
-    dtype = rows.dtype if dtype is None else dtype
-    y_dtype = _float_dtype(dtype if y is None else y.dtype, "y")
-    base_dtype = y_dtype
-    if base is not None:
-        base_dtype = _float_dtype(base.dtype, "base")
-    _tensors(((base, (T, d), base.dtype if base is not None else None, "base"), (w, (T, k), torch.float32, "w"),
-              (y, (T, d), y.dtype if y is not None else None, "y"), (rows, (R, d), rows.dtype, "rows"),
-              (pair_pos, (T, k), torch.int32, "pair_pos")))
+    kind = rows.dtype
+    rows_dtype = _float_dtype(kind, "rows")
+    R, d = _dims(rows, 2, "rows")
+    T, k = _dims(pair_pos, 2, "pair_pos")
+    if (R | T | d | k) >> 31:
+        _sizes("rows, pair_pos", R, T, d, k)
+    if y is not None:
+        dtype = y.dtype
+    elif dtype is None:
+        dtype = kind
+    y_dtype = rows_dtype if dtype is kind else _float_dtype(dtype, "y")
+    base_kind = None if base is None else base.dtype
+    base_dtype = y_dtype if base_kind is None or base_kind is dtype else _float_dtype(base_kind, "base")
+    _tensors(((base, (T, d), base_kind, "base"), (w, (T, k), torch.float32, "w"), (y, (T, d), dtype, "y"),
+              (rows, (R, d), kind, "rows"), (pair_pos, (T, k), torch.int32, "pair_pos")))
     return _combine_rows("combine_rows", stream, (rows, pair_pos, w, base, y), rows, rows_dtype, R, T, d, k,
                          pair_pos, w, base, base_dtype, y, dtype, y_dtype)
 
@@ -1279,13 +1287,13 @@ def combine_backward(dy, rows, pair_pos, w=None, drows=None, dw=None, need_rows=
     if (drows is not None and not need_rows) or (dw is not None and not need_w):
         raise ValueError("combine_backward: a buffer given for a gradient that is not needed")
     dy_dtype, rows_dtype = _float_dtype(dy.dtype, "dy"), _float_dtype(like.dtype, "rows")
-    _shape(dy, (None, None), "dy")
-    T, d = dy.shape
-    _shape(like, (None, d), "rows")
-    R = like.shape[0]
-    _shape(pair_pos, (T, None), "pair_pos")
-    k = pair_pos.shape[1]
-    _sizes("rows, pair_pos", R, T, d, k)
+    T, d = _dims(dy, 2, "dy")
+    R, width = _dims(like, 2, "rows")
+    if width != d:
+        _shape(like, (None, d), "rows")
+    k = _dims(pair_pos, 2, "pair_pos")[1]
+    if (R | T | d | k) >> 31:
+        _sizes("rows, pair_pos", R, T, d, k)
     _tensors(((rows, (R, d), like.dtype, "rows"), (drows, (R, d), like.dtype, "drows"),
               (w, (T, k), torch.float32, "w"), (dw, (T, k), torch.float32, "dw"), (dy, (T, d), dy.dtype, "dy"),
               (pair_pos, (T, k), torch.int32, "pair_pos")))
@@ -1319,16 +1327,16 @@ def lora(base, x, a, b, adapter, seq_offsets=None, scale=None, y=None, ws=None, 
     each); scale fp32 [n] (None: ones).  Returns y in base's type; y may be base.
     Rows of no request are left as they were (undefined in a y allocated here)."""
     x_dtype, y_dtype = _float_dtype(x.dtype, "x"), _float_dtype(base.dtype, "base")
-    _shape(x, (None, None), "x")
-    T, d_in = x.shape
-    _shape(base, (T, None), "base")
-    d_out = base.shape[1]
-    _shape(a, (None, None, d_in), "a")
-    n, rank = a.shape[0], a.shape[1]
-    _shape(b, (n, d_out, rank), "b")
-    _shape(adapter, (T if seq_offsets is None else None,), "adapter")
-    S = adapter.shape[0]
-    _sizes("lora", T, d_in, d_out, n, rank, S)
+    T, d_in = _dims(x, 2, "x")
+    d_out = _dims(base, 2, "base")[1]
+    n, rank, width = _dims(a, 3, "a")
+    if width != d_in:
+        _shape(a, (None, None, d_in), "a")
+    S, = _dims(adapter, 1, "adapter")
+    if seq_offsets is None and S != T:
+        _shape(adapter, (T,), "adapter")
+    if (T | d_in | d_out | n | rank | S) >> 31:
+        _sizes("lora", T, d_in, d_out, n, rank, S)
     _tensors(((seq_offsets, (S + 1,), torch.int32, "seq_offsets"), (scale, (n,), torch.float32, "scale"),
               (y, (T, d_out), base.dtype, "y"), (x, (T, d_in), x.dtype, "x"), (base, (T, d_out), base.dtype, "base"),
               (a, (n, rank, d_in), torch.bfloat16, "a"), (b, (n, d_out, rank), torch.bfloat16, "b"),
@@ -1366,13 +1374,14 @@ def verify_drafts(p, q, draft, u_accept, u_sample, n_draft=None, tokens=None, n_
     random numbers in [0, 1).  Returns (tokens int32 [B, n + 1]: the accepted
     drafts, the token drawn after them, then -1; n_accepted int32 [B])."""
     dtype = _float_dtype(p.dtype, "p")
-    _shape(draft, (None, None), "draft")
-    B, n = draft.shape
+    B, n = _dims(draft, 2, "draft")
     if n > MAX_DRAFTS:
         raise ValueError(f"draft: at most {MAX_DRAFTS} drafts expected, got {n}")
-    _shape(p, (B, n + 1, None), "p")
-    V = p.shape[2]
-    _sizes("p", B, V)
+    requests, places, V = _dims(p, 3, "p")
+    if requests != B or places != n + 1:
+        _shape(p, (B, n + 1, None), "p")
+    if (B | V) >> 31:
+        _sizes("p", B, V)
     _tensors(((q, (B, n, V), p.dtype, "q"), (u_accept, (B, n), torch.float32, "u_accept"),
               (u_sample, (B,), torch.float32, "u_sample"), (n_draft, (B,), torch.int32, "n_draft"),
               (tokens, (B, n + 1), torch.int32, "tokens"), (n_accepted, (B,), torch.int32, "n_accepted"),
