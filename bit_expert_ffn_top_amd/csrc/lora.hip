@@ -11,10 +11,14 @@
 // columns; A is small (64 KB at rank 16 and 2048 columns), and a second launch
 // would cost more.  Many rows: two launches, with h in the workspace in the order
 // in which the second one's lanes read it.
-// Operands are read as their rows lie and change lanes in LDS: an operand's layout
-// read directly has 16 bytes of 16 rows in each quarter of a wavefront, and the
-// path to the cache then moves 16 bytes per cycle and CU instead of 64 (8,192
-// rows at rank 64: 45 us where this takes XX).  y leaves the same way.
+// Operands are read as their rows lie and change lanes in LDS: read directly, an
+// operand's layout has 16 bytes of each of 16 rows in a quarter of a wavefront,
+// sixteen cache lines where four would do (8,192 rows at rank 64, two launches: 50 us
+// where this takes 28).  y leaves the same way.
+// Measured (2,048 columns in and out, bfloat16): 8,192 rows of eight requests, rank
+// 64, 101 MB of x, base and y: 13.1 + 16.2 us, 20 at a copy's rate; what is left is
+// each workgroup's chain of loads, LDS and products.  64 rows with an adapter each,
+// rank 16, 1,536 columns out: 6.4 us, one fp32 row 6.9, that chain alone.
 // fp32 values enter as sums of bfloat16 parts: x as three (exact but for its
 // smallest values), h as two where the results are bfloat16 (off by 2^-16 of it,
 // where they round by 2^-8) and three where they are fp32.  A row has the same
@@ -608,9 +612,10 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
   }
 }
 
-// A workgroup takes 64 columns of two tiles, one per wavefront.  B goes through
-// LDS for all of them, adapter by adapter where the tiles' requests have different
-// ones.
+// A workgroup takes 64 columns of two tiles, one per wavefront (8,192 rows, rank 64,
+// with one, two, three, four and eight tiles: 29.4, 28.2, 27.7, 28.6 and 38.9 us for
+// both launches).  B goes through LDS for all of them, adapter by adapter where the
+// tiles' requests have different ones.
 template <typename YT, int RS>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   constexpr int HP = h_parts<YT>();
@@ -683,7 +688,10 @@ int most_tiles(int64_t T, int n_seq, int rows) {
 }
 
 // Where every row is a request: from how many rows on those of one adapter share a
-// workgroup, and up to how many (each looks through all adapters).
+// workgroup, and up to how many (each looks through all adapters).  Apart against
+// together, 4 and 48 adapters of rank 16, bfloat16: 512 rows 12.5 against 18.3 and
+// 15.5 against 13.9 us, 1,024 rows 26.2 against 22.7 and 28.3 against 20.8, 4,096
+// rows 88 against 60 and 93 against 65.
 constexpr int kTogether = 1024, kMostTogether = 4096;
 
 template <typename XT, typename YT, int MT>
@@ -696,6 +704,8 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
     lora_up_kernel<YT, (MT + 1) / 2><<<grid, 64 * kUpWaves, 0, s>>>(g);
     return hipGetLastError();
   }
+  // about a workgroup per CU: slices of the columns while there are few tiles (one
+  // row, 1,536 columns in 3 slices 7.4 us, in 24 6.4; 64 rows in 3 5.9, in 24 6.7)
   const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
   g.together = !g.seq && tiles >= kTogether && tiles <= kMostTogether;
   // those that are left after rows have joined others, if these are spread evenly
@@ -715,7 +725,9 @@ hipError_t launch_as(const LoraArgs& g, hipStream_t s) {
   return launch_rank<XT, YT, 8>(g, s);
 }
 
-// Rows from which two launches are made.
+// Rows from which two launches are made (eight requests, 2,048 columns, bfloat16,
+// one launch against two: 1,024 rows at rank 16 10.4 and 10.5 us, at rank 64 15.7
+// against 15.0; 2,048 rows 12.5 against 12.1 and 19.5 against 16.3).
 constexpr int64_t kManyRows = 1024;
 
 }  // namespace
