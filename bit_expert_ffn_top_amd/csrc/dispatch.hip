@@ -14,6 +14,7 @@
 
 #include "moe_internal.h"
 #include "row_device.h"
+#include "scan_device.h"
 
 namespace bitffn {
 namespace {
@@ -47,6 +48,21 @@ __host__ __device__ inline int counts_row(int E) { return (E + 7) & ~7; }
 
 __device__ __forceinline__ bool is_expert(int e, int E) { return e >= 0 && e < E; }
 
+// The ids of pairs p0 + thread, + 256, .. below p1: eight loads at a time, so that
+// a workgroup waits for memory once for 2,048 of them.  -1 for ids of no expert.
+template <typename F>
+__device__ __forceinline__ void each_id(const int32_t* __restrict__ idx, int p0, int p1, int E, F f) {
+  constexpr int kBatch = 8;
+  for (int p = p0 + static_cast<int>(threadIdx.x); p < p1; p += kBatch * kThreads) {
+    int e[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) e[i] = idx[min(p + i * kThreads, p1 - 1)];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (p + i * kThreads < p1) f(p + i * kThreads, is_expert(e[i], E) ? e[i] : -1);
+  }
+}
+
 // Pairs of every expert in one part of the tokens.
 __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a) {
   __shared__ int32_t s_count[kMaxE];
@@ -55,10 +71,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a
   __syncthreads();
   const int t0 = min(a.T, static_cast<int>(blockIdx.x) * a.part_tokens);
   const int t1 = min(a.T, t0 + a.part_tokens);
-  for (int p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += kThreads) {
-    const int e = a.idx[p];
-    if (is_expert(e, a.E)) atomicAdd(&s_count[e], 1);
-  }
+  each_id(a.idx, t0 * a.k, t1 * a.k, a.E, [&](int, int e) {
+    if (e >= 0) atomicAdd(&s_count[e], 1);
+  });
   __syncthreads();
   for (int e = threadIdx.x; e < row; e += kThreads)
     a.counts[static_cast<int>(blockIdx.x) * row + e] = static_cast<uint16_t>(s_count[e]);
@@ -92,12 +107,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
     t1 = min(a.T, t0 + a.tokens);
   }
   const int p0 = t0 * k, own = (t1 - t0) * k;
-  const int32_t* idx = a.idx;
   for (int e = tid; e < kMaxE; e += kThreads) s_total[e] = s_before[e] = 0;
-  for (int q = tid; q < own; q += kThreads) {
-    const int e = idx[p0 + q];
-    s_own[q] = is_expert(e, E) ? e : -1;
-  }
+  for (int q = own + tid; q < (own + 3) / 4 * 4; q += kThreads) s_own[q] = -1;
+  each_id(a.idx, p0, p0 + own, E, [&](int p, int e) { s_own[p - p0] = e; });
   __syncthreads();
   if (COUNTED) {
     // eight experts' counts per load, the parts dealt to groups of threads
@@ -108,15 +120,21 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) total[i] = before[i] = 0;
       const uint4* src = reinterpret_cast<const uint4*>(a.counts) + j;
-#pragma unroll 8
-      for (int c = g; c < a.parts; c += groups) {
-        const uint4 v = src[c * vecs];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      constexpr int kBatch = 8;
+      for (int c = g; c < a.parts; c += kBatch * groups) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-          total[i] += n;
-          before[i] += c < part ? n : 0;
+        for (int n = 0; n < kBatch; ++n) v[n] = src[min(c + n * groups, a.parts - 1) * vecs];
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+          const int at = c + n * groups;
+          const uint32_t w[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int m = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+            total[i] += at < a.parts ? m : 0;
+            before[i] += at < part ? m : 0;
+          }
         }
       }
 #pragma unroll
@@ -125,20 +143,16 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
         if (before[i]) atomicAdd(&s_before[8 * j + i], before[i]);
       }
     }
-    for (int p = part * a.part_tokens * k + tid; p < p0; p += kThreads) {
-      const int e = idx[p];
-      if (is_expert(e, E)) atomicAdd(&s_before[e], 1);
-    }
+    each_id(a.idx, part * a.part_tokens * k, p0, E, [&](int, int e) {
+      if (e >= 0) atomicAdd(&s_before[e], 1);
+    });
   } else {
-    const int n = a.T * k;
-#pragma unroll 4
-    for (int p = tid; p < n; p += kThreads) {
-      const int e = idx[p];
-      if (is_expert(e, E)) {
+    each_id(a.idx, 0, a.T * k, E, [&](int p, int e) {
+      if (e >= 0) {
         atomicAdd(&s_total[e], 1);
         if (p < p0) atomicAdd(&s_before[e], 1);
       }
-    }
+    });
   }
   __syncthreads();
   // the experts' first rows: an exclusive scan, four experts per thread
@@ -149,12 +163,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
     c[j] = sum;
     sum += s_total[tid * kPer + j];
   }
-  int scan = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int up = __shfl_up(scan, off);
-    if (lane >= off) scan += up;
-  }
+  const int scan = wave_scan_add(sum);
   if (lane == 63) s_wave[wave] = scan;
   __syncthreads();
   int first = scan - sum;
@@ -172,7 +181,11 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {
     int at = -1;
     if (e >= 0) {
       at = s_before[e];
-      for (int r = 0; r < q; ++r) at += s_own[r] == e;
+#pragma unroll 4
+      for (int r = 0; r < q; r += 4) {   // four at a time; those past q do not count
+        const int4 o = *reinterpret_cast<const int4*>(&s_own[r]);
+        at += (o.x == e) + (r + 1 < q && o.y == e) + (r + 2 < q && o.z == e) + (r + 3 < q && o.w == e);
+      }
     }
     s_pos[q] = at;
     a.pair_pos[p0 + q] = at;
