@@ -3,9 +3,10 @@
 //
 // Both products are on the matrix cores, with the adapter's rows as the first
 // operand:
-//   h = A x    16 or 32 consecutive rows of one request (a row alone where every
-//              row is a request); the eight wavefronts of a workgroup split the
-//              columns, and their sums meet in LDS in a fixed order
+//   h = A x    16 or 32 consecutive rows of one request, or 16 of one adapter where
+//              every row is a request (a row alone where there are few); the eight
+//              wavefronts of a workgroup split the columns, and their sums meet in
+//              LDS in a fixed order
 //   y = B h    64 columns per wavefront
 // Few rows: both in one launch.  A workgroup repeats h for its slice of y's
 // columns; A is small (64 KB at rank 16 and 2048 columns), and a second launch
@@ -175,41 +176,97 @@ struct Rows {
   __device__ __forceinline__ Rows from(int i) const { return {row0 + i, n - i, nullptr}; }   // not LISTED
 };
 
-// Where every row is a request: row t and the next rows with its adapter, 16 in
-// all, if a whole number of sixteens of them comes before t; else false, they are
-// other workgroups'.  A row without an adapter is alone.
-__device__ __forceinline__ bool rows_of_adapter(const LoraArgs& g, int t, int m, int* list, int& n) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int i = 0; i < t; i += 64) {
-    const int s = i + lane;
-    before += __popcll(__ballot(s < t && g.adapter[min(s, g.T - 1)] == m));
+// Where every row is a request: tile `tile` of the rows sorted by adapter, 16 of
+// one adapter (the last ones of each may be fewer; rows without one come last),
+// found by the whole workgroup.  It counts every adapter's rows in LDS, scans their
+// tiles, and then gathers the rows: each wavefront looks through an eighth of all.
+struct TogetherShared {
+  int count[MOE_MAX_EXPERTS + 1];
+  int wave[kWaves];
+  int who, nth;    // the tile's adapter, and which of its tiles it is
+  int list[16];
+  int n;
+};
+
+__device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared& sh, int& m) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int buckets = g.n_adapters + 1;
+  for (int b = tid; b < buckets; b += kThreads) sh.count[b] = 0;
+  if (tid == 0) {
+    sh.who = -1;
+    sh.n = 0;
   }
-  if (before % 16) return false;
-  n = 1;
-  if (lane == 0) list[0] = 0;
-  for (int i = t + 1; i < g.T && n < 16; i += 64) {
-    const int s = i + lane;
-    const bool same = s < g.T && g.adapter[min(s, g.T - 1)] == m;
-    const uint64_t all = __ballot(same);
-    const int at = n + __popcll(all & ((uint64_t{1} << lane) - 1));
-    if (same && at < 16) list[at] = s - t;
-    n += __popcll(all);
+  __syncthreads();
+  const int part = ((g.T + kWaves - 1) / kWaves + 63) / 64 * 64;   // rows of a wavefront
+  const int t0 = min(g.T, wave * part), t1 = min(g.T, t0 + part);
+  const auto bucket = [&](int t) {
+    const int id = g.adapter[min(t, g.T - 1)];
+    return id >= 0 && id < g.n_adapters ? id : g.n_adapters;
+  };
+  constexpr int kBatch = 8;
+  for (int t = t0 + lane; t < t1; t += 64 * kBatch) {
+    int b[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) b[i] = bucket(t + 64 * i);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (t + 64 * i < t1) atomicAdd(&sh.count[b[i]], 1);
   }
-  n = min(n, 16);
+  __syncthreads();
+  constexpr int kPer = (MOE_MAX_EXPERTS + kThreads) / kThreads;   // buckets of a thread
+  int n[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
+    n[i] = b < buckets ? (sh.count[b] + 15) / 16 : 0;
+    sum += n[i];
+  }
+  const int scan = wave_scan_add(sum);
+  if (lane == 63) sh.wave[wave] = scan;
+  __syncthreads();
+  int left = tile - (scan - sum);
+  for (int w = 0; w < wave; ++w) left -= sh.wave[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (left >= 0 && left < n[i]) {
+      sh.who = tid * kPer + i;
+      sh.nth = left;
+    }
+    left -= n[i];
+  }
+  __syncthreads();
+  const int who = sh.who;
+  if (who < 0) return false;   // uniform
+  int mine = 0;
+  for (int t = t0; t < t1; t += 64)
+    mine += __popcll(__ballot(t + lane < t1 && bucket(t + lane) == who));
+  if (lane == 0) sh.wave[wave] = mine;   // read above, before the barrier
+  __syncthreads();
+  int at = -16 * sh.nth;   // place of the next row found among the tile's
+  for (int w = 0; w < wave; ++w) at += sh.wave[w];
+  for (int t = t0; t < t1 && at < 16; t += 64) {
+    const bool hit = t + lane < t1 && bucket(t + lane) == who;
+    const uint64_t all = __ballot(hit);
+    const int place = at + __popcll(all & ((uint64_t{1} << lane) - 1));
+    if (hit && place >= 0 && place < 16) sh.list[place] = t + lane;
+    at += __popcll(all);
+  }
+  if (tid == 0) sh.n = min(16, sh.count[who] - 16 * sh.nth);
+  __syncthreads();
+  m = who < g.n_adapters ? who : -1;
   return true;
 }
 
 // Rows of a tile without an adapter: columns [n0, n1) of base.
-template <typename YT>
-__device__ __forceinline__ void copy_base(const LoraArgs& g, int row0, int rows, int n0, int n1) {
+template <typename YT, bool LISTED>
+__device__ __forceinline__ void copy_base(const LoraArgs& g, const Rows<LISTED>& rows, int n0, int n1) {
   const YT* base = static_cast<const YT*>(g.base);
   YT* y = static_cast<YT*>(g.y);
   if (y == base) return;
   const int parts = (n1 - n0) / 8;
-  for (int i = threadIdx.x; i < rows * parts; i += blockDim.x) {
+  for (int i = threadIdx.x; i < rows.n * parts; i += blockDim.x) {
     const int t = i / parts;
-    const int64_t at = static_cast<int64_t>(row0 + t) * g.d_out + n0 + 8 * (i - t * parts);
+    const int64_t at = static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out + n0 + 8 * (i - t * parts);
     RowPart<YT, 8> v;
     v.load(base + at);
     v.store(y + at);
@@ -507,23 +564,27 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   static_assert(kWaveBytes % 16 == 0, "");
   __shared__ __align__(16) char s_wave[kWaves * kWaveBytes];
   __shared__ nu4 s_h[HP][RS][64];
-  __shared__ int s_list[kWaves][16];   // each wavefront's own: no barrier
+  __shared__ TogetherShared s_rows;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int row0, row1, request;
-  if (!find_tile(g, blockIdx.x, 16, row0, row1, request)) return;
-  const int m = adapter_of(g, request);
+  Rows<true> rows{0, 0, s_rows.list};
+  int m;
+  if (g.together) {
+    if (!find_together(g, blockIdx.x, s_rows, m)) return;
+    rows.n = s_rows.n;
+  } else {
+    int row1, request;
+    if (!find_tile(g, blockIdx.x, 16, rows.row0, row1, request)) return;
+    rows.n = row1 - rows.row0;
+    m = adapter_of(g, request);
+    if (tid < 16) s_rows.list[tid] = tid;
+    __syncthreads();
+  }
+  m = __builtin_amdgcn_readfirstlane(m);
   const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
   if (m < 0 || m >= g.n_adapters) {
-    copy_base<YT>(g, row0, row1 - row0, n0, n1);
+    copy_base<YT>(g, rows, n0, n1);
     return;
   }
-  Rows<true> rows{row0, row1 - row0, s_list[wave]};
-  if (g.together) {
-    if (!rows_of_adapter(g, row0, m, s_list[wave], rows.n)) return;
-  } else if (lane < 16) {
-    s_list[wave][lane] = lane;
-  }
-  wave_order();
   const float scale = g.scale ? g.scale[m] : 1.0f;
   char* mine = s_wave + wave * kWaveBytes;
   const uint16_t* b = g.b + static_cast<int64_t>(m) * g.d_out * g.rank;
@@ -688,11 +749,11 @@ int most_tiles(int64_t T, int n_seq, int rows) {
 }
 
 // Where every row is a request: from how many rows on those of one adapter share a
-// workgroup, and up to how many (each looks through all adapters).  Apart against
-// together, 4 and 48 adapters of rank 16, bfloat16: 512 rows 12.5 against 18.3 and
-// 15.5 against 13.9 us, 1,024 rows 26.2 against 22.7 and 28.3 against 20.8, 4,096
-// rows 88 against 60 and 93 against 65.
-constexpr int kTogether = 1024, kMostTogether = 4096;
+// workgroup (apart against together, bfloat16, rank 64, 4 and 48 adapters: 64 rows
+// 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and 15.3
+// against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows 280
+// against 38 and 448 against 64).
+constexpr int kTogether = 128;
 
 template <typename XT, typename YT, int MT>
 hipError_t launch_rank(LoraArgs g, hipStream_t s) {
@@ -706,11 +767,10 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
   }
   // about a workgroup per CU: slices of the columns while there are few tiles (one
   // row, 1,536 columns in 3 slices 7.4 us, in 24 6.4; 64 rows in 3 5.9, in 24 6.7)
-  const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
-  g.together = !g.seq && tiles >= kTogether && tiles <= kMostTogether;
-  // those that are left after rows have joined others, if these are spread evenly
-  const int64_t left = g.together ? std::min(tiles, tiles / 16 + g.n_adapters) : tiles;
-  const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / left)));
+  g.together = !g.seq && g.T >= kTogether;
+  const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16)
+                              : g.together ? most_tiles(g.T, g.n_adapters + 1, 16) : g.T;
+  const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / tiles)));
   g.slice = (groups + slices - 1) / slices * kGroup;
   const dim3 grid(static_cast<unsigned>(tiles), (g.d_out + g.slice - 1) / g.slice);
   lora_kernel<XT, YT, MT><<<grid, kThreads, 0, s>>>(g);

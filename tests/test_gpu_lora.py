@@ -245,14 +245,34 @@ def test_many_rows_of_one_request():
 
 
 @pytest.mark.parametrize("types", TYPES)
-@pytest.mark.parametrize("T,n", [(1024, 1), (1024, 40), (1500, 3), (4096, 200), (4097, 3)])
+@pytest.mark.parametrize("T,n", [(127, 5), (128, 5), (1024, 1), (1024, 40), (1500, 3), (4096, 200), (4097, 3)])
 def test_many_single_rows(T, n, types):
-    """From 1,024 rows on, rows of one adapter share a workgroup, wherever they
-    lie; rows without one among them; and the bits that bounds between all rows
-    give, which take other launches."""
+    """From 128 rows on, rows of one adapter share a workgroup, wherever they lie;
+    rows without one among them; and the bits that bounds between all rows give,
+    which take other launches."""
     bf = _bf()
     base, x, a, b, scale = _inputs(T, n, 24, 96, 48, *types)
     who = np.random.default_rng(T + n).integers(-1, n + 1, T)
     who[:40] = np.where(np.arange(40) % 3, 0, -1)
     y = _check(base, x, a, b, who, None, scale)
     assert torch.equal(bf.lora(base, x, a, b, _i32(who), seq_offsets=_i32(np.arange(T + 1)), scale=scale), y)
+
+
+@pytest.mark.parametrize("T,n,d_in", [(65536, 5, 32), (65536, 1024, 64), (8000, 1024, 16384), (65536, 2, 16384)])
+def test_the_most_single_rows(T, n, d_in):
+    """Up to the most rows, adapters and row bytes: the bits that bounds give."""
+    bf = _bf()
+    dev = need_gpu()
+    g = torch.Generator(device=dev).manual_seed(T + n)
+    x = torch.randn((T, d_in), generator=g, device=dev)
+    base = torch.randn((T, 16), generator=g, device=dev)
+    a = (torch.randn((n, 8, d_in), generator=g, device=dev) / d_in ** 0.5).bfloat16()
+    b = torch.randn((n, 16, 8), generator=g, device=dev).bfloat16()
+    who = torch.randint(-1, n + 1, (T,), generator=g, device=dev).int()
+    y = bf.lora(base, x, a, b, who)
+    assert torch.equal(bf.lora(base, x, a, b, who, seq_offsets=_i32(np.arange(T + 1))), y)
+    none = (who < 0) | (who >= n)
+    assert torch.equal(y[none], base[none]) and not torch.equal(y[~none], base[~none])
+    some = torch.randint(0, T, (40,), generator=g, device=dev).tolist() + [0, T - 1]
+    r = ol.lora(_np(base[some]), _np(x[some]), _np(a), _np(b), who[some].cpu().numpy())
+    assert (np.abs(_np(y[some]) - r["y"]) <= _bound(r, d_in, 8, F32)).all()
