@@ -3,10 +3,10 @@
 //
 // Both products are on the matrix cores, with the adapter's rows as the first
 // operand:
-//   h = A x    16 or 32 consecutive rows of one request, or 16 of one adapter where
-//              every row is a request (a row alone where there are few); the eight
-//              wavefronts of a workgroup split the columns, and their sums meet in
-//              LDS in a fixed order
+//   h = A x    16 or 32 consecutive rows of one request, or 16 of one adapter
+//              gathered from many short requests; the eight wavefronts of a
+//              workgroup split the columns, and their sums meet in LDS in a fixed
+//              order
 //   y = B h    64 columns per wavefront
 // Few rows: both in one launch.  A workgroup repeats h for its slice of y's
 // columns; A is small (64 KB at rank 16 and 2048 columns), and a second launch
@@ -50,7 +50,7 @@ struct LoraArgs {
   void* y;
   int T, d_in, d_out, n_adapters, rank, n_seq;
   int slice;     // output columns of a workgroup, a multiple of kGroup
-  int together;  // rows of one adapter share a workgroup (a row for every request)
+  int together;  // rows of one adapter share a workgroup
   int4* tiles;   // in the workspace (many rows)
   nu4* h;
   int n_tiles;
@@ -176,82 +176,108 @@ struct Rows {
   __device__ __forceinline__ Rows from(int i) const { return {row0 + i, n - i, nullptr}; }   // not LISTED
 };
 
-// Where every row is a request: tile `tile` of the rows sorted by adapter, 16 of
-// one adapter (the last ones of each may be fewer; rows without one come last),
-// found by the whole workgroup.  It counts every adapter's rows in LDS, scans their
-// tiles, and then gathers the rows: each wavefront looks through an eighth of all.
+// Tile `tile` of the requests' rows sorted by adapter, 16 rows of one adapter (the
+// last ones of each may be fewer; rows without one come last), found by the whole
+// workgroup: it counts every adapter's rows in LDS, scans their tiles, and gathers
+// the rows.  Each wavefront looks through an eighth of the requests.
 struct TogetherShared {
   int count[MOE_MAX_EXPERTS + 1];
-  int wave[kWaves];
+  int wave[2][kWaves];
   int who, nth;    // the tile's adapter, and which of its tiles it is
   int list[16];
-  int n;
 };
 
-__device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared& sh, int& m) {
+// The rows of 64 requests from s on, one per lane: the first, and how many; requests
+// from s1 on have none.  low: the largest bound so far.
+__device__ __forceinline__ void request_rows(const LoraArgs& g, int s, int s1, int& low, int& start, int& n) {
+  const int lane = threadIdx.x & 63;
+  if (!g.seq) {
+    start = s + lane;
+    n = start < s1;
+    return;
+  }
+  const int bound = s + lane < s1 ? min(max(g.seq[s + lane + 1], 0), g.T) : 0;
+  const int upto = wave_scan_max(bound), end = max(low, upto);
+  start = max(low, lane_before(upto));
+  n = end - start;
+  low = max(low, lane_value(upto, 63));
+}
+
+__device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared& sh, int& m, int& rows) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int buckets = g.n_adapters + 1;
   for (int b = tid; b < buckets; b += kThreads) sh.count[b] = 0;
-  if (tid == 0) {
-    sh.who = -1;
-    sh.n = 0;
+  if (tid == 0) sh.who = -1;
+  const int part = ((g.n_seq + kWaves - 1) / kWaves + 63) / 64 * 64;   // requests of a wavefront
+  const int s0 = min(g.n_seq, wave * part), s1 = min(g.n_seq, s0 + part);
+  int low = 0;   // the largest bound before the wavefront's requests
+  if (g.seq) {
+    int top = 0;
+    for (int s = s0 + lane; s < s1; s += 64) top = max(top, min(max(g.seq[s + 1], 0), g.T));
+    top = lane_value(wave_scan_max(top), 63);
+    if (lane == 0) sh.wave[0][wave] = top;
+    low = min(max(g.seq[0], 0), g.T);
   }
   __syncthreads();
-  const int part = ((g.T + kWaves - 1) / kWaves + 63) / 64 * 64;   // rows of a wavefront
-  const int t0 = min(g.T, wave * part), t1 = min(g.T, t0 + part);
-  const auto bucket = [&](int t) {
-    const int id = g.adapter[min(t, g.T - 1)];
+  if (g.seq)
+    for (int w = 0; w < wave; ++w) low = max(low, sh.wave[0][w]);
+  const auto bucket = [&](int s) {
+    const int id = g.adapter[min(s + lane, g.n_seq - 1)];
     return id >= 0 && id < g.n_adapters ? id : g.n_adapters;
   };
-  constexpr int kBatch = 8;
-  for (int t = t0 + lane; t < t1; t += 64 * kBatch) {
-    int b[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) b[i] = bucket(t + 64 * i);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (t + 64 * i < t1) atomicAdd(&sh.count[b[i]], 1);
+  int upto = low, start, n;
+  for (int s = s0; s < s1; s += 64) {
+    const int b = bucket(s);
+    request_rows(g, s, s1, upto, start, n);
+    if (n > 0) atomicAdd(&sh.count[b], n);
   }
   __syncthreads();
   constexpr int kPer = (MOE_MAX_EXPERTS + kThreads) / kThreads;   // buckets of a thread
-  int n[kPer], sum = 0;
+  int tiles[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = tid * kPer + i;
-    n[i] = b < buckets ? (sh.count[b] + 15) / 16 : 0;
-    sum += n[i];
+    tiles[i] = b < buckets ? (sh.count[b] + 15) / 16 : 0;
+    sum += tiles[i];
   }
   const int scan = wave_scan_add(sum);
-  if (lane == 63) sh.wave[wave] = scan;
+  if (lane == 63) sh.wave[1][wave] = scan;
   __syncthreads();
   int left = tile - (scan - sum);
-  for (int w = 0; w < wave; ++w) left -= sh.wave[w];
+  for (int w = 0; w < wave; ++w) left -= sh.wave[1][w];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (left >= 0 && left < n[i]) {
+    if (left >= 0 && left < tiles[i]) {
       sh.who = tid * kPer + i;
       sh.nth = left;
     }
-    left -= n[i];
+    left -= tiles[i];
   }
   __syncthreads();
   const int who = sh.who;
   if (who < 0) return false;   // uniform
   int mine = 0;
-  for (int t = t0; t < t1; t += 64)
-    mine += __popcll(__ballot(t + lane < t1 && bucket(t + lane) == who));
-  if (lane == 0) sh.wave[wave] = mine;   // read above, before the barrier
+  upto = low;
+  for (int s = s0; s < s1; s += 64) {
+    const int b = bucket(s);
+    request_rows(g, s, s1, upto, start, n);
+    mine += b == who ? n : 0;
+  }
+  mine = lane_value(wave_scan_add(mine), 63);
+  if (lane == 0) sh.wave[0][wave] = mine;   // last read before two barriers
   __syncthreads();
   int at = -16 * sh.nth;   // place of the next row found among the tile's
-  for (int w = 0; w < wave; ++w) at += sh.wave[w];
-  for (int t = t0; t < t1 && at < 16; t += 64) {
-    const bool hit = t + lane < t1 && bucket(t + lane) == who;
-    const uint64_t all = __ballot(hit);
-    const int place = at + __popcll(all & ((uint64_t{1} << lane) - 1));
-    if (hit && place >= 0 && place < 16) sh.list[place] = t + lane;
-    at += __popcll(all);
+  for (int w = 0; w < wave; ++w) at += sh.wave[0][w];
+  upto = low;
+  for (int s = s0; s < s1 && at < 16; s += 64) {
+    const int b = bucket(s);
+    request_rows(g, s, s1, upto, start, n);
+    if (b != who) n = 0;
+    const int end = at + wave_scan_add(n), first = end - n;
+    for (int place = max(first, 0); place < min(end, 16); ++place) sh.list[place] = start + place - first;
+    at = lane_value(end, 63);
   }
-  if (tid == 0) sh.n = min(16, sh.count[who] - 16 * sh.nth);
+  rows = min(16, sh.count[who] - 16 * sh.nth);
   __syncthreads();
   m = who < g.n_adapters ? who : -1;
   return true;
@@ -569,8 +595,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   Rows<true> rows{0, 0, s_rows.list};
   int m;
   if (g.together) {
-    if (!find_together(g, blockIdx.x, s_rows, m)) return;
-    rows.n = s_rows.n;
+    if (!find_together(g, blockIdx.x, s_rows, m, rows.n)) return;
   } else {
     int row1, request;
     if (!find_tile(g, blockIdx.x, 16, rows.row0, row1, request)) return;
@@ -748,12 +773,18 @@ int most_tiles(int64_t T, int n_seq, int rows) {
   return static_cast<int>((T + (rows - 1) * std::min(static_cast<int64_t>(n_seq), T)) / rows);
 }
 
-// Where every row is a request: from how many rows on those of one adapter share a
-// workgroup (apart against together, bfloat16, rank 64, 4 and 48 adapters: 64 rows
-// 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and 15.3
-// against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows 280
-// against 38 and 448 against 64).
-constexpr int kTogether = 128;
+// Requests beyond the number of adapters from which rows of one adapter share a
+// workgroup: that many tiles at least are spared, for some 2 us of gathering (a row
+// for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
+// 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
+// 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
+// 280 against 38 and 448 against 64).
+constexpr int kTogether = 64;
+
+// Their offsets into x have 32 bits.
+bool gathers(int64_t T, int n_seq, int n_adapters, int64_t row_bytes) {
+  return n_seq >= n_adapters + kTogether && T * row_bytes < (int64_t{1} << 32) - (1 << 17);
+}
 
 template <typename XT, typename YT, int MT>
 hipError_t launch_rank(LoraArgs g, hipStream_t s) {
@@ -767,9 +798,9 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
   }
   // about a workgroup per CU: slices of the columns while there are few tiles (one
   // row, 1,536 columns in 3 slices 7.4 us, in 24 6.4; 64 rows in 3 5.9, in 24 6.7)
-  g.together = !g.seq && g.T >= kTogether;
-  const int64_t tiles = g.seq ? most_tiles(g.T, g.n_seq, 16)
-                              : g.together ? most_tiles(g.T, g.n_adapters + 1, 16) : g.T;
+  g.together = gathers(g.T, g.n_seq, g.n_adapters, int64_t{g.d_in} * sizeof(XT));
+  const int64_t tiles = g.together ? most_tiles(g.T, g.n_adapters + 1, 16)
+                                   : g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
   const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / tiles)));
   g.slice = (groups + slices - 1) / slices * kGroup;
   const dim3 grid(static_cast<unsigned>(tiles), (g.d_out + g.slice - 1) / g.slice);
@@ -790,10 +821,17 @@ hipError_t launch_as(const LoraArgs& g, hipStream_t s) {
 // against 15.0; 2,048 rows 12.5 against 12.1 and 19.5 against 16.3).
 constexpr int64_t kManyRows = 1024;
 
+// Rows per request below which, if they can be gathered, one launch is made all the
+// same: its tiles are full where the others' hold one request each (48 adapters,
+// rank 64, bfloat16, gathered against two launches: 1,000 requests of 2 rows 28
+// against 78 us, 500 of 1 to 7 28 against 43, 8,000 rows in 500 62 against 57, 4,000
+// in 200 38 against 30).
+constexpr int64_t kShortRows = 16;
+
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t T, int rank, int n_seq) {
-  if (n_seq == 0 || T < kManyRows) return 0;   // 0: a row for every request
+  if (n_seq == 0 || T < kManyRows) return 0;   // n_seq = 0: a row for every request
   const int64_t tiles = most_tiles(T, n_seq, kTileRows), steps = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
   return static_cast<size_t>(align256(tiles * 16) + tiles * kTiles16 * 3 * steps * 1024);
 }
@@ -804,7 +842,9 @@ hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, 
                        void* y, int y_dtype, void* ws, hipStream_t s) {
   LoraArgs g{base, x, a, b, seq, adapter, scale, y, static_cast<int>(T),
              d_in, d_out, n_adapters, rank, n_seq, 0, 0, nullptr, nullptr, 0};
-  if (lora_workspace_bytes(T, rank, seq ? n_seq : 0) > 0) {
+  const bool short_requests = T / kShortRows < n_seq &&
+                              gathers(T, n_seq, n_adapters, int64_t{d_in} * (x_dtype == MOE_DTYPE_F32 ? 4 : 2));
+  if (lora_workspace_bytes(T, rank, seq ? n_seq : 0) > 0 && !short_requests) {
     g.n_tiles = most_tiles(T, n_seq, kTileRows);
     g.tiles = static_cast<int4*>(ws);
     g.h = reinterpret_cast<nu4*>(static_cast<char*>(ws) + align256(int64_t{g.n_tiles} * 16));

@@ -247,9 +247,9 @@ def test_many_rows_of_one_request():
 @pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("T,n", [(127, 5), (128, 5), (1024, 1), (1024, 40), (1500, 3), (4096, 200), (4097, 3)])
 def test_many_single_rows(T, n, types):
-    """From 128 rows on, rows of one adapter share a workgroup, wherever they lie;
-    rows without one among them; and the bits that bounds between all rows give,
-    which take other launches."""
+    """Where requests outnumber the adapters, rows of one adapter share a workgroup,
+    wherever they lie; rows without one among them; and the same with bounds between
+    all rows."""
     bf = _bf()
     base, x, a, b, scale = _inputs(T, n, 24, 96, 48, *types)
     who = np.random.default_rng(T + n).integers(-1, n + 1, T)
@@ -276,3 +276,36 @@ def test_the_most_single_rows(T, n, d_in):
     some = torch.randint(0, T, (40,), generator=g, device=dev).tolist() + [0, T - 1]
     r = ol.lora(_np(base[some]), _np(x[some]), _np(a), _np(b), who[some].cpu().numpy())
     assert (np.abs(_np(y[some]) - r["y"]) <= _bound(r, d_in, 8, F32)).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("S,T", [(70, 150), (200, 900), (400, 1100), (900, 3000), (6000, 20000)])
+def test_many_short_requests_with_bounds_out_of_order(S, T, types):
+    """Gathered rows of requests of 0 to many rows, bounds that step back or leave
+    the range, rows of no request between them; and the bits that rows have alone."""
+    bf = _bf()
+    n = 4
+    base, x, a, b, scale = _inputs(T, n, 16, 64, 48, *types)
+    rng = np.random.default_rng(S)
+    bounds = np.sort(rng.integers(3, T - 2, S + 1))
+    at = rng.integers(0, S + 1, S // 10)
+    bounds[at] = rng.choice([-2 ** 31, -1, 0, T // 3, T - 5], len(at))
+    if S > 300:
+        bounds[-1] = 2 ** 31 - 1
+    who = rng.integers(-1, n + 1, S)
+    y = _check(base, x, a, b, who, bounds, scale)
+    of = ol.requests_of(T, bounds)
+    for t in rng.choice(np.flatnonzero(of >= 0), 5):
+        one = bf.lora(base[t:t + 1].clone(), x[t:t + 1].clone(), a, b, _i32(who[of[t]:of[t] + 1]), scale=scale)
+        assert torch.equal(one[0], y[t])
+
+
+def test_gathered_rows_of_one_long_and_many_short_requests():
+    """Rows of one adapter from a request of 700 rows and 150 single ones."""
+    bf = _bf()
+    base, x, a, b, scale = _inputs(850, 2, 40, 96, 64, BF16, F32)
+    bounds = np.concatenate([np.arange(76), [775], 776 + np.arange(75)])
+    who = np.where(np.arange(len(bounds) - 1) % 3, 1, 0)
+    y = _check(base, x, a, b, who, bounds, scale)
+    one = bf.lora(base[75:775].clone(), x[75:775].clone(), a, b, _i32(who[75:76]), seq_offsets=_i32([0, 700]), scale=scale)
+    assert torch.equal(one, y[75:775])
