@@ -721,9 +721,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
     const int t = tile0 + w;
     all[w] = t < g.n_tiles ? g.tiles[t].z : -1;
   }
-  YRows<YT, kGroup> yr[kTiles16];
+  // Loads arrive in the order in which they are asked for: B, which all wait for
+  // first, from the L2 cache, then h, then base, which the results are added to.
+  int who = -1;
 #pragma unroll
-  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, rows.from(16 * j), c);
+  for (int w = kUpWaves - 1; w >= 0; --w) who = all[w] >= 0 ? all[w] : who;
+  const auto rows_of_b = [&](int adapter) { return g.b + static_cast<int64_t>(adapter) * g.d_out * g.rank; };
+  B bl;
+  if (who >= 0) bl.load(g, rows_of_b(who), c, tid);
   nu4 hv[kTiles16][HP][RS];
   if (m >= 0) {
     const nu4* h = g.h + static_cast<int64_t>(tile) * kTiles16 * (HP * RS * 64) + lane;
@@ -733,23 +738,26 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
       for (int p = 0; p < HP; ++p)
 #pragma unroll
         for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
-  } else if (g.y != g.base) {   // no adapter
+  }
+  YRows<YT, kGroup> yr[kTiles16];
+#pragma unroll
+  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, rows.from(16 * j), c);
+  if (m < 0 && g.y != g.base) {   // no adapter
 #pragma unroll
     for (int j = 0; j < kTiles16; ++j) yr[j].copy(g, rows.from(16 * j), c);
   }
   bool first = true;
   for (int w = 0; w < kUpWaves; ++w) {
-    const int who = all[w];
+    who = all[w];
     bool again = who < 0;
     for (int v = 0; v < w; ++v) again |= all[v] == who;
     if (again) continue;   // uniform
-    if (!first) __syncthreads();   // the last adapter's rows have been read
-    first = false;
-    {
-      B bl;
-      bl.load(g, g.b + static_cast<int64_t>(who) * g.d_out * g.rank, c, tid);
-      bl.put(g, c, s_b, tid);
+    if (!first) {
+      bl.load(g, rows_of_b(who), c, tid);
+      __syncthreads();   // the last adapter's rows have been read
     }
+    first = false;
+    bl.put(g, c, s_b, tid);
     __syncthreads();
     if (m != who) continue;
 #pragma unroll
