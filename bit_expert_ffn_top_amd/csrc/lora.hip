@@ -283,14 +283,15 @@ __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, Toget
   return true;
 }
 
-// Rows of a tile without an adapter: columns [n0, n1) of base.
+// Rows of a tile without an adapter: columns [n0, n1) of base, by a workgroup or a
+// wavefront.
 template <typename YT, bool LISTED>
-__device__ __forceinline__ void copy_base(const LoraArgs& g, const Rows<LISTED>& rows, int n0, int n1) {
+__device__ __forceinline__ void copy_base(const LoraArgs& g, const Rows<LISTED>& rows, int n0, int n1, int threads) {
   const YT* base = static_cast<const YT*>(g.base);
   YT* y = static_cast<YT*>(g.y);
   if (y == base) return;
   const int parts = (n1 - n0) / 8;
-  for (int i = threadIdx.x; i < rows.n * parts; i += blockDim.x) {
+  for (int i = threadIdx.x % threads; i < rows.n * parts; i += threads) {
     const int t = i / parts;
     const int64_t at = static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out + n0 + 8 * (i - t * parts);
     RowPart<YT, 8> v;
@@ -520,43 +521,40 @@ template <typename YT, int COLS>
 struct YRows {
   static constexpr int kPerRow = COLS / 8, kRows = 64 / kPerRow, kLoads = 16 / kRows;
   RowPart<YT, 8> v[kLoads];
+  // Rows and columns past the end re-read the last ones (which a tile has even where
+  // its second sixteen have none): no load depends on a comparison, so that waiting
+  // for one need not be waiting for all.
   template <bool LISTED>
   __device__ __forceinline__ void load(const LoraArgs& g, const Rows<LISTED>& rows, int c) {
-    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+    const int lane = threadIdx.x & 63, col = min(c + 8 * (lane % kPerRow), g.d_out - 8);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int t = n * kRows + lane / kPerRow;
-      if (t < rows.n && col < g.d_out)
-        v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out + col);
+      const int t = max(rows.row0 + rows.held(n * kRows + lane / kPerRow), 0);
+      v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(t) * g.d_out + col);
     }
   }
-  __device__ __forceinline__ void copy(const LoraArgs& g, const Rows<false>& rows, int c) const {
-    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+  // v = base + the results in LDS, [row][COLS + 4]
+  __device__ __forceinline__ void add(const float* lds) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int t = n * kRows + lane / kPerRow;
-      if (t < rows.n && col < g.d_out)
-        v[n].template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(rows.row0 + t) * g.d_out + col);
-    }
-  }
-  // y = base + the results in LDS, [row][COLS + 4]
-  template <bool LISTED>
-  __device__ __forceinline__ void store(const LoraArgs& g, const Rows<LISTED>& rows, int c, const float* lds) {
-    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int t = n * kRows + lane / kPerRow;
-      const nf4* d = reinterpret_cast<const nf4*>(lds + t * (COLS + 4) + 8 * (lane % kPerRow));
+      const nf4* d = reinterpret_cast<const nf4*>(lds + (n * kRows + lane / kPerRow) * (COLS + 4) + 8 * (lane % kPerRow));
       const nf4 lo = d[0], hi = d[1];
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = v[n].get(e) + (e < 4 ? lo[e % 4] : hi[e % 4]);
-      if (t < rows.n && col < g.d_out) {
-        RowPart<YT, 8> out;
-        out.set(f);
-        out.template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out +
-                                 col);
-      }
+      v[n].set(f);
+    }
+  }
+  template <bool LISTED>
+  __device__ __forceinline__ void store(const LoraArgs& g, const Rows<LISTED>& rows, int c) const {
+    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int t = n * kRows + lane / kPerRow;
+      if (t < rows.n && col < g.d_out)
+        v[n].template store<true>(static_cast<YT*>(g.y) + static_cast<int64_t>(rows.row0 + rows.after(t)) * g.d_out +
+                                  col);
     }
   }
 };
@@ -607,7 +605,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   m = __builtin_amdgcn_readfirstlane(m);
   const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
   if (m < 0 || m >= g.n_adapters) {
-    copy_base<YT>(g, rows, n0, n1);
+    copy_base<YT>(g, rows, n0, n1, kThreads);
     return;
   }
   const float scale = g.scale ? g.scale[m] : 1.0f;
@@ -655,7 +653,8 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
       up_product<RS, HP, kCols>(bv, hv, res, tile);
     }
     wave_order();
-    yr.store(g, rows, c, res);
+    yr.add(res);
+    yr.store(g, rows, c);
     if (k + 1 < k1) yr.load(g, rows, c + kCols);
   }
 }
@@ -721,31 +720,30 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
     const int t = tile0 + w;
     all[w] = t < g.n_tiles ? g.tiles[t].z : -1;
   }
-  // Loads arrive in the order in which they are asked for: B, which all wait for
-  // first, from the L2 cache, then h, then base, which the results are added to.
   int who = -1;
 #pragma unroll
   for (int w = kUpWaves - 1; w >= 0; --w) who = all[w] >= 0 ? all[w] : who;
+  if (who < 0) {   // no adapter in any of the tiles (uniform)
+    copy_base<YT>(g, rows, c, min(g.d_out, c + kGroup), 64);
+    return;
+  }
+  // Loads arrive in the order in which they are asked for: B, which all wait for
+  // first, from the L2 cache, then h (whatever is there, for a tile without an
+  // adapter), then base, which the results are added to.
   const auto rows_of_b = [&](int adapter) { return g.b + static_cast<int64_t>(adapter) * g.d_out * g.rank; };
   B bl;
-  if (who >= 0) bl.load(g, rows_of_b(who), c, tid);
+  bl.load(g, rows_of_b(who), c, tid);
   nu4 hv[kTiles16][HP][RS];
-  if (m >= 0) {
-    const nu4* h = g.h + static_cast<int64_t>(tile) * kTiles16 * (HP * RS * 64) + lane;
+  const nu4* h = g.h + static_cast<int64_t>(min(tile, g.n_tiles - 1)) * kTiles16 * (HP * RS * 64) + lane;
 #pragma unroll
-    for (int j = 0; j < kTiles16; ++j)
+  for (int j = 0; j < kTiles16; ++j)
 #pragma unroll
-      for (int p = 0; p < HP; ++p)
+    for (int p = 0; p < HP; ++p)
 #pragma unroll
-        for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
-  }
+      for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
   YRows<YT, kGroup> yr[kTiles16];
 #pragma unroll
   for (int j = 0; j < kTiles16; ++j) yr[j].load(g, rows.from(16 * j), c);
-  if (m < 0 && g.y != g.base) {   // no adapter
-#pragma unroll
-    for (int j = 0; j < kTiles16; ++j) yr[j].copy(g, rows.from(16 * j), c);
-  }
   bool first = true;
   for (int w = 0; w < kUpWaves; ++w) {
     who = all[w];
@@ -770,9 +768,13 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
         up_product<RS, HP, kGroup>(bv, hv[j], s_res[wave], t);
       }
       wave_order();
-      yr[j].store(g, rows.from(16 * j), c, s_res[wave]);
+      yr[j].add(s_res[wave]);
       wave_order();
     }
+  }
+  if (m >= 0 || g.y != g.base) {   // without an adapter: base as it is
+#pragma unroll
+    for (int j = 0; j < kTiles16; ++j) yr[j].store(g, rows.from(16 * j), c);
   }
 }
 
