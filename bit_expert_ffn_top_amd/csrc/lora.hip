@@ -52,6 +52,7 @@ struct LoraArgs {
   int slice;     // output columns of a workgroup, a multiple of kGroup
   int together;  // rows of one adapter share a workgroup
   int4* tiles;   // in the workspace (many rows)
+  int* lists;
   nu4* h;
   int n_tiles;
 };
@@ -173,18 +174,22 @@ struct Rows {
   __device__ __forceinline__ int after(int i) const { return LISTED ? list[i] : i; }   // i < n
   // The same with the last one in place of those that are missing.
   __device__ __forceinline__ int held(int i) const { return after(min(i, n - 1)); }
-  __device__ __forceinline__ Rows from(int i) const { return {row0 + i, n - i, nullptr}; }   // not LISTED
+  // The rows from the i-th on (there may be none).
+  __device__ __forceinline__ Rows from(int i) const {
+    return LISTED ? Rows{row0, n - i, list + i} : Rows{row0 + i, n - i, nullptr};
+  }
 };
 
-// Tile `tile` of the requests' rows sorted by adapter, 16 rows of one adapter (the
+// Tile `tile` of the requests' rows sorted by adapter, ROWS of one adapter (the
 // last ones of each may be fewer; rows without one come last), found by the whole
 // workgroup: it counts every adapter's rows in LDS, scans their tiles, and gathers
 // the rows.  Each wavefront looks through an eighth of the requests.
+template <int ROWS>
 struct TogetherShared {
   int count[MOE_MAX_EXPERTS + 1];
   int wave[2][kWaves];
   int who, nth;    // the tile's adapter, and which of its tiles it is
-  int list[16];
+  int list[ROWS];
 };
 
 // The rows of 64 requests from s on, one per lane: the first, and how many; requests
@@ -203,7 +208,9 @@ __device__ __forceinline__ void request_rows(const LoraArgs& g, int s, int s1, i
   low = max(low, lane_value(upto, 63));
 }
 
-__device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared& sh, int& m, int& rows) {
+template <int ROWS>
+__device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared<ROWS>& sh, int& m,
+                                              int& rows) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int buckets = g.n_adapters + 1;
   for (int b = tid; b < buckets; b += kThreads) sh.count[b] = 0;
@@ -237,7 +244,7 @@ __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, Toget
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = tid * kPer + i;
-    tiles[i] = b < buckets ? (sh.count[b] + 15) / 16 : 0;
+    tiles[i] = b < buckets ? (sh.count[b] + ROWS - 1) / ROWS : 0;
     sum += tiles[i];
   }
   const int scan = wave_scan_add(sum);
@@ -266,18 +273,18 @@ __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, Toget
   mine = lane_value(wave_scan_add(mine), 63);
   if (lane == 0) sh.wave[0][wave] = mine;   // last read before two barriers
   __syncthreads();
-  int at = -16 * sh.nth;   // place of the next row found among the tile's
+  int at = -ROWS * sh.nth;   // place of the next row found among the tile's
   for (int w = 0; w < wave; ++w) at += sh.wave[0][w];
   upto = low;
-  for (int s = s0; s < s1 && at < 16; s += 64) {
+  for (int s = s0; s < s1 && at < ROWS; s += 64) {
     const int b = bucket(s);
     request_rows(g, s, s1, upto, start, n);
     if (b != who) n = 0;
     const int end = at + wave_scan_add(n), first = end - n;
-    for (int place = max(first, 0); place < min(end, 16); ++place) sh.list[place] = start + place - first;
+    for (int place = max(first, 0); place < min(end, ROWS); ++place) sh.list[place] = start + place - first;
     at = lane_value(end, 63);
   }
-  rows = min(16, sh.count[who] - 16 * sh.nth);
+  rows = min(ROWS, sh.count[who] - ROWS * sh.nth);
   __syncthreads();
   m = who < g.n_adapters ? who : -1;
   return true;
@@ -521,15 +528,16 @@ template <typename YT, int COLS>
 struct YRows {
   static constexpr int kPerRow = COLS / 8, kRows = 64 / kPerRow, kLoads = 16 / kRows;
   RowPart<YT, 8> v[kLoads];
-  // Rows and columns past the end re-read the last ones (which a tile has even where
-  // its second sixteen have none): no load depends on a comparison, so that waiting
-  // for one need not be waiting for all.
-  template <bool LISTED>
+  // Rows and columns past the end re-read the last ones: no load depends on a
+  // comparison, so that waiting for one need not be waiting for all.  ALL: the list
+  // has 16 rows, whatever their number.
+  template <bool ALL = false, bool LISTED>
   __device__ __forceinline__ void load(const LoraArgs& g, const Rows<LISTED>& rows, int c) {
     const int lane = threadIdx.x & 63, col = min(c + 8 * (lane % kPerRow), g.d_out - 8);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const int t = max(rows.row0 + rows.held(n * kRows + lane / kPerRow), 0);
+      const int i = n * kRows + lane / kPerRow;
+      const int t = max(rows.row0 + (ALL ? rows.after(i) : rows.held(i)), 0);
       v[n].load(static_cast<const YT*>(g.base) + static_cast<int64_t>(t) * g.d_out + col);
     }
   }
@@ -575,6 +583,26 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& g, int request) {
   return __builtin_amdgcn_readfirstlane(g.adapter[request]);
 }
 
+// The rows and adapter (-1: none) of the workgroup's tile, of one request.
+template <int ROWS, bool LISTED>
+__device__ __forceinline__ bool tile_rows(const LoraArgs& g, Rows<LISTED>& rows, int& m) {
+  int row1, request;
+  if (!find_tile(g, blockIdx.x, ROWS, rows.row0, row1, request)) return false;
+  rows.n = row1 - rows.row0;
+  m = adapter_of(g, request);
+  if (m >= g.n_adapters) m = -1;
+  return true;
+}
+
+// The same of gathered rows.
+template <int ROWS>
+__device__ __forceinline__ bool tile_rows(const LoraArgs& g, TogetherShared<ROWS>& sh, Rows<true>& rows, int& m) {
+  rows.list = sh.list;
+  if (!find_together<ROWS>(g, blockIdx.x, sh, m, rows.n)) return false;
+  m = __builtin_amdgcn_readfirstlane(m);
+  return true;
+}
+
 // Few rows, one launch.  MT: 16-rank tiles (rank <= 16 MT).
 template <typename XT, typename YT, int MT>
 __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
@@ -588,23 +616,19 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   static_assert(kWaveBytes % 16 == 0, "");
   __shared__ __align__(16) char s_wave[kWaves * kWaveBytes];
   __shared__ nu4 s_h[HP][RS][64];
-  __shared__ TogetherShared s_rows;
+  __shared__ TogetherShared<16> s_rows;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Rows<true> rows{0, 0, s_rows.list};
-  int m;
+  int m = -1;
   if (g.together) {
-    if (!find_together(g, blockIdx.x, s_rows, m, rows.n)) return;
+    if (!tile_rows(g, s_rows, rows, m)) return;
   } else {
-    int row1, request;
-    if (!find_tile(g, blockIdx.x, 16, rows.row0, row1, request)) return;
-    rows.n = row1 - rows.row0;
-    m = adapter_of(g, request);
+    if (!tile_rows<16>(g, rows, m)) return;
     if (tid < 16) s_rows.list[tid] = tid;
     __syncthreads();
   }
-  m = __builtin_amdgcn_readfirstlane(m);
   const int n0 = blockIdx.y * g.slice, n1 = min(g.d_out, n0 + g.slice);
-  if (m < 0 || m >= g.n_adapters) {
+  if (m < 0) {
     copy_base<YT>(g, rows, n0, n1, kThreads);
     return;
   }
@@ -660,29 +684,36 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
 }
 
 // Many rows, two launches.  The workspace holds a table of the first one's tiles
-// (rows, request, adapter or -1), which spares the second one the search, and h by
-// 16 rows in the order of the second product's operand:
-// [tile][16 rows][part][step][lane][8].
+// (first row, number of rows, adapter or -1) and, where they are gathered, their rows,
+// which spares the second one the search, and h by 16 rows in the order of the second
+// product's operand: [tile][16 rows][part][step][lane][8].
 constexpr int kTileRows = 32;
 constexpr int kTiles16 = kTileRows / 16;
 constexpr int kUpWaves = 2;    // tiles of a workgroup
 constexpr int kUpGridRows = 32768;
 
-template <typename XT, typename YT, int MT>
+template <typename XT, typename YT, int MT, bool LISTED>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
   using D = Down<XT, MT, kTiles16>;
   constexpr int HP = h_parts<YT>(), RS = (MT + 1) / 2;
   __shared__ __align__(16) char s_wave[kWaves * D::kBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int row0 = 0, row1 = 0, request, m = -1;
-  if (find_tile(g, blockIdx.x, kTileRows, row0, row1, request)) m = adapter_of(g, request);
-  if (m >= g.n_adapters) m = -1;
-  if (tid == 0) g.tiles[blockIdx.x] = make_int4(row0, row1, m, 0);
+  Rows<LISTED> rows{0, 0, nullptr};
+  int m = -1;
+  if constexpr (LISTED) {
+    __shared__ TogetherShared<kTileRows> s_rows;
+    const bool found = tile_rows(g, s_rows, rows, m);
+    if (tid < kTileRows)   // rows past the end re-read the last one
+      g.lists[blockIdx.x * kTileRows + tid] = found ? rows.held(tid) : 0;
+  } else {
+    tile_rows<kTileRows>(g, rows, m);
+  }
+  if (tid == 0) g.tiles[blockIdx.x] = make_int4(rows.row0, rows.n, m, 0);
   if (m < 0) return;
   const float scale = g.scale ? g.scale[m] : 1.0f;
   for (int pass = 0; pass < MT / D::kRanks; ++pass) {
     if (pass) __syncthreads();   // the sums have been read
-    down_product<XT, MT, kTiles16>(g, m, Rows<false>{row0, row1 - row0, nullptr}, pass, s_wave + wave * D::kBytes);
+    down_product<XT, MT, kTiles16>(g, m, rows, pass, s_wave + wave * D::kBytes);
     __syncthreads();
     constexpr int kSteps = (D::kRanks + 1) / 2;
     if (wave < kSteps * kTiles16) {
@@ -701,7 +732,7 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
 // with one, two, three, four and eight tiles: 29.4, 28.2, 27.7, 28.6 and 38.9 us for
 // both launches).  B goes through LDS for all of them, adapter by adapter where the
 // tiles' requests have different ones.
-template <typename YT, int RS>
+template <typename YT, int RS, bool LISTED>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   constexpr int HP = h_parts<YT>();
   using B = BRows<RS, kGroup, 64 * kUpWaves>;
@@ -712,7 +743,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   const int c = blockIdx.x * kGroup, tile0 = (blockIdx.z * kUpGridRows + blockIdx.y) * kUpWaves;
   const int tile = tile0 + wave;
   const int4 mine = tile < g.n_tiles ? g.tiles[tile] : make_int4(0, 0, -1, 0);
-  const Rows<false> rows{mine.x, mine.y - mine.x, nullptr};
+  const Rows<LISTED> rows{mine.x, mine.y, LISTED ? g.lists + min(tile, g.n_tiles - 1) * kTileRows : nullptr};
   const int m = mine.z;
   int all[kUpWaves];   // the tiles' adapters
 #pragma unroll
@@ -743,7 +774,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
       for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
   YRows<YT, kGroup> yr[kTiles16];
 #pragma unroll
-  for (int j = 0; j < kTiles16; ++j) yr[j].load(g, rows.from(16 * j), c);
+  for (int j = 0; j < kTiles16; ++j) yr[j].template load<LISTED>(g, rows.from(16 * j), c);
   bool first = true;
   for (int w = 0; w < kUpWaves; ++w) {
     who = all[w];
@@ -783,32 +814,23 @@ int most_tiles(int64_t T, int n_seq, int rows) {
   return static_cast<int>((T + (rows - 1) * std::min(static_cast<int64_t>(n_seq), T)) / rows);
 }
 
-// Requests beyond the number of adapters from which rows of one adapter share a
-// workgroup: that many tiles at least are spared, for some 2 us of gathering (a row
-// for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
-// 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
-// 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
-// 280 against 38 and 448 against 64).
-constexpr int kTogether = 64;
-
-// Their offsets into x have 32 bits.
-bool gathers(int64_t T, int n_seq, int n_adapters, int64_t row_bytes) {
-  return n_seq >= n_adapters + kTogether && T * row_bytes < (int64_t{1} << 32) - (1 << 17);
-}
-
 template <typename XT, typename YT, int MT>
 hipError_t launch_rank(LoraArgs g, hipStream_t s) {
   const int groups = (g.d_out + kGroup - 1) / kGroup;
   if (g.h) {
-    lora_down_kernel<XT, YT, MT><<<g.n_tiles, kThreads, 0, s>>>(g);
     const int rows = (g.n_tiles + kUpWaves - 1) / kUpWaves;
     const dim3 grid(groups, min(rows, kUpGridRows), (rows + kUpGridRows - 1) / kUpGridRows);
-    lora_up_kernel<YT, (MT + 1) / 2><<<grid, 64 * kUpWaves, 0, s>>>(g);
+    if (g.together) {
+      lora_down_kernel<XT, YT, MT, true><<<g.n_tiles, kThreads, 0, s>>>(g);
+      lora_up_kernel<YT, (MT + 1) / 2, true><<<grid, 64 * kUpWaves, 0, s>>>(g);
+    } else {
+      lora_down_kernel<XT, YT, MT, false><<<g.n_tiles, kThreads, 0, s>>>(g);
+      lora_up_kernel<YT, (MT + 1) / 2, false><<<grid, 64 * kUpWaves, 0, s>>>(g);
+    }
     return hipGetLastError();
   }
   // about a workgroup per CU: slices of the columns while there are few tiles (one
   // row, 1,536 columns in 3 slices 7.4 us, in 24 6.4; 64 rows in 3 5.9, in 24 6.7)
-  g.together = gathers(g.T, g.n_seq, g.n_adapters, int64_t{g.d_in} * sizeof(XT));
   const int64_t tiles = g.together ? most_tiles(g.T, g.n_adapters + 1, 16)
                                    : g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
   const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / tiles)));
@@ -831,19 +853,35 @@ hipError_t launch_as(const LoraArgs& g, hipStream_t s) {
 // against 15.0; 2,048 rows 12.5 against 12.1 and 19.5 against 16.3).
 constexpr int64_t kManyRows = 1024;
 
-// Rows per request below which, if they can be gathered, one launch is made all the
-// same: its tiles are full where the others' hold one request each (48 adapters,
-// rank 64, bfloat16, gathered against two launches: 1,000 requests of 2 rows 28
-// against 78 us, 500 of 1 to 7 28 against 43, 8,000 rows in 500 62 against 57, 4,000
-// in 200 38 against 30).
-constexpr int64_t kShortRows = 16;
+// The same for gathered rows (one launch against two, bfloat16, rank 64, 48 adapters:
+// a row for every request, 1,024 rows 19.2 against 18.7 us, with 4 adapters 14.4
+// against 17.0; 2,048 rows 24.7 against 22.2; 8,192 rows 67 against 53; 1,000 requests
+// of two rows 25.7 against 21.8; 512 single rows beside a prompt of 8,192 61 against 38).
+constexpr int64_t kManyGathered = 1536;
+
+// Requests beyond the number of adapters from which rows of one adapter share a
+// workgroup: that many tiles at least are spared, for some 2 us of gathering (a row
+// for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
+// 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
+// 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
+// 280 against 37 and 448 against 53; where rows fill their tiles anyhow, 256 requests
+// of 8,000 rows, 42 against 41 and in fp32 64 against 67).
+constexpr int kTogether = 64;
+
+// Their offsets into x have 32 bits.
+bool gathers(int64_t T, int n_seq, int n_adapters, int64_t row_bytes) {
+  return n_seq >= n_adapters + kTogether && T * row_bytes < (int64_t{1} << 32) - (1 << 17);
+}
 
 }  // namespace
 
+// n_seq = 0: a row for every request; then there are two launches only with gathered
+// rows, of at most MOE_MAX_EXPERTS adapters and those without one.
 size_t lora_workspace_bytes(int64_t T, int rank, int n_seq) {
-  if (n_seq == 0 || T < kManyRows) return 0;   // n_seq = 0: a row for every request
-  const int64_t tiles = most_tiles(T, n_seq, kTileRows), steps = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
-  return static_cast<size_t>(align256(tiles * 16) + tiles * kTiles16 * 3 * steps * 1024);
+  if (T < kManyRows || (n_seq == 0 && T > 65536)) return 0;
+  const int64_t tiles = most_tiles(T, n_seq ? n_seq : MOE_MAX_EXPERTS + 1, kTileRows);
+  const int64_t steps = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
+  return static_cast<size_t>(align256(tiles * 16) + tiles * kTileRows * 4 + tiles * kTiles16 * 3 * steps * 1024);
 }
 
 hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,
@@ -851,13 +889,15 @@ hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, 
                        const int32_t* seq, int n_seq, const int32_t* adapter, const float* scale,
                        void* y, int y_dtype, void* ws, hipStream_t s) {
   LoraArgs g{base, x, a, b, seq, adapter, scale, y, static_cast<int>(T),
-             d_in, d_out, n_adapters, rank, n_seq, 0, 0, nullptr, nullptr, 0};
-  const bool short_requests = T / kShortRows < n_seq &&
-                              gathers(T, n_seq, n_adapters, int64_t{d_in} * (x_dtype == MOE_DTYPE_F32 ? 4 : 2));
-  if (lora_workspace_bytes(T, rank, seq ? n_seq : 0) > 0 && !short_requests) {
-    g.n_tiles = most_tiles(T, n_seq, kTileRows);
-    g.tiles = static_cast<int4*>(ws);
-    g.h = reinterpret_cast<nu4*>(static_cast<char*>(ws) + align256(int64_t{g.n_tiles} * 16));
+             d_in, d_out, n_adapters, rank, n_seq, 0, 0, nullptr, nullptr, nullptr, 0};
+  g.together = gathers(T, n_seq, n_adapters, int64_t{d_in} * (x_dtype == MOE_DTYPE_F32 ? 4 : 2));
+  if (g.together ? T >= kManyGathered : seq && T >= kManyRows) {
+    g.n_tiles = most_tiles(T, g.together ? n_adapters + 1 : n_seq, kTileRows);
+    char* at = static_cast<char*>(ws);
+    g.tiles = reinterpret_cast<int4*>(at);
+    at += align256(int64_t{g.n_tiles} * 16);
+    g.lists = reinterpret_cast<int*>(at);
+    g.h = reinterpret_cast<nu4*>(at + int64_t{g.n_tiles} * kTileRows * 4);
   }
   const bool xf = x_dtype == MOE_DTYPE_F32, yf = y_dtype == MOE_DTYPE_F32;
   const auto f = xf ? (yf ? launch_as<float, float> : launch_as<float, uint16_t>)

@@ -309,3 +309,21 @@ def test_gathered_rows_of_one_long_and_many_short_requests():
     y = _check(base, x, a, b, who, bounds, scale)
     one = bf.lora(base[75:775].clone(), x[75:775].clone(), a, b, _i32(who[75:76]), seq_offsets=_i32([0, 700]), scale=scale)
     assert torch.equal(one, y[75:775])
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rank,d_in,d_out", [(8, 96, 80), (40, 160, 144), (72, 64, 336), (128, 288, 64)])
+def test_gathered_rows_beside_a_prompt(rank, d_in, d_out, types):
+    """Many rows in two launches, gathered: single rows on both sides of a prompt whose
+    adapter others share, rows without one, and the result in place of base."""
+    bf = _bf()
+    n, singles, prompt = 5, 190, 1500
+    T = 2 * singles + prompt
+    base, x, a, b, scale = _inputs(T, n, rank, d_in, d_out, *types)
+    bounds = np.concatenate([np.arange(singles + 1), singles + prompt + np.arange(singles + 1)])
+    who = np.random.default_rng(rank).integers(-1, n + 1, len(bounds) - 1)
+    who[singles] = 2
+    y = _check(base, x, a, b, who, bounds, scale)
+    into = base.clone()
+    bf.lora(into, x, a, b, _i32(who), seq_offsets=_i32(bounds), scale=scale, y=into)
+    assert torch.equal(into, y)
