@@ -192,23 +192,48 @@ struct TogetherShared {
   int list[ROWS];
 };
 
-// The rows of 64 requests from s on, one per lane: the first, and how many; requests
-// from s1 on have none.  low: the largest bound so far.
-__device__ __forceinline__ void request_rows(const LoraArgs& g, int s, int s1, int& low, int& start, int& n) {
+// Requests of a wavefront whose adapters and bounds are asked for at a time; if it
+// has no more, they are kept (8,192 rows that are requests, rank 64, 48 adapters, two
+// launches: one at a time 53.8 us, four 49.9, eight 49.5, sixteen, then kept, 48.0;
+// eight in one launch of few rows cost 1 us).
+template <int BATCH>
+struct Requests {
+  int id[BATCH], bound[BATCH];
+};
+
+// f(bucket, first row, number of rows), one request per lane, for the requests
+// [s0, s1), in order, until it is false; requests from s1 on have no rows.  low: the
+// largest bound before s0.  kept: q has them.
+template <int BATCH, typename F>
+__device__ __forceinline__ void for_requests(const LoraArgs& g, Requests<BATCH>& q, bool kept, int s0, int s1,
+                                             int low, F f) {
   const int lane = threadIdx.x & 63;
-  if (!g.seq) {
-    start = s + lane;
-    n = start < s1;
-    return;
+  for (int s = s0; s < s1; s += 64 * BATCH) {
+    if (!kept) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) q.id[j] = g.adapter[min(s + 64 * j + lane, g.n_seq - 1)];
+      if (g.seq) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) q.bound[j] = g.seq[min(s + 64 * j + lane, g.n_seq - 1) + 1];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int r = s + 64 * j + lane;
+      if (s + 64 * j >= s1) return;   // uniform
+      int start = r, n = r < s1;
+      if (g.seq) {
+        const int upto = wave_scan_max(r < s1 ? min(max(q.bound[j], 0), g.T) : 0);
+        start = max(low, lane_before(upto));
+        n = max(low, upto) - start;
+        low = max(low, lane_value(upto, 63));
+      }
+      if (!f(q.id[j] >= 0 && q.id[j] < g.n_adapters ? q.id[j] : g.n_adapters, start, n)) return;   // uniform
+    }
   }
-  const int bound = s + lane < s1 ? min(max(g.seq[s + lane + 1], 0), g.T) : 0;
-  const int upto = wave_scan_max(bound), end = max(low, upto);
-  start = max(low, lane_before(upto));
-  n = end - start;
-  low = max(low, lane_value(upto, 63));
 }
 
-template <int ROWS>
+template <int ROWS, int BATCH = ROWS == 16 ? 2 : 16>
 __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, TogetherShared<ROWS>& sh, int& m,
                                               int& rows) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -228,16 +253,12 @@ __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, Toget
   __syncthreads();
   if (g.seq)
     for (int w = 0; w < wave; ++w) low = max(low, sh.wave[0][w]);
-  const auto bucket = [&](int s) {
-    const int id = g.adapter[min(s + lane, g.n_seq - 1)];
-    return id >= 0 && id < g.n_adapters ? id : g.n_adapters;
-  };
-  int upto = low, start, n;
-  for (int s = s0; s < s1; s += 64) {
-    const int b = bucket(s);
-    request_rows(g, s, s1, upto, start, n);
+  Requests<BATCH> q;
+  const bool keep = part <= 64 * BATCH;
+  for_requests(g, q, false, s0, s1, low, [&](int b, int, int n) {
     if (n > 0) atomicAdd(&sh.count[b], n);
-  }
+    return true;
+  });
   __syncthreads();
   constexpr int kPer = (MOE_MAX_EXPERTS + kThreads) / kThreads;   // buckets of a thread
   int tiles[kPer], sum = 0;
@@ -264,26 +285,22 @@ __device__ __forceinline__ bool find_together(const LoraArgs& g, int tile, Toget
   const int who = sh.who;
   if (who < 0) return false;   // uniform
   int mine = 0;
-  upto = low;
-  for (int s = s0; s < s1; s += 64) {
-    const int b = bucket(s);
-    request_rows(g, s, s1, upto, start, n);
+  for_requests(g, q, keep, s0, s1, low, [&](int b, int, int n) {
     mine += b == who ? n : 0;
-  }
+    return true;
+  });
   mine = lane_value(wave_scan_add(mine), 63);
   if (lane == 0) sh.wave[0][wave] = mine;   // last read before two barriers
   __syncthreads();
   int at = -ROWS * sh.nth;   // place of the next row found among the tile's
   for (int w = 0; w < wave; ++w) at += sh.wave[0][w];
-  upto = low;
-  for (int s = s0; s < s1 && at < ROWS; s += 64) {
-    const int b = bucket(s);
-    request_rows(g, s, s1, upto, start, n);
+  for_requests(g, q, keep, s0, s1, low, [&](int b, int start, int n) {
     if (b != who) n = 0;
     const int end = at + wave_scan_add(n), first = end - n;
     for (int place = max(first, 0); place < min(end, ROWS); ++place) sh.list[place] = start + place - first;
     at = lane_value(end, 63);
-  }
+    return at < ROWS;
+  });
   rows = min(ROWS, sh.count[who] - ROWS * sh.nth);
   __syncthreads();
   m = who < g.n_adapters ? who : -1;
@@ -340,13 +357,15 @@ __device__ __forceinline__ nu4 get_chunk(const char* lds, int row, int chunk) {
   return *reinterpret_cast<const nu4*>(lds + 128 * row + 16 * (chunk ^ (row & 7)));
 }
 
-// Shared memory of one wavefront, in its three uses.
+// Shared memory of one wavefront, in its three uses: x, then A, then the sums (A beside
+// x would leave fp32 one workgroup per CU: 8,192 rows that are requests, rank 16, 48
+// adapters, 305 workgroups, 76 us instead of 61).
 template <typename XT, int MT, int NT>
 struct Down {
   static constexpr int kUnits = sizeof(XT) / 2;   // of x, for 64 columns
   static constexpr int kRanks = MT < 4 ? MT : 4;  // 16-rank tiles of a pass
   static constexpr int kPartRow = 16 * kRanks + 4;
-  static constexpr int kStage = (NT * kUnits + 2) * kUnitBytes;
+  static constexpr int kStage = std::max(NT * kUnits, 2) * kUnitBytes;
   static constexpr int kPart = 16 * NT * kPartRow * 4;
   static constexpr int kBytes = kStage > kPart ? kStage : kPart;
   // 64-column units asked for at a time
@@ -374,8 +393,6 @@ __device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Row
   for (int i = 0; i < MP; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = nf4{0.0f, 0.0f, 0.0f, 0.0f};
-  char* xs = lds;
-  char* as = lds + NT * XU * kUnitBytes;
   const int units = (g.d_in + 63) / 64;
   for (int u0 = wave; u0 < units; u0 += kWaves * U) {
     nu4 av[U][MP][2], xv[U][NT][XU][2];
@@ -408,21 +425,22 @@ __device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Row
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int w = 0; w < XU; ++w) put_unit(xs + (j * XU + w) * kUnitBytes, xv[n][j][w]);
+        for (int w = 0; w < XU; ++w) put_unit(lds + (j * XU + w) * kUnitBytes, xv[n][j][w]);
         wave_order();
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           nu4 v[XU];
 #pragma unroll
           for (int w = 0; w < XU; ++w)
-            v[w] = XU == 1 ? get_chunk(xs + j * kUnitBytes, l16, 4 * s + quad)
-                           : get_chunk(xs + (j * XU + s) * kUnitBytes, l16, 2 * quad + w);
+            v[w] = XU == 1 ? get_chunk(lds + j * kUnitBytes, l16, 4 * s + quad)
+                           : get_chunk(lds + (j * XU + s) * kUnitBytes, l16, 2 * quad + w);
           XParts<XT>::split(v, xp[s][j]);
         }
       }
 #pragma unroll
       for (int i = 0; i < MP; ++i) {
-        char* at = as + (i & 1) * kUnitBytes;
+        char* at = lds + (i & 1) * kUnitBytes;   // x has been read
+        wave_order();
         put_unit(at, av[n][i]);
         wave_order();
 #pragma unroll
@@ -855,7 +873,7 @@ constexpr int64_t kManyRows = 1024;
 
 // The same for gathered rows (one launch against two, bfloat16, rank 64, 48 adapters:
 // a row for every request, 1,024 rows 19.2 against 18.7 us, with 4 adapters 14.4
-// against 17.0; 2,048 rows 24.7 against 22.2; 8,192 rows 67 against 53; 1,000 requests
+// against 17.0; 2,048 rows 24.7 against 21.3; 8,192 rows 67 against 48; 1,000 requests
 // of two rows 25.7 against 21.8; 512 single rows beside a prompt of 8,192 61 against 38).
 constexpr int64_t kManyGathered = 1536;
 
@@ -864,7 +882,7 @@ constexpr int64_t kManyGathered = 1536;
 // for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
 // 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
 // 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
-// 280 against 37 and 448 against 53; where rows fill their tiles anyhow, 256 requests
+// 280 against 32 and 448 against 48; where rows fill their tiles anyhow, 256 requests
 // of 8,000 rows, 42 against 41 and in fp32 64 against 67).
 constexpr int kTogether = 64;
 
