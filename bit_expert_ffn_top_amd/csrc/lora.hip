@@ -3,10 +3,9 @@
 //
 // Both products are on the matrix cores, with the adapter's rows as the first
 // operand:
-//   h = A x    16 or 32 consecutive rows of one request, or 16 of one adapter
-//              gathered from many short requests; the eight wavefronts of a
-//              workgroup split the columns, and their sums meet in LDS in a fixed
-//              order
+//   h = A x    16 or 32 consecutive rows of one request, or as many of one adapter
+//              gathered from many requests; the eight wavefronts of a workgroup
+//              split the columns, and their sums meet in LDS in a fixed order
 //   y = B h    64 columns per wavefront
 // Few rows: both in one launch.  A workgroup repeats h for its slice of y's
 // columns; A is small (64 KB at rank 16 and 2048 columns), and a second launch
@@ -15,7 +14,7 @@
 // Operands are read as their rows lie and change lanes in LDS: read directly, an
 // operand's layout has 16 bytes of each of 16 rows in a quarter of a wavefront,
 // sixteen cache lines where four would do (8,192 rows at rank 64, two launches: 50 us
-// where this takes 28).  y leaves the same way.
+// where this takes 26).  y leaves the same way.
 // Measured (2,048 columns in and out, bfloat16): 8,192 rows of eight requests, rank
 // 64, 101 MB of x, base and y: 13.1 + 16.2 us, 20 at a copy's rate; what is left is
 // each workgroup's chain of loads, LDS and products.  64 rows with an adapter each,
@@ -601,11 +600,11 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& g, int request) {
   return __builtin_amdgcn_readfirstlane(g.adapter[request]);
 }
 
-// The rows and adapter (-1: none) of the workgroup's tile, of one request.
+// The rows and adapter (-1: none) of a tile, of one request.
 template <int ROWS, bool LISTED>
-__device__ __forceinline__ bool tile_rows(const LoraArgs& g, Rows<LISTED>& rows, int& m) {
+__device__ __forceinline__ bool tile_rows(const LoraArgs& g, int tile, Rows<LISTED>& rows, int& m) {
   int row1, request;
-  if (!find_tile(g, blockIdx.x, ROWS, rows.row0, row1, request)) return false;
+  if (!find_tile(g, tile, ROWS, rows.row0, row1, request)) return false;
   rows.n = row1 - rows.row0;
   m = adapter_of(g, request);
   if (m >= g.n_adapters) m = -1;
@@ -614,9 +613,10 @@ __device__ __forceinline__ bool tile_rows(const LoraArgs& g, Rows<LISTED>& rows,
 
 // The same of gathered rows.
 template <int ROWS>
-__device__ __forceinline__ bool tile_rows(const LoraArgs& g, TogetherShared<ROWS>& sh, Rows<true>& rows, int& m) {
+__device__ __forceinline__ bool tile_rows(const LoraArgs& g, int tile, TogetherShared<ROWS>& sh, Rows<true>& rows,
+                                          int& m) {
   rows.list = sh.list;
-  if (!find_together<ROWS>(g, blockIdx.x, sh, m, rows.n)) return false;
+  if (!find_together<ROWS>(g, tile, sh, m, rows.n)) return false;
   m = __builtin_amdgcn_readfirstlane(m);
   return true;
 }
@@ -639,9 +639,9 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   Rows<true> rows{0, 0, s_rows.list};
   int m = -1;
   if (g.together) {
-    if (!tile_rows(g, s_rows, rows, m)) return;
+    if (!tile_rows(g, blockIdx.x, s_rows, rows, m)) return;
   } else {
-    if (!tile_rows<16>(g, rows, m)) return;
+    if (!tile_rows<16>(g, blockIdx.x, rows, m)) return;
     if (tid < 16) s_rows.list[tid] = tid;
     __syncthreads();
   }
@@ -710,23 +710,35 @@ constexpr int kTiles16 = kTileRows / 16;
 constexpr int kUpWaves = 2;    // tiles of a workgroup
 constexpr int kUpGridRows = 32768;
 
+// Workgroups go to the eight XCDs in turn: four tiles that follow each other, which
+// mostly share an adapter, go to one, whose L2 cache then reads it once (8,192 rows,
+// rank 64, two launches, with 1, 4, 8 and all n / 8 tiles: eight prompts 26.8, 26.1,
+// 26.8 and 29.0 us; single rows, 48 adapters, 47.6, 43.0, 42.2 and 47.3, 4 adapters
+// 32.2, 32.8, 33.7 and 37.2).
+__device__ __forceinline__ int tile_of(int block, int n) {
+  constexpr int kRun = 4, kTurn = 8 * kRun;
+  const int i = block % kTurn, first = block - i;
+  return first + kTurn <= n ? first + i % 8 * kRun + i / 8 : block;
+}
+
 template <typename XT, typename YT, int MT, bool LISTED>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
   using D = Down<XT, MT, kTiles16>;
   constexpr int HP = h_parts<YT>(), RS = (MT + 1) / 2;
   __shared__ __align__(16) char s_wave[kWaves * D::kBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tile = tile_of(blockIdx.x, gridDim.x);
   Rows<LISTED> rows{0, 0, nullptr};
   int m = -1;
   if constexpr (LISTED) {
     __shared__ TogetherShared<kTileRows> s_rows;
-    const bool found = tile_rows(g, s_rows, rows, m);
+    const bool found = tile_rows(g, tile, s_rows, rows, m);
     if (tid < kTileRows)   // rows past the end re-read the last one
-      g.lists[blockIdx.x * kTileRows + tid] = found ? rows.held(tid) : 0;
+      g.lists[tile * kTileRows + tid] = found ? rows.held(tid) : 0;
   } else {
-    tile_rows<kTileRows>(g, rows, m);
+    tile_rows<kTileRows>(g, tile, rows, m);
   }
-  if (tid == 0) g.tiles[blockIdx.x] = make_int4(rows.row0, rows.n, m, 0);
+  if (tid == 0) g.tiles[tile] = make_int4(rows.row0, rows.n, m, 0);
   if (m < 0) return;
   const float scale = g.scale ? g.scale[m] : 1.0f;
   for (int pass = 0; pass < MT / D::kRanks; ++pass) {
@@ -739,7 +751,7 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
       nu4 h[HP];
       join_sums<D, HP, D::kBytes>(s_wave, 16 * part16 + (lane & 15), 32 * step + 8 * (lane >> 4),
                                   min(g.rank - 64 * pass, 16 * D::kRanks), scale, h);
-      nu4* out = g.h + (static_cast<int64_t>(blockIdx.x) * kTiles16 + part16) * (HP * RS * 64) + lane;
+      nu4* out = g.h + (static_cast<int64_t>(tile) * kTiles16 + part16) * (HP * RS * 64) + lane;
 #pragma unroll
       for (int p = 0; p < HP; ++p) out[(p * RS + 2 * pass + step) * 64] = h[p];
     }
@@ -873,8 +885,8 @@ constexpr int64_t kManyRows = 1024;
 
 // The same for gathered rows (one launch against two, bfloat16, rank 64, 48 adapters:
 // a row for every request, 1,024 rows 19.2 against 18.7 us, with 4 adapters 14.4
-// against 17.0; 2,048 rows 24.7 against 21.3; 8,192 rows 67 against 48; 1,000 requests
-// of two rows 25.7 against 21.8; 512 single rows beside a prompt of 8,192 61 against 38).
+// against 17.0; 2,048 rows 24.7 against 21.3; 8,192 rows 67 against 43; 1,000 requests
+// of two rows 25.7 against 21.3; 512 single rows beside a prompt of 8,192 61 against 38).
 constexpr int64_t kManyGathered = 1536;
 
 // Requests beyond the number of adapters from which rows of one adapter share a
@@ -882,8 +894,8 @@ constexpr int64_t kManyGathered = 1536;
 // for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
 // 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
 // 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
-// 280 against 32 and 448 against 48; where rows fill their tiles anyhow, 256 requests
-// of 8,000 rows, 42 against 41 and in fp32 64 against 67).
+// 280 against 33 and 448 against 43; where rows fill their tiles
+// anyhow, 8,000 rows of 256 requests, the two are even).
 constexpr int kTogether = 64;
 
 // Their offsets into x have 32 bits.
