@@ -539,18 +539,21 @@ struct BRows {
   }
 };
 
-// A wavefront's 16 rows of COLS columns of base and y as they lie: a lane holds
-// eight columns of each of kLoads rows.
-template <typename YT, int COLS>
+// A wavefront's 16 rows of COLS columns of base and y as they lie: a lane holds kN
+// columns of each of kLoads rows.  Eight fp32 columns are two stores that leave gaps,
+// and 7% of what they write goes out twice: 8,192 rows of eight prompts, rank 64, with
+// eight and four 53.7 and 50.8 us.  Few rows are better off with eight (one row 6.5
+// against 6.7 us, 512 rows, rank 64, 13.9 against 14.3).
+template <typename YT, int COLS, int kN>
 struct YRows {
-  static constexpr int kPerRow = COLS / 8, kRows = 64 / kPerRow, kLoads = 16 / kRows;
-  RowPart<YT, 8> v[kLoads];
+  static constexpr int kPerRow = COLS / kN, kRows = 64 / kPerRow, kLoads = 16 / kRows;
+  RowPart<YT, kN> v[kLoads];
   // Rows and columns past the end re-read the last ones: no load depends on a
   // comparison, so that waiting for one need not be waiting for all.  ALL: the list
   // has 16 rows, whatever their number.
   template <bool ALL = false, bool LISTED>
   __device__ __forceinline__ void load(const LoraArgs& g, const Rows<LISTED>& rows, int c) {
-    const int lane = threadIdx.x & 63, col = min(c + 8 * (lane % kPerRow), g.d_out - 8);
+    const int lane = threadIdx.x & 63, col = min(c + kN * (lane % kPerRow), g.d_out - kN);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
       const int i = n * kRows + lane / kPerRow;
@@ -563,17 +566,20 @@ struct YRows {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
-      const nf4* d = reinterpret_cast<const nf4*>(lds + (n * kRows + lane / kPerRow) * (COLS + 4) + 8 * (lane % kPerRow));
-      const nf4 lo = d[0], hi = d[1];
-      float f[8];
+      const nf4* d = reinterpret_cast<const nf4*>(lds + (n * kRows + lane / kPerRow) * (COLS + 4) +
+                                                  kN * (lane % kPerRow));
+      nf4 r[kN / 4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = v[n].get(e) + (e < 4 ? lo[e % 4] : hi[e % 4]);
+      for (int e = 0; e < kN / 4; ++e) r[e] = d[e];
+      float f[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) f[e] = v[n].get(e) + r[e / 4][e % 4];
       v[n].set(f);
     }
   }
   template <bool LISTED>
   __device__ __forceinline__ void store(const LoraArgs& g, const Rows<LISTED>& rows, int c) const {
-    const int lane = threadIdx.x & 63, col = c + 8 * (lane % kPerRow);
+    const int lane = threadIdx.x & 63, col = c + kN * (lane % kPerRow);
 #pragma unroll
     for (int n = 0; n < kLoads; ++n) {
       const int t = n * kRows + lane / kPerRow;
@@ -657,7 +663,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   const int k0 = min(blocks, wave * per), k1 = min(blocks, k0 + per);
   // the first block's rows of B and base are on their way meanwhile
   B bl;
-  YRows<YT, kCols> yr;
+  YRows<YT, kCols, 8> yr;
   if (k0 < k1) {
     bl.load(g, b, n0 + k0 * kCols, lane);
     yr.load(g, rows, n0 + k0 * kCols);
@@ -802,7 +808,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
     for (int p = 0; p < HP; ++p)
 #pragma unroll
       for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
-  YRows<YT, kGroup> yr[kTiles16];
+  YRows<YT, kGroup, 16 / sizeof(YT)> yr[kTiles16];
 #pragma unroll
   for (int j = 0; j < kTiles16; ++j) yr[j].template load<LISTED>(g, rows.from(16 * j), c);
   bool first = true;
