@@ -5,8 +5,8 @@
 //   drows[pos] = w dy[t]      dw = <dy[t], rows[pos]>
 // Nothing is computed to speak of; HBM bounds all of it where there are many
 // tokens, launches and dependent loads where there are few.  A chunk of 8,192
-// tokens x 10 pairs of 2,048 bfloat16 columns (335 MB of rows): dispatch 5.3 us for
-// the counts + 74 us (4.9 TB/s), its gradient and the combine 62 and 64 us (5.9 and
+// tokens x 10 pairs of 2,048 bfloat16 columns (335 MB of rows): dispatch 4.8 us for
+// the counts + 72 us (5.0 TB/s), its gradient and the combine 62 and 64 us (5.9 and
 // 6.2 TB/s), the combine's gradients 143 us (4.9 TB/s).  Rows are streamed past the
 // caches in both directions: they are more than these hold (plain stores and loads:
 // dispatch 94 us, combine 84 us).
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a
 // that an earlier launch counted, and counts what its own part holds before its
 // tokens.  Ranks among its own pairs are counted directly, which keeps equal ids
 // of a token in order.  Then it reads its tokens' rows once and writes each to
-// its k places.  64 tokens x 10 pairs: 5.6 us, most of it the chain of counting,
+// its k places.  64 tokens x 10 pairs: 5.4 us, most of it the chain of counting,
 // scanning and ranking.
 template <typename V, bool COUNTED>   // V: the part of a row that one lane moves
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(DispatchArgs a) {

@@ -16,9 +16,10 @@
 // sixteen cache lines where four would do (8,192 rows at rank 64, two launches: 50 us
 // where this takes 26).  y leaves the same way.
 // Measured (2,048 columns in and out, bfloat16): 8,192 rows of eight requests, rank
-// 64, 101 MB of x, base and y: 13.1 + 16.2 us, 20 at a copy's rate; what is left is
-// each workgroup's chain of loads, LDS and products.  64 rows with an adapter each,
-// rank 16, 1,536 columns out: 6.4 us, one fp32 row 6.9, that chain alone.
+// 64, 101 MB of x, base and y: 13.1 + 14.9 us, 26 in a row of calls, 20 at a copy's
+// rate; what is left is each workgroup's chain of loads, LDS and products.  64 rows
+// with an adapter each, rank 16, 1,536 columns out: 6.5 us, one fp32 row 6.9, that
+// chain alone.
 // fp32 values enter as sums of bfloat16 parts: x as three (exact but for its
 // smallest values), h as two where the results are bfloat16 (off by 2^-16 of it,
 // where they round by 2^-8) and three where they are fp32.  A row has the same
