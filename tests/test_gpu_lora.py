@@ -327,3 +327,16 @@ def test_gathered_rows_beside_a_prompt(rank, d_in, d_out, types):
     into = base.clone()
     bf.lora(into, x, a, b, _i32(who), seq_offsets=_i32(bounds), scale=scale, y=into)
     assert torch.equal(into, y)
+
+
+@pytest.mark.parametrize("T,S", [(1000, 5000), (1000, 65536), (3000, 20000), (40000, 12000), (40000, 65536)])
+def test_more_requests_than_are_looked_at_at_once(T, S):
+    """Gathered rows of many requests, most of them without a row where they are more
+    than the rows, some bounds out of order."""
+    n = 7
+    base, x, a, b, scale = _inputs(T, n, 8, 32, 16, BF16, F32)
+    rng = np.random.default_rng(S)
+    bounds = np.sort(rng.integers(0, T + 1, S + 1))
+    at = rng.integers(0, S + 1, S // 20)
+    bounds[at] = rng.integers(0, T // 2, len(at))
+    _check(base, x, a, b, rng.integers(-1, n + 1, S), bounds, scale)
