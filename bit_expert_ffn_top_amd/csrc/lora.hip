@@ -80,7 +80,9 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
 template <>
 struct XParts<float> {
   static constexpr int kParts = 3;
-  // Each part takes the highest eight bits that are left: 24 in all.
+  // Each part takes the highest eight bits that are left: 24 in all.  An infinity is
+  // whole in its first part and leaves nothing (a difference would be NaN); a NaN
+  // whose high half is an infinity's leaves one.
   static __device__ __forceinline__ void split(const nu4 (&v)[2], nu4 (&out)[3]) {
     uint32_t r[8];
 #pragma unroll
@@ -90,9 +92,12 @@ struct XParts<float> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[part][i] = high_halves(r[2 * i], r[2 * i + 1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, r[i]) -
-                                                __builtin_bit_cast(float, r[i] & 0xFFFF0000u));
+      for (int i = 0; i < 8; ++i) {
+        const float v = __builtin_bit_cast(float, r[i]);
+        const float left = v - __builtin_bit_cast(float, r[i] & 0xFFFF0000u);
+        // what is left of a finite value is finite
+        r[i] = __builtin_bit_cast(uint32_t, part == 0 && __builtin_isinf(v) ? 0.0f : left);
+      }
     }
   }
 };

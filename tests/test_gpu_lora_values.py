@@ -1,0 +1,69 @@
+"""GPU tests of values that a product of parts can get wrong: infinities and NaN of
+x.  Every form of the call: few rows, many rows, and both of gathered rows.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.lora as ol
+from parity import need_gpu
+from test_gpu_lora import BF16, F32, TYPES, _bf, _bound, _i32, _inputs, _np
+
+pytestmark = pytest.mark.gpu
+
+# rows, bounds of the requests (None: a row for each)
+FORMS = {"few": (20, [0, 12, 20]), "gathered": (200, None), "many": (1100, [0, 600, 1100]),
+         "many gathered": (1600, None)}
+
+
+def _form(name):
+    """(T, bounds, the adapter of every request, that of every row), two adapters."""
+    T, seq = FORMS[name]
+    who = np.arange(T if seq is None else len(seq) - 1) % 2
+    return T, seq, who, who if seq is None else np.repeat(who, np.diff(seq))
+
+
+def _call(form, base, x, a, b, scale=None):
+    _, seq, who, _ = _form(form)
+    return _bf().lora(base, x, a, b, _i32(who), seq_offsets=None if seq is None else _i32(seq), scale=scale)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("form", FORMS)
+def test_infinities_are_the_formulas(form, types):
+    """An infinity in x gives the infinities and NaN that the formula gives in 64
+    bits, whatever parts its type enters as: a column of A of one sign, rows of B of
+    one sign (infinite results) and of both (NaN), infinities of both signs in a row,
+    an infinity times zero, a NaN whose high half is an infinity's."""
+    T, seq, who, of = _form(form)
+    base, x, a, b, scale = _inputs(T, 2, 16, 96, 48, *types)
+    a[:, :, 13] = a[:, :, 13].abs() + 0.5
+    a[:, :, 70] = a[:, :, 70].abs() + 0.5
+    a[1, 3, 70] = 0.0
+    sign = 1.0 - 2.0 * (torch.arange(44, device=b.device) % 2)
+    b[:, :44] = ((b[:, :44].abs() + 0.25) * sign[None, :, None]).to(BF16)
+    inf = float("inf")
+    rows = [1, 2, 13, 14, T // 2 + 2, T // 2 + 3, T - 2, T - 1]
+    for i, t in enumerate(rows):
+        if i % 4 < 3:
+            x[t, 13] = (inf, -inf, inf)[i % 4]
+        if i % 4 == 2:
+            x[t, 70] = -inf
+        if i % 4 == 3:
+            x[t, 70] = inf
+    low = 5
+    if x.dtype == F32:
+        x.view(torch.int32)[low, 20] = 0x7F800001
+    else:
+        x[low, 20] = float("nan")
+    got = _np(_call(form, base, x, a, b, scale))
+    with np.errstate(invalid="ignore"):
+        r = ol.lora(_np(base), _np(x), _np(a), _np(b), who, seq, _np(scale))
+    special = np.zeros(T, bool)
+    special[rows + [low]] = True
+    want = r["y"]
+    assert not np.isfinite(want[special]).any() and np.isinf(want[special]).any() and np.isnan(want[low]).all()
+    assert np.array_equal(got[special], want[special], equal_nan=True)
+    with np.errstate(invalid="ignore"):
+        ok = np.abs(got - want) <= _bound(r, 96, 16, base.dtype)
+    assert ok[~special].all()
