@@ -20,10 +20,10 @@
 // rate; what is left is each workgroup's chain of loads, LDS and products.  64 rows
 // with an adapter each, rank 16, 1,536 columns out: 6.5 us, one fp32 row 6.9, that
 // chain alone.
-// fp32 values enter as sums of bfloat16 parts: x as three (exact but for its
-// smallest values), h as two where the results are bfloat16 (off by 2^-16 of it,
-// where they round by 2^-8) and three where they are fp32.  A row has the same
-// bits whatever other rows there are.
+// fp32 values, x and h, enter as sums of three bfloat16 parts, exact but for the
+// smallest values.  (With two parts of h for bfloat16 y the prompts above took 26.0
+// instead of 27.2 us, but columns of B that cancel show what is lost.)  A row has the
+// same bits whatever other rows there are.
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -62,12 +62,12 @@ __device__ __forceinline__ nf4 mfma(nu4 a, nu4 b, nf4 c) {
                                                  c, 0, 0, 0);
 }
 
-// Eight consecutive values of x, as they lie in LDS, as bfloat16 parts.
-template <typename XT>
-struct XParts;
+// Eight consecutive values of x, as they lie in LDS, or of h as bfloat16 parts.
+template <typename T>
+struct Parts;
 
 template <>
-struct XParts<uint16_t> {
+struct Parts<uint16_t> {
   static constexpr int kParts = 1;
   static __device__ __forceinline__ void split(const nu4 (&v)[1], nu4 (&out)[1]) { out[0] = v[0]; }
 };
@@ -78,7 +78,7 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
 }
 
 template <>
-struct XParts<float> {
+struct Parts<float> {
   static constexpr int kParts = 3;
   // Each part takes the highest eight bits that are left: 24 in all.  An infinity is
   // whole in its first part and leaves nothing (a difference would be NaN); a NaN
@@ -383,7 +383,7 @@ template <typename XT, int MT, int NT, bool LISTED>
 __device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Rows<LISTED>& rows, int pass,
                                              char* lds) {
   using D = Down<XT, MT, NT>;
-  constexpr int MP = D::kRanks, XU = D::kUnits, XP = XParts<XT>::kParts, U = D::kAhead;
+  constexpr int MP = D::kRanks, XU = D::kUnits, XP = Parts<XT>::kParts, U = D::kAhead;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, quad = lane >> 4;
   const char* a = reinterpret_cast<const char*>(g.a + static_cast<int64_t>(m) * g.rank * g.d_in);
@@ -439,7 +439,7 @@ __device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Row
           for (int w = 0; w < XU; ++w)
             v[w] = XU == 1 ? get_chunk(lds + j * kUnitBytes, l16, 4 * s + quad)
                            : get_chunk(lds + (j * XU + s) * kUnitBytes, l16, 2 * quad + w);
-          XParts<XT>::split(v, xp[s][j]);
+          Parts<XT>::split(v, xp[s][j]);
         }
       }
 #pragma unroll
@@ -469,17 +469,13 @@ __device__ __forceinline__ void down_product(const LoraArgs& g, int m, const Row
       *reinterpret_cast<nf4*>(part + (16 * j + l16) * D::kPartRow + 16 * i + 4 * quad) = acc[i][j];
 }
 
-// The next bfloat16 part of h, which keeps the rest (an infinity has none).
-__device__ __forceinline__ float take_part(float& h) {
-  const float v = bf16_bits_to_float(pack_bf16(h, 0.0f) & 0xFFFFu);
-  h = __builtin_isfinite(v) ? h - v : 0.0f;
-  return v;
-}
+constexpr int kHParts = Parts<float>::kParts;
 
 // Eight ranks (64 pass + 32 step + 8 quad ..) of token t: the wavefronts' sums in
-// order, scaled, as bfloat16 parts; zeros past the adapter's rank.
-template <typename D, int HP, int STRIDE>   // STRIDE: from one wavefront's sums to the next one's
-__device__ __forceinline__ void join_sums(const char* lds, int t, int r, int ranks, float scale, nu4 (&out)[HP]) {
+// order, scaled; zeros past the adapter's rank.
+template <typename D, int STRIDE>   // STRIDE: from one wavefront's sums to the next one's
+__device__ __forceinline__ void join_sums(const char* lds, int t, int r, int ranks, float scale,
+                                          nu4 (&out)[2]) {
   float h[8];
   if (r < ranks) {
 #pragma unroll
@@ -497,17 +493,7 @@ __device__ __forceinline__ void join_sums(const char* lds, int t, int r, int ran
     for (int e = 0; e < 8; ++e) h[e] = 0.0f;
   }
 #pragma unroll
-  for (int p = 0; p < HP; ++p)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = take_part(h[2 * e]), hi = take_part(h[2 * e + 1]);
-      out[p][e] = pack_bf16(lo, hi);
-    }
-}
-
-template <typename YT>
-constexpr int h_parts() {
-  return sizeof(YT) == 4 ? 3 : 2;
+  for (int e = 0; e < 8; ++e) out[e / 4][e % 4] = __builtin_bit_cast(uint32_t, h[e]);
 }
 
 // Rows c .. c + COLS - 1 of B, which follow each other in memory, 16 bytes per
@@ -597,14 +583,14 @@ struct YRows {
 };
 
 // B h of 16 columns per row tile of B and 16 tokens, to LDS [token][COLS + 4].
-template <int RS, int HP, int COLS>
-__device__ __forceinline__ void up_product(const nu4 (&bv)[RS], const nu4 (&hv)[HP][RS], float* lds, int tile) {
+template <int RS, int COLS>
+__device__ __forceinline__ void up_product(const nu4 (&bv)[RS], const nu4 (&hv)[kHParts][RS], float* lds, int tile) {
   const int lane = threadIdx.x & 63;
   nf4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int s = 0; s < RS; ++s)
 #pragma unroll
-    for (int p = 0; p < HP; ++p) acc = mfma(bv[s], hv[p][s], acc);
+    for (int p = 0; p < kHParts; ++p) acc = mfma(bv[s], hv[p][s], acc);
   *reinterpret_cast<nf4*>(lds + (lane & 15) * (COLS + 4) + 16 * tile + 4 * (lane >> 4)) = acc;
 }
 
@@ -637,7 +623,6 @@ __device__ __forceinline__ bool tile_rows(const LoraArgs& g, int tile, TogetherS
 template <typename XT, typename YT, int MT>
 __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   using D = Down<XT, MT, 1>;
-  constexpr int HP = h_parts<YT>();
   constexpr int RS = (MT + 1) / 2;   // 32-rank steps of the second product
   constexpr int kCols = 32;          // columns that a wavefront takes at a time
   using B = BRows<RS, kCols, 64>;
@@ -645,7 +630,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
   constexpr int kWaveBytes = D::kBytes > kUp ? D::kBytes : kUp;
   static_assert(kWaveBytes % 16 == 0, "");
   __shared__ __align__(16) char s_wave[kWaves * kWaveBytes];
-  __shared__ nu4 s_h[HP][RS][64];
+  __shared__ nu4 s_h[kHParts][RS][64];
   __shared__ TogetherShared<16> s_rows;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   Rows<true> rows{0, 0, s_rows.list};
@@ -680,16 +665,17 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
     constexpr int kSteps = (D::kRanks + 1) / 2;
     if (tid < 64 * kSteps) {
       const int r = 32 * wave + 8 * (lane >> 4);
-      nu4 h[HP];
-      join_sums<D, HP, kWaveBytes>(s_wave, lane & 15, r, min(g.rank - 64 * pass, 16 * D::kRanks), scale, h);
+      nu4 v[2], h[kHParts];
+      join_sums<D, kWaveBytes>(s_wave, lane & 15, r, min(g.rank - 64 * pass, 16 * D::kRanks), scale, v);
+      Parts<float>::split(v, h);
 #pragma unroll
-      for (int p = 0; p < HP; ++p) s_h[p][2 * pass + wave][lane] = h[p];
+      for (int p = 0; p < kHParts; ++p) s_h[p][2 * pass + wave][lane] = h[p];
     }
     __syncthreads();
   }
-  nu4 hv[HP][RS];
+  nu4 hv[kHParts][RS];
 #pragma unroll
-  for (int p = 0; p < HP; ++p)
+  for (int p = 0; p < kHParts; ++p)
 #pragma unroll
     for (int s = 0; s < RS; ++s) hv[p][s] = s_h[p][s][lane];
   float* res = reinterpret_cast<float*>(mine + B::kBytes);
@@ -704,7 +690,7 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
       nu4 bv[RS];
 #pragma unroll
       for (int s = 0; s < RS; ++s) bv[s] = B::get(g, mine, 16 * tile + (lane & 15), s);
-      up_product<RS, HP, kCols>(bv, hv, res, tile);
+      up_product<RS, kCols>(bv, hv, res, tile);
     }
     wave_order();
     yr.add(res);
@@ -716,7 +702,8 @@ __global__ __launch_bounds__(kThreads) void lora_kernel(LoraArgs g) {
 // Many rows, two launches.  The workspace holds a table of the first one's tiles
 // (first row, number of rows, adapter or -1) and, where they are gathered, their rows,
 // which spares the second one the search, and h by 16 rows in the order of the second
-// product's operand: [tile][16 rows][part][step][lane][8].
+// product's operand, in fp32, which is less to read than its parts: [tile][16 rows]
+// [half][step][lane][4].
 constexpr int kTileRows = 32;
 constexpr int kTiles16 = kTileRows / 16;
 constexpr int kUpWaves = 2;    // tiles of a workgroup
@@ -733,10 +720,10 @@ __device__ __forceinline__ int tile_of(int block, int n) {
   return first + kTurn <= n ? first + i % 8 * kRun + i / 8 : block;
 }
 
-template <typename XT, typename YT, int MT, bool LISTED>
+template <typename XT, int MT, bool LISTED>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
   using D = Down<XT, MT, kTiles16>;
-  constexpr int HP = h_parts<YT>(), RS = (MT + 1) / 2;
+  constexpr int RS = (MT + 1) / 2;
   __shared__ __align__(16) char s_wave[kWaves * D::kBytes];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tile = tile_of(blockIdx.x, gridDim.x);
@@ -760,12 +747,12 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
     constexpr int kSteps = (D::kRanks + 1) / 2;
     if (wave < kSteps * kTiles16) {
       const int part16 = wave / kSteps, step = wave - part16 * kSteps;
-      nu4 h[HP];
-      join_sums<D, HP, D::kBytes>(s_wave, 16 * part16 + (lane & 15), 32 * step + 8 * (lane >> 4),
+      nu4 h[2];
+      join_sums<D, D::kBytes>(s_wave, 16 * part16 + (lane & 15), 32 * step + 8 * (lane >> 4),
                                   min(g.rank - 64 * pass, 16 * D::kRanks), scale, h);
-      nu4* out = g.h + (static_cast<int64_t>(tile) * kTiles16 + part16) * (HP * RS * 64) + lane;
+      nu4* out = g.h + (static_cast<int64_t>(tile) * kTiles16 + part16) * (2 * RS * 64) + lane;
 #pragma unroll
-      for (int p = 0; p < HP; ++p) out[(p * RS + 2 * pass + step) * 64] = h[p];
+      for (int p = 0; p < 2; ++p) out[(p * RS + 2 * pass + step) * 64] = h[p];
     }
   }
 }
@@ -776,7 +763,6 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
 // tiles' requests have different ones.
 template <typename YT, int RS, bool LISTED>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
-  constexpr int HP = h_parts<YT>();
   using B = BRows<RS, kGroup, 64 * kUpWaves>;
   __shared__ __align__(16) char s_b[B::kBytes];
   __shared__ __align__(16) float s_res[kUpWaves][16 * (kGroup + 4)];
@@ -806,14 +792,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
   const auto rows_of_b = [&](int adapter) { return g.b + static_cast<int64_t>(adapter) * g.d_out * g.rank; };
   B bl;
   bl.load(g, rows_of_b(who), c, tid);
-  nu4 hv[kTiles16][HP][RS];
-  const nu4* h = g.h + static_cast<int64_t>(min(tile, g.n_tiles - 1)) * kTiles16 * (HP * RS * 64) + lane;
+  nu4 hv[kTiles16][RS][2];
+  const nu4* h = g.h + static_cast<int64_t>(min(tile, g.n_tiles - 1)) * kTiles16 * (2 * RS * 64) + lane;
 #pragma unroll
   for (int j = 0; j < kTiles16; ++j)
 #pragma unroll
-    for (int p = 0; p < HP; ++p)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int s = 0; s < RS; ++s) hv[j][p][s] = h[((j * HP + p) * RS + s) * 64];
+      for (int s = 0; s < RS; ++s) hv[j][s][p] = h[((j * 2 + p) * RS + s) * 64];
   YRows<YT, kGroup, 16 / sizeof(YT)> yr[kTiles16];
 #pragma unroll
   for (int j = 0; j < kTiles16; ++j) yr[j].template load<LISTED>(g, rows.from(16 * j), c);
@@ -833,12 +819,20 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
     if (m != who) continue;
 #pragma unroll
     for (int j = 0; j < kTiles16; ++j) {
+      nu4 hp[kHParts][RS];
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        nu4 v[kHParts];
+        Parts<float>::split(hv[j][s], v);
+#pragma unroll
+        for (int p = 0; p < kHParts; ++p) hp[p][s] = v[p];
+      }
 #pragma unroll
       for (int t = 0; t < kGroup / 16; ++t) {
         nu4 bv[RS];
 #pragma unroll
         for (int s = 0; s < RS; ++s) bv[s] = B::get(g, s_b, 16 * t + (lane & 15), s);
-        up_product<RS, HP, kGroup>(bv, hv[j], s_res[wave], t);
+        up_product<RS, kGroup>(bv, hp, s_res[wave], t);
       }
       wave_order();
       yr[j].add(s_res[wave]);
@@ -863,10 +857,10 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
     const int rows = (g.n_tiles + kUpWaves - 1) / kUpWaves;
     const dim3 grid(groups, min(rows, kUpGridRows), (rows + kUpGridRows - 1) / kUpGridRows);
     if (g.together) {
-      lora_down_kernel<XT, YT, MT, true><<<g.n_tiles, kThreads, 0, s>>>(g);
+      lora_down_kernel<XT, MT, true><<<g.n_tiles, kThreads, 0, s>>>(g);
       lora_up_kernel<YT, (MT + 1) / 2, true><<<grid, 64 * kUpWaves, 0, s>>>(g);
     } else {
-      lora_down_kernel<XT, YT, MT, false><<<g.n_tiles, kThreads, 0, s>>>(g);
+      lora_down_kernel<XT, MT, false><<<g.n_tiles, kThreads, 0, s>>>(g);
       lora_up_kernel<YT, (MT + 1) / 2, false><<<grid, 64 * kUpWaves, 0, s>>>(g);
     }
     return hipGetLastError();
@@ -923,7 +917,7 @@ size_t lora_workspace_bytes(int64_t T, int rank, int n_seq) {
   if (T < kManyRows || (n_seq == 0 && T > 65536)) return 0;
   const int64_t tiles = most_tiles(T, n_seq ? n_seq : MOE_MAX_EXPERTS + 1, kTileRows);
   const int64_t steps = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
-  return static_cast<size_t>(align256(tiles * 16) + tiles * kTileRows * 4 + tiles * kTiles16 * 3 * steps * 1024);
+  return static_cast<size_t>(align256(tiles * 16) + tiles * kTileRows * 4 + tiles * kTiles16 * 2 * steps * 1024);
 }
 
 hipError_t launch_lora(const void* base, const void* x, int x_dtype, int64_t T, int d_in, int d_out,

@@ -722,11 +722,10 @@ int moe_combine_backward(const void* dy, int dy_dtype, const void* rows, int row
  *   (y_dtype), y may be base; a bf16 [n_adapters][rank][d_in], b bf16
  *   [n_adapters][d_out][rank]; adapter int32 [n_seq]; scale fp32 [n_adapters]
  *   (NULL: ones).
- * base is for instance moe_mxfp4_linear's y.  Sums in fp32 in a fixed order, the
- * result rounded once; A x enters the second product as a sum of two (bf16 y) or
- * three (fp32 y) bfloat16 values, which loses 2^-16 or 2^-24 of it.  Infinities and
- * NaN of x have the formula's results.  A row has the same bits whatever the other
- * rows and requests are.  A smaller rank is a larger one padded with zeros.
+ * base is for instance moe_mxfp4_linear's y.  Sums in fp32 in a fixed order, A x
+ * (scaled) held in fp32, the result rounded once.  Infinities and NaN of x have the
+ * formula's results.  A row has the same bits whatever the other rows and requests
+ * are.  A smaller rank is a larger one padded with zeros.
  * Limits: 0 <= T < 2^24, 1 <= n_seq <= 65536 (n_seq = T = 0 without seq_offsets),
  * 1 <= n_adapters <= MOE_MAX_EXPERTS, rank a multiple of 8 in 8..MOE_MAX_RANK,
  * d_in a multiple of 32 and d_out of 16, both up to MOE_MAX_MX_COLS.

@@ -1,5 +1,6 @@
 """GPU tests of values that a product of parts can get wrong: infinities and NaN of
-x.  Every form of the call: few rows, many rows, and both of gathered rows.
+x, values of h that cancel.  Every form of the call: few rows, many rows, and both of
+gathered rows.
 """
 import numpy as np
 import pytest
@@ -67,3 +68,57 @@ def test_infinities_are_the_formulas(form, types):
     with np.errstate(invalid="ignore"):
         ok = np.abs(got - want) <= _bound(r, 96, 16, base.dtype)
     assert ok[~special].all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("form", FORMS)
+def test_values_of_h_that_cancel(form, types):
+    """Two ranks whose h differ by one value of x and whose columns of B are opposite:
+    y is that value times B's.  All values are whole numbers: h between 2^18 and
+    2^20, sums of both products below 2^24, and y of at most 254, so that fp32 sums
+    and one rounding to the output's type are exact, and any bit of h that is lost is
+    seen."""
+    T, _, _, of = _form(form)
+    xt, yt = types
+    dev = need_gpu()
+    g = torch.Generator().manual_seed(T)
+    x = torch.randint(64, 128, (T, 64), generator=g) * (1 - 2 * torch.randint(0, 2, (T, 1), generator=g))
+    x = x.to(xt).to(dev)
+    a = torch.zeros((2, 16, 64))
+    a[:, 2] = torch.randint(64, 127, (2, 64), generator=g).float()
+    a[:, 9] = a[:, 2]
+    a[0, 9, 40] += 1
+    a[1, 9, 7] += 1
+    b = torch.zeros((2, 48, 16))
+    c = (torch.arange(48) % 2 + 1).float()
+    b[:, :, 2], b[:, :, 9] = -c, c
+    a, b = a.to(BF16).to(dev), b.to(BF16).to(dev)
+    y = _call(form, torch.zeros((T, 48), dtype=yt, device=dev), x, a, b)
+    at = torch.from_numpy(np.where(of == 0, 40, 7)).to(dev)
+    want = x.float().gather(1, at[:, None]) * c.to(dev)
+    assert torch.equal(y.float(), want)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("form", FORMS)
+def test_h_past_the_largest_bfloat16(form, types):
+    """A finite h that lies between the largest bfloat16 and the largest fp32 value is
+    no infinity: h = x0 + x1, a sum that fp32 holds exactly, times a power of two,
+    rounded once."""
+    T, _, _, of = _form(form)
+    xt, yt = types
+    dev = need_gpu()
+    top = 2.0 ** 127 * (2 - 2.0 ** -7)             # the largest bfloat16
+    x = torch.zeros((T, 64))
+    x[:, 5], x[:, 60] = top, 2.0 ** 119 + 2.0 ** 113 * (torch.arange(T) % 2)
+    x = (x * (1 - 2 * (torch.arange(T) % 3 == 1).float())[:, None]).to(xt)
+    a, b = torch.zeros((2, 16, 64)), torch.zeros((2, 48, 16))
+    a[:, 11, 5] = a[:, 11, 60] = 1.0
+    p = 2.0 ** -(torch.arange(48) % 7 + 3.0)
+    b[0, :, 11], b[1, :, 11] = p, -p
+    h = x[:, 5].double() + x[:, 60].double()
+    assert (h.abs() > top + 2.0 ** 118).all() and torch.equal(h.float().double(), h)
+    sign = torch.from_numpy(np.where(of == 0, 1.0, -1.0))
+    want = (sign[:, None] * h[:, None] * p.double()).to(yt)
+    y = _call(form, torch.zeros((T, 48), dtype=yt, device=dev), x.to(dev), a.to(BF16).to(dev), b.to(BF16).to(dev))
+    assert torch.equal(y.cpu(), want)
