@@ -1199,7 +1199,8 @@ def dispatch(x, idx, n_experts, rows=None, offsets=None, pair_pos=None, ws=None,
     """A row for every pair of idx int32 [T, k], groups ascending by expert: the
     token's row of x [T, d] (fp32 or bf16) (moe_dispatch).  Pairs whose id lies
     outside [0, n_experts) have none (pair_pos -1), and the rows past offsets[E]
-    are left as they were (undefined in rows allocated here)."""
+    are left as they were (undefined in rows allocated here: whoever reads them all,
+    not the groups alone, gives rows of zeros)."""
     dtype = _float_dtype(x.dtype, "x")
     T, d = _dims(x, 2, "x")
     k = _dims(idx, 2, "idx")[1]
@@ -1259,7 +1260,7 @@ def dispatch_backward(drows, pair_pos, dx=None, dtype=None, stream=None):
 def _combine_backward(dev, stream, dy, dy_dtype, rows, rows_dtype, R, T, d, k, pair_pos, w, drows, dw, need_rows,
                       need_w):
     if drows is None and need_rows:
-        drows = torch.empty_like(rows)
+        drows = torch.zeros_like(rows)   # rows of no pair have no gradient
     if dw is None and need_w:
         dw = torch.empty((T, k), dtype=torch.float32, device=dev)
     _check(lib().moe_combine_backward(dy.data_ptr(), dy_dtype, _addr(rows), rows_dtype, R, T, d, k,
@@ -1275,8 +1276,9 @@ def combine_backward(dy, rows, pair_pos, w=None, drows=None, dw=None, need_rows=
     ones) [T, k] as the forward call took them.  Returns (drows [R, d] in rows'
     type, dw fp32 [T, k]): the rows' gradients in the groups' order, and what
     route_backward takes; None for one that is not needed.  Rows that are no
-    pair's are left as they were (undefined in drows allocated here).  Where only
-    drows is needed, it may be given in place of rows with rows None."""
+    pair's are zeros in drows allocated here and left as they were in one that is
+    given, which spares the clearing.  Where only drows is needed, it may be given in
+    place of rows with rows None."""
     like = rows if rows is not None else drows
     if like is None:
         raise ValueError("combine_backward: rows, or drows without need_w, expected")

@@ -1,0 +1,54 @@
+"""GPU tests of the gradients that combine_backward allocates itself: rows that no
+pair uses have the gradient zero there, whatever the memory held.
+"""
+import numpy as np
+import pytest
+import torch
+
+from parity import need_gpu
+from test_gpu_dispatch import BF16, F32, _bf, _dev, _pos, _randn
+
+pytestmark = pytest.mark.gpu
+
+
+def _soil(n_bytes):
+    """NaN in the memory that the next allocation of this size is likely to get."""
+    for _ in range(4):
+        torch.full((n_bytes // 4,), float("nan"), device=need_gpu())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,k,d,R,missing", [(1, 1, 4, 3, 0.0), (40, 6, 264, 240, 0.3), (700, 10, 72, 7000, 1.0),
+                                             (5, 2, 16384, 64, 0.1), (0, 3, 64, 9, 0.0)])
+@pytest.mark.parametrize("need_w", [True, False])
+def test_rows_of_no_pair(T, k, d, R, missing, dtype, need_w):
+    bf = _bf()
+    pos = _pos(np.random.default_rng(T + d), T, k, R, missing)
+    dy, rows, w = _randn(1, (T, d), dtype), _randn(2, (R, d), dtype), _randn(3, (T, k), F32)
+    given = torch.zeros_like(rows)
+    bf.combine_backward(dy, rows, _dev(pos), w, drows=given, need_w=False)
+    _soil(rows.numel() * rows.element_size())
+    drows, dw = bf.combine_backward(dy, rows, _dev(pos), w, need_w=need_w)
+    assert torch.equal(drows, given) and (dw is None) != need_w
+    none = np.setdiff1d(np.arange(R), pos.ravel())
+    assert len(none) and not drows[torch.from_numpy(none).to(drows.device)].any()
+
+
+def test_in_a_graph():
+    """Cleared on every replay: another step's pairs leave nothing behind."""
+    bf = _bf()
+    rng = np.random.default_rng(3)
+    pos = [_dev(_pos(rng, 30, 4, 120, 0.4)) for _ in range(3)]
+    dy, rows, w = _randn(1, (30, 132), BF16), _randn(2, (120, 132), BF16), _randn(3, (30, 4), F32)
+    want = [bf.combine_backward(dy, rows, p, w) for p in pos]
+    live = pos[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        drows, dw = bf.combine_backward(dy, rows, live, w)
+    for i in (1, 2, 0, 2, 1):
+        live.copy_(pos[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(drows, want[i][0]) and torch.equal(dw, want[i][1])
+        assert torch.equal(bf.combine_backward(dy, rows, pos[i], w)[0], want[i][0])
