@@ -234,7 +234,11 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(
     for (int j = 0; j < N; ++j) acc[j] = b.get(j);
   }
   // the terms in batches: all places of a batch, then all its rows (one that is
-  // missing re-reads one that is there, so that no load waits for a comparison)
+  // missing re-reads one that is there, so that no load waits for a comparison).  More
+  // terms at a time are more registers, which cost where there are few terms; few at a
+  // time are waits (2048 bfloat16 columns, batches of 4, 8, 10 and 16 terms: 8,192
+  // tokens x 2 23, 23, 24 and 31 us, x 10 65, 65, 64 and 64, x 24 142, 142, 141 and 139;
+  // 64 tokens x 2 2.9, 3.1, 3.2 and 3.7, x 10 5.4, 5.2, 4.2 and 4.8)
   constexpr int KC = 10;
   const int64_t q0 = static_cast<int64_t>(t) * k;
   for (int i0 = 0; i0 < k; i0 += KC) {
@@ -368,13 +372,18 @@ hipError_t combine_backward_as(const void* dy, const void* rows, int64_t R, int 
                                   static_cast<int>(R), d, k, pair_pos, w, static_cast<RT*>(drows),
                                   dw);
   };
+  // A lane keeps up to 32 values of dy, eight parts of four or four of eight: twice as
+  // many spill, with 128 registers for each of 1,024 threads (4,096 tokens x 8, 4096
+  // bfloat16 columns: 170 us with 64 values, 124 with none; kept against not, 2048
+  // columns: bfloat16 61 against 69 us, fp32 114 against 123).
   constexpr int W = part_of<GT, RT>();
+  constexpr bool kEight = W == 4;
   if (d <= 64 * W)
     go(combine_backward_kernel<GT, RT, W, 1>);
   else if (d <= 256 * W)
     go(combine_backward_kernel<GT, RT, W, 4>);
-  else if (d <= 2048)
-    go(combine_backward_kernel<GT, RT, W, 2048 / (64 * W)>);
+  else if (kEight && d <= 512 * W)
+    go(combine_backward_kernel<GT, RT, W, kEight ? 8 : 4>);
   else
     go(combine_backward_kernel<GT, RT, W, 0>);
   return hipGetLastError();

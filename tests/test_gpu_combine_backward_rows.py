@@ -1,12 +1,14 @@
-"""GPU tests of the gradients that combine_backward allocates itself: rows that no
-pair uses have the gradient zero there, whatever the memory held.
+"""GPU tests of combine_backward: the gradients that it allocates itself, where rows
+that no pair uses have the gradient zero, whatever the memory held; and row lengths on
+both sides of what a lane keeps of dy.
 """
 import numpy as np
 import pytest
 import torch
 
+import oracle.dispatch as od
 from parity import need_gpu
-from test_gpu_dispatch import BF16, F32, _bf, _dev, _pos, _randn
+from test_gpu_dispatch import BF16, F32, HALF_STEP, U, _bf, _dev, _np, _pos, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +54,19 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(drows, want[i][0]) and torch.equal(dw, want[i][1])
         assert torch.equal(bf.combine_backward(dy, rows, pos[i], w)[0], want[i][0])
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("d", [252, 256, 260, 508, 512, 516, 1020, 1024, 1028, 2044, 2048, 2052, 2056, 4100])
+def test_row_lengths(d, types):
+    """Bars as in test_gpu_dispatch: one rounding of w dy to fp32 and one to the rows'
+    type; d + 2 roundings of the terms of dw."""
+    bf = _bf()
+    gt, rt = types
+    pos = _pos(np.random.default_rng(d), 9, 5, 60, 0.2)
+    dy, rows, w = _randn(1, (9, d), gt), _randn(2, (60, d), rt), _randn(3, (9, 5), F32)
+    drows, dw = bf.combine_backward(dy, rows, _dev(pos), w)
+    ref, ref_w, mag = od.combine_backward(_np(dy), _np(rows), pos, _np(w))
+    ref = np.nan_to_num(ref)
+    assert (np.abs(_np(drows) - ref) <= (U + HALF_STEP[rt] * (1 + U)) * np.abs(ref)).all()
+    assert (np.abs(_np(dw) - ref_w) <= (d + 2) * U * mag).all()
