@@ -14,15 +14,15 @@
 // Operands are read as their rows lie and change lanes in LDS: read directly, an
 // operand's layout has 16 bytes of each of 16 rows in a quarter of a wavefront,
 // sixteen cache lines where four would do (8,192 rows at rank 64, two launches: 50 us
-// where this takes 26).  y leaves the same way.
+// where this took 28).  y leaves the same way.
 // Measured (2,048 columns in and out, bfloat16): 8,192 rows of eight requests, rank
-// 64, 101 MB of x, base and y: 13.1 + 14.9 us, 26 in a row of calls, 20 at a copy's
-// rate; what is left is each workgroup's chain of loads, LDS and products.  64 rows
-// with an adapter each, rank 16, 1,536 columns out: 6.5 us, one fp32 row 6.9, that
-// chain alone.
+// 64, 101 MB of x, base and y: 12.3 + 16.7 us each launch alone, 27 in a graph of calls
+// (as the variants below are compared), 20 at a copy's rate; what is left is each
+// workgroup's chain of loads, LDS and products.  64 rows with an adapter each, rank 16,
+// 1,536 columns out: 6.5 us, one fp32 row 7.1, that chain alone.
 // fp32 values, x and h, enter as sums of three bfloat16 parts, exact but for the
-// smallest values.  (With two parts of h for bfloat16 y the prompts above took 26.0
-// instead of 27.2 us, but columns of B that cancel show what is lost.)  A row has the
+// smallest values.  (With two parts of h for bfloat16 y the prompts above took 26
+// instead of 27 us, but columns of B that cancel show what is lost.)  A row has the
 // same bits whatever other rows there are.
 #include <algorithm>
 
@@ -199,8 +199,8 @@ struct TogetherShared {
 
 // Requests of a wavefront whose adapters and bounds are asked for at a time; if it
 // has no more, they are kept (8,192 rows that are requests, rank 64, 48 adapters, two
-// launches: one at a time 53.8 us, four 49.9, eight 49.5, sixteen, then kept, 48.0;
-// eight in one launch of few rows cost 1 us).
+// launches: one at a time 48.3 us, four 44.9, eight 44.7, sixteen, then kept, 43.6; 512
+// of them in one launch, with two 16.3 and with eight 17.6).
 template <int BATCH>
 struct Requests {
   int id[BATCH], bound[BATCH];
@@ -364,7 +364,7 @@ __device__ __forceinline__ nu4 get_chunk(const char* lds, int row, int chunk) {
 
 // Shared memory of one wavefront, in its three uses: x, then A, then the sums (A beside
 // x would leave fp32 one workgroup per CU: 8,192 rows that are requests, rank 16, 48
-// adapters, 305 workgroups, 76 us instead of 61).
+// adapters, 305 workgroups, 76 us instead of 58).
 template <typename XT, int MT, int NT>
 struct Down {
   static constexpr int kUnits = sizeof(XT) / 2;   // of x, for 64 columns
@@ -534,8 +534,8 @@ struct BRows {
 // A wavefront's 16 rows of COLS columns of base and y as they lie: a lane holds kN
 // columns of each of kLoads rows.  Eight fp32 columns are two stores that leave gaps,
 // and 7% of what they write goes out twice: 8,192 rows of eight prompts, rank 64, with
-// eight and four 53.7 and 50.8 us.  Few rows are better off with eight (one row 6.5
-// against 6.7 us, 512 rows, rank 64, 13.9 against 14.3).
+// eight and four 53.2 and 50.8 us.  Few rows are better off with eight (one row 6.69
+// against 6.75 us, 512 rows, rank 64, 14.0 against 14.2).
 template <typename YT, int COLS, int kN>
 struct YRows {
   static constexpr int kPerRow = COLS / kN, kRows = 64 / kPerRow, kLoads = 16 / kRows;
@@ -711,9 +711,9 @@ constexpr int kUpGridRows = 32768;
 
 // Workgroups go to the eight XCDs in turn: four tiles that follow each other, which
 // mostly share an adapter, go to one, whose L2 cache then reads it once (8,192 rows,
-// rank 64, two launches, with 1, 4, 8 and all n / 8 tiles: eight prompts 26.8, 26.1,
-// 26.8 and 29.0 us; single rows, 48 adapters, 47.6, 43.0, 42.2 and 47.3, 4 adapters
-// 32.2, 32.8, 33.7 and 37.2).
+// rank 64, two launches, with 1, 4, 8 and all n / 8 tiles: eight prompts 28.2, 27.4,
+// 28.3 and 29.7 us; single rows, 48 adapters, 48.2, 44.2, 43.1 and 47.7, 4 adapters
+// 33.8, 33.9, 34.3 and 34.2).
 __device__ __forceinline__ int tile_of(int block, int n) {
   constexpr int kRun = 4, kTurn = 8 * kRun;
   const int i = block % kTurn, first = block - i;
@@ -758,8 +758,8 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraArgs g) {
 }
 
 // A workgroup takes 64 columns of two tiles, one per wavefront (8,192 rows, rank 64,
-// with one, two, three, four and eight tiles: 29.4, 28.2, 27.7, 28.6 and 38.9 us for
-// both launches).  B goes through LDS for all of them, adapter by adapter where the
+// with one, two, three, four and eight tiles: 28.0, 27.6, 27.1, 27.3 and 34.3 us for
+// both launches; single rows of 48 adapters 44.7, 44.0, 43.5, 44.3 and 50.2).  B goes through LDS for all of them, adapter by adapter where the
 // tiles' requests have different ones.
 template <typename YT, int RS, bool LISTED>
 __global__ __launch_bounds__(64 * kUpWaves) void lora_up_kernel(LoraArgs g) {
@@ -866,7 +866,7 @@ hipError_t launch_rank(LoraArgs g, hipStream_t s) {
     return hipGetLastError();
   }
   // about a workgroup per CU: slices of the columns while there are few tiles (one
-  // row, 1,536 columns in 3 slices 7.4 us, in 24 6.4; 64 rows in 3 5.9, in 24 6.7)
+  // row, 1,536 columns in 3 slices 7.6 us, in 24 6.7; 64 rows in 3 6.2, in 24 14.8)
   const int64_t tiles = g.together ? most_tiles(g.T, g.n_adapters + 1, 16)
                                    : g.seq ? most_tiles(g.T, g.n_seq, 16) : g.T;
   const int slices = static_cast<int>(std::max(int64_t{1}, std::min(int64_t{groups}, 256 / tiles)));
@@ -884,24 +884,26 @@ hipError_t launch_as(const LoraArgs& g, hipStream_t s) {
   return launch_rank<XT, YT, 8>(g, s);
 }
 
-// Rows from which two launches are made (eight requests, 2,048 columns, bfloat16,
-// one launch against two: 1,024 rows at rank 16 10.4 and 10.5 us, at rank 64 15.7
-// against 15.0; 2,048 rows 12.5 against 12.1 and 19.5 against 16.3).
+// Rows from which two launches are made (eight requests, bfloat16, one launch against
+// two: 2,048 columns, 2,048 rows at rank 16 14.1 against 12.0 us, at rank 64 19.4
+// against 16.7; 1,024 rows 9.5 against 10.6 and 13.1 against 15.3, but with 4,096
+// columns 14.7 against 13.7 and 21.7 against 20.4: the border lies between, the lower
+// the longer the rows).
 constexpr int64_t kManyRows = 1024;
 
 // The same for gathered rows (one launch against two, bfloat16, rank 64, 48 adapters:
-// a row for every request, 1,024 rows 19.2 against 18.7 us, with 4 adapters 14.4
-// against 17.0; 2,048 rows 24.7 against 21.3; 8,192 rows 67 against 43; 1,000 requests
-// of two rows 25.7 against 21.3; 512 single rows beside a prompt of 8,192 61 against 38).
+// a row for every request, 1,024 rows 19.1 against 19.3 us, with 4 adapters 14.4
+// against 17.4; 2,048 rows 24.7 against 22.5; 8,192 rows 63 against 44; 1,000 requests
+// of two rows 25.5 against 22.3; 512 single rows beside a prompt of 8,192 44 against 40).
 constexpr int64_t kManyGathered = 1536;
 
 // Requests beyond the number of adapters from which rows of one adapter share a
 // workgroup: that many tiles at least are spared, for some 2 us of gathering (a row
 // for every request, apart against together, bfloat16, rank 64, 4 and 48 adapters:
-// 64 rows 10.4 against 10.1 and 11.1 against 15.7 us, 128 rows 13.5 against 9.5 and
-// 15.3 against 15.8, 512 rows 23.7 against 13.0 and 33.4 against 17.2, 8,192 rows
-// 280 against 33 and 448 against 43; where rows fill their tiles
-// anyhow, 8,000 rows of 256 requests, the two are even).
+// 64 rows 10.5 against 10.3 and 11.3 against 15.4 us, 128 rows 13.0 against 9.4 and
+// 14.4 against 15.4, 512 rows 23.1 against 13.0 and 31.0 against 16.2, 8,192 rows
+// 274 against 34 and 438 against 44; where rows fill their tiles anyhow, 8,000 rows
+// of 256 requests, 45 against 39, in fp32 59 against 60).
 constexpr int kTogether = 64;
 
 // Their offsets into x have 32 bits.

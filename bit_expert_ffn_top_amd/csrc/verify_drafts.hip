@@ -10,6 +10,12 @@
 // again, and the value.  Each wavefront of the first launch judges the drafts for
 // itself (two dependent reads) rather than wait for a launch that does.  Should
 // nothing be left of p, p itself is drawn from: its sums are formed beside r's.
+// Measured (fp32, three drafts, 64 requests unless said): 131,072 values 11.3 + 4.2 us;
+// most drafts are accepted there, and a request that keeps all of its drafts reads no
+// row of q, so that is 42 MB, 8 us at a copy's rate: what is left is that chain of reads
+// before the rows' own.  On both sides of the border, in a graph of calls: 16,384
+// values in one launch 8.3 us, 16,385 in two 8.6; one request 5.8 and 7.2; bfloat16 8.3
+// and 8.5, 6.3 and 6.8.  A call pays 4 us more for the second launch and its workspace.
 #include "moe_internal.h"
 #include "row_device.h"
 #include "scan_device.h"
