@@ -70,3 +70,17 @@ def test_row_lengths(d, types):
     ref = np.nan_to_num(ref)
     assert (np.abs(_np(drows) - ref) <= (U + HALF_STEP[rt] * (1 + U)) * np.abs(ref)).all()
     assert (np.abs(_np(dw) - ref_w) <= (d + 2) * U * mag).all()
+
+
+def test_on_a_given_stream():
+    """The clearing runs on the stream that the call is given."""
+    bf = _bf()
+    pos = _dev(_pos(np.random.default_rng(5), 900, 8, 9000, 0.5))
+    dy, rows, w = _randn(1, (900, 1024), BF16), _randn(2, (9000, 1024), BF16), _randn(3, (900, 8), F32)
+    want = bf.combine_backward(dy, rows, pos, w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = bf.combine_backward(dy, rows, pos, w, stream=side)
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -122,3 +122,19 @@ def test_h_past_the_largest_bfloat16(form, types):
     want = (sign[:, None] * h[:, None] * p.double()).to(yt)
     y = _call(form, torch.zeros((T, 48), dtype=yt, device=dev), x.to(dev), a.to(BF16).to(dev), b.to(BF16).to(dev))
     assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("yt", [F32, BF16])
+@pytest.mark.parametrize("rank", [8, 32, 40, 64, 72, 128])
+@pytest.mark.parametrize("form", ["many", "many gathered"])
+def test_a_workspace_of_the_size_that_is_asked_for(form, rank, yt):
+    """Nothing is written past it, and it may hold anything."""
+    bf = _bf()
+    T, seq, who, _ = _form(form)
+    base, x, a, b, scale = _inputs(T, 2, rank, 96, 48, BF16, yt)
+    want = _call(form, base, x, a, b, scale)
+    need = bf.lora_workspace_bytes(T, rank, 0 if seq is None else len(who))
+    assert need > 0
+    ws = torch.full((need + 65536,), 0xFF, dtype=torch.uint8, device=x.device)
+    y = bf.lora(base, x, a, b, _i32(who), seq_offsets=None if seq is None else _i32(seq), scale=scale, ws=ws[:need])
+    assert torch.equal(y, want) and (ws[need:] == 0xFF).all()
